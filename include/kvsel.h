@@ -447,6 +447,126 @@ int kvsel_stage_restore(kvsel_ctx* ctx, const void* host_k, const void* host_v, 
                         int page, double rope_base, int rope_style, void* k_pool, void* v_pool, int P,
                         int chunk_blocks, int gather_threads, int mode, void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* one serving step around the retention path                                */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * Block tables, slots and slot maps from lengths (the page tables that the
+ * retention calls' slot maps come from).  Session s has cached[s] tokens in
+ * its pages and gets new_len[s] more.  It holds ceil(cached / page) pages,
+ * listed in its table row, and its further pages are taken from free_pages in
+ * order, the sessions one after the other:
+ *   block_table[s][j] for the new pages j (other entries are not touched)
+ *   cu_new[s+1]       = new_len[0] + ... + new_len[s], cu_new[0] = 0
+ *   new_slots[i], new_pos[i]  slot (page id * page + offset) and position of
+ *                     the i-th new token, sessions packed one after the other;
+ *                     -1 behind the last token
+ *   slot_map[s][p]    slot of the session's position p, -1 behind its last token
+ *   counts            { new tokens, pages taken }
+ * Nothing is synchronised.  A length below 0, or a session whose tokens its
+ * table row, slot_map's row or new_slots cannot hold, is cut to what fits and
+ * sets the device error word; so do too few free pages and page ids outside
+ * [0, P): their slots (and new table entries) are -1.
+ *   cached, new_len int32 [S]; free_pages int32 [n_free] (distinct, held by no
+ *   session); block_table int32 [S][max_blocks] in/out; cu_new int32 [S+1];
+ *   new_slots, new_pos int32 [T]; slot_map int32 [S][ld] or NULL with ld = 0;
+ *   counts int32 [2]
+ * Requires S <= 16384, P*page and max_blocks*page < 2^31 - 4096.  No workspace.
+ */
+int kvsel_plan_slots(kvsel_ctx* ctx, const int32_t* cached, const int32_t* new_len, int S, int page, int P,
+                     const int32_t* free_pages, int n_free, int32_t* block_table, int max_blocks,
+                     int32_t* cu_new, int32_t* new_slots, int32_t* new_pos, int T, int32_t* slot_map, int ld,
+                     int32_t* counts, void* stream);
+
+/*
+ * The 4-bit KV cache.  A row (one token's K or V of one kv head, D values) is
+ * cut into groups of 16.  A group is 16 E2M1 codes (bit 3 the sign, bits 2..0
+ * the magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6) and one scale byte, which holds
+ * bits 14..7 of the scale's fp16 pattern (5 exponent bits, 3 mantissa bits):
+ *   s    = the smallest such scale with max|x| <= 6 s
+ *   code = the magnitude nearest to |x| / s, ties to the even code, x's sign
+ *   value = code * s, exact in bf16 and in fp16
+ * so that a value is off by at most s, itself below 0.19 max|x| but for groups
+ * whose max|x| is below 2^-11.  A group that holds a NaN or a magnitude above 61440 is stored as
+ * NaN: scale byte 255, codes 0.  Byte i of a group's 8 holds the codes of its
+ * values 2i (low four bits) and 2i + 1.
+ *   codes   u8 [P][Hkv][page][D/2]    scales  u8 [P][Hkv][page][D/16]
+ * for one layer, K and V each; slot n is row n % page of page n / page, as in
+ * kvsel_plan_slots.  A row takes 0.5625 D bytes.
+ */
+
+/*
+ * Store rows in the cache: token i's K and V rows go to slot slots[i].  A
+ * negative slot skips the token; one at or above P*page is skipped too and
+ * sets the device error word.  Tokens of one call should name distinct slots.
+ *   k, v   src_dtype F32 or BF16; token i's Hkv rows lie back to back at
+ *          element i*k_stride (i*v_stride)
+ * Requires D in {64,128,256}, P*page < 2^31, rows, strides and caches 16-byte
+ * aligned.  No workspace.
+ */
+int kvsel_kv4_store(kvsel_ctx* ctx, const void* k, const void* v, int src_dtype, int64_t k_stride,
+                    int64_t v_stride, int T, int Hkv, int D, const int32_t* slots, uint8_t* k_codes,
+                    uint8_t* k_scales, uint8_t* v_codes, uint8_t* v_scales, int P, int page, void* stream);
+
+/*
+ * Read rows back: the stored values of slot slots[i], exact, to token i's bf16
+ * K and V rows (laid out as in kvsel_kv4_store; k and v may not overlap the
+ * caches).  A slot outside [0, P*page) gives rows of zeros; one at or above
+ * P*page sets the device error word.  Rules as kvsel_kv4_store.
+ */
+int kvsel_kv4_load(kvsel_ctx* ctx, const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v_codes,
+                   const uint8_t* v_scales, int P, int page, const int32_t* slots, int T, int Hkv, int D,
+                   void* k, void* v, int64_t k_stride, int64_t v_stride, void* stream);
+
+/*
+ * Attention over the 4-bit cache, Tq query rows per session (Tq = 1: a decode
+ * step; more: drafted tokens or a short continuation).  The query rows are the
+ * last of the session's seq_lens[s] tokens: row t sits at position
+ * seq_lens[s] - Tq + t and sees the tokens j up to its own whose slot is live:
+ *   out[s,t,h] = softmax_j( scale * q[s,t,h] . K[j,g(h)] ) V[j,g(h)]
+ *   lse[s,t,h] = ln sum_j exp( scale * q[s,t,h] . K[j,g(h)] )
+ * with g(h) = h / (Hq/Hkv).  A row that sees nothing gives zeros and -inf.
+ * Token j's slot is slot_map[s][j] or, with block_table,
+ * block_table[s][j / page] * page + j % page (exactly one of the two is
+ * given).  Negative slots and pages and the slot `dead_slot` (what
+ * kvsel_redirect_slots writes; -1 for none) are not live: their rows are never
+ * read.  Other slots or pages outside the cache are taken as not live and set
+ * the device error word, as does a seq_lens[s] below 0 or beyond the map's or
+ * table's reach (it is cut to that).
+ *   q    bf16, token (s,t) at element (s*Tq + t)*q_stride, its Hq rows back to back
+ *   out  bf16 [S][Tq][Hq][D]; lse fp32 [S][Tq][Hq] or NULL
+ *   ld   row length of slot_map or block_table (int32 [S][ld])
+ * Products take K, V exactly and the query rows and softmax weights in fp16
+ * after scaling by powers of two; all sums are fp32.
+ * Requires D in {64,128,256}, Hq % Hkv == 0, scale > 0, Tq <= 1024, S and
+ * Hq <= 65535, P*page < 2^31; q, q_stride, out and the caches 16-byte aligned.
+ */
+int kvsel_kv4_attention(kvsel_ctx* ctx, const void* q, int64_t q_stride, int S, int Tq, int Hq, int Hkv, int D,
+                        const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v_codes,
+                        const uint8_t* v_scales, int P, int page, const int32_t* seq_lens,
+                        const int32_t* slot_map, const int32_t* block_table, int ld, int dead_slot, float scale,
+                        void* out, float* lse, void* stream);
+
+/*
+ * Causal attention over packed prompts (the pass that gives the K, V and query
+ * rows which the cache and the retention calls take).  Sequence s holds tokens
+ * [cu_seqlens[s], cu_seqlens[s+1]); its token i sees its tokens up to i:
+ *   out[i,h] = softmax_j( scale * q[i,h] . k[j,g(h)] ) v[j,g(h)]
+ *   lse[i,h] = ln sum_j exp( scale * q[i,h] . k[j,g(h)] )
+ * with g(h) = h / (Hq/Hkv).  Sequences may be empty.  Rows of tokens outside
+ * every sequence are not touched.  cu_seqlens must not descend; a negative
+ * start sets the device error word.
+ *   q, k, v  bf16, token i at element i*stride, its heads back to back
+ *   out      bf16 [T][Hq][D]; lse fp32 [T][Hq] or NULL
+ * The products take bf16 (softmax weights rounded to it), sums are fp32.
+ * Requires D in {64,128}, Hq % Hkv == 0, scale > 0, T <= 2^24, S and
+ * Hq <= 65535; q, k, v, out and strides 16-byte aligned.  No workspace.
+ */
+int kvsel_prompt_attention(kvsel_ctx* ctx, const void* q, const void* k, const void* v, int64_t q_stride,
+                           int64_t k_stride, int64_t v_stride, const int32_t* cu_seqlens, int S, int T, int Hq,
+                           int Hkv, int D, float scale, void* out, float* lse, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -25,8 +25,12 @@ SOURCES = [
     "workset_kernels.cu",
     "stage_pipeline.cu",
     "fp8_index.cu",
+    "slot_plan.cu",
+    "kv4_cache.cu",
+    "kv4_attention.cu",
+    "prompt_attention.cu",
 ]
-HEADERS = ["kvsel_internal.h", os.path.join("..", "..", "include", "kvsel.h")]
+HEADERS = ["kvsel_internal.h", "kv4_format.cuh", os.path.join("..", "..", "include", "kvsel.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xptxas", "-v"]

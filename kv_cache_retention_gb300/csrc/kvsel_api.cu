@@ -199,13 +199,14 @@ int kvsel_check_device(kvsel_ctx* ctx, void* stream) {
     if (!word) return KVSEL_OK;
     cudaMemset(ctx->dev_err, 0, sizeof(unsigned));
     if (word & KVSEL_DEV_TIMEOUT) return fail(ctx, KVSEL_ERR_TIMEOUT, "a bounded device wait gave up (tensor-core pipeline)");
-    return fail(ctx, KVSEL_ERR_DEVICE_CHECK, "device check failed:%s%s%s%s%s%s",
+    return fail(ctx, KVSEL_ERR_DEVICE_CHECK, "device check failed:%s%s%s%s%s%s%s",
                 (word & KVSEL_DEV_BAD_SLOT) ? " slot out of range" : "",
                 (word & KVSEL_DEV_BAD_POSITION) ? " position out of range" : "",
                 (word & KVSEL_DEV_BAD_BLOCK) ? " source block or cursor id out of range" : "",
                 (word & KVSEL_DEV_BAD_PAGE) ? " page out of range" : "",
                 (word & KVSEL_DEV_BAD_SET) ? " working set not ascending or page held twice" : "",
-                (word & KVSEL_DEV_POOL_FULL) ? " too few free pages" : "");
+                (word & KVSEL_DEV_POOL_FULL) ? " too few free pages" : "",
+                (word & KVSEL_DEV_BAD_LENGTH) ? " length out of range" : "");
 }
 
 int kvsel_memory_update(kvsel_ctx* ctx, const void* q_rows, int q_dtype, int L, int Hq, int R, int D,

@@ -58,6 +58,7 @@ enum kvsel_devcheck : unsigned {
     KVSEL_DEV_BAD_PAGE = 1u << 3,
     KVSEL_DEV_BAD_SET = 1u << 4,   // a working set not ascending, or a page held twice
     KVSEL_DEV_POOL_FULL = 1u << 5, // fewer free pages than incoming blocks
+    KVSEL_DEV_BAD_LENGTH = 1u << 6, // a session's or sequence's length outside its tables or packed rows
     KVSEL_DEV_TIMEOUT = 1u << 8,  // a bounded wait inside a kernel gave up
 };
 
@@ -88,6 +89,20 @@ struct kvsel_trace {
     }
     kvsel_trace(const kvsel_trace&) = delete;
     kvsel_trace& operator=(const kvsel_trace&) = delete;
+};
+
+// Puts the caller's current device back when a call ends.
+struct kvsel_device_scope {
+    int before = -1;
+    kvsel_device_scope() {
+        if (cudaGetDevice(&before) != cudaSuccess) before = -1;
+    }
+    ~kvsel_device_scope() {
+        int now = -1;
+        if (before >= 0 && cudaGetDevice(&now) == cudaSuccess && now != before) cudaSetDevice(before);
+    }
+    kvsel_device_scope(const kvsel_device_scope&) = delete;
+    kvsel_device_scope& operator=(const kvsel_device_scope&) = delete;
 };
 
 // Error helpers shared by the translation units that implement calls:
