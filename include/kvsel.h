@@ -540,7 +540,7 @@ int kvsel_kv4_load(kvsel_ctx* ctx, const uint8_t* k_codes, const uint8_t* k_scal
  * Products take K, V exactly and the query rows and softmax weights in fp16
  * after scaling by powers of two; all sums are fp32.
  * Requires D in {64,128,256}, Hq % Hkv == 0, scale > 0, Tq <= 1024, S and
- * Hq <= 65535, P*page < 2^31; q, q_stride, out and the caches 16-byte aligned.
+ * Hq <= 65535, P*page < 2^31, P*page*Hkv < 2^32; q, q_stride, out and the caches 16-byte aligned.
  */
 int kvsel_kv4_attention(kvsel_ctx* ctx, const void* q, int64_t q_stride, int S, int Tq, int Hq, int Hkv, int D,
                         const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v_codes,

@@ -173,6 +173,7 @@ int kvsel_ctx_destroy(kvsel_ctx* ctx) {
     cudaDeviceSynchronize();
     kvsel_stager_release(ctx);
     if (ctx->ws) cudaFree(ctx->ws);
+    if (ctx->kv4_partials) cudaFree(ctx->kv4_partials);
     if (ctx->dev_err) cudaFree(ctx->dev_err);
     for (int i = 0; i < ctx->n_rope; ++i) {
         cudaFree(ctx->rope[i].lo);

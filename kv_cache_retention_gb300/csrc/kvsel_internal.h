@@ -47,6 +47,9 @@ struct kvsel_ctx {
     // Device address of the fixed scratch array of kvsel_rule_scores_noalloc on
     // this context's device, looked up by that call's first use on the context.
     void* noalloc_scratch = nullptr;
+    // Partial results and arrival counters of kvsel_kv4_attention calls that split a session's
+    // tokens; of one size, allocated by the first such call, the counters 0 between launches.
+    void* kv4_partials = nullptr;
     char err[512] = {0};
 };
 

@@ -365,6 +365,40 @@ def test_attention_never_reads_dropped_rows(ctx):
     assert torch.isnan(out).all()
 
 
+@pytest.mark.parametrize("Tq", [1, 3])
+def test_attention_nan_keys_and_queries(ctx, Tq):
+    """A NaN key group makes the rows that see it NaN, a NaN query its own row, in one kv head only; the rows before
+    the token stay as they are, also where it is the only thing a warp sees."""
+    g = torch.Generator(device="cuda").manual_seed(15)
+    Hq, Hkv, D, page, n = 8, 2, 128, 16, 77
+    cache = _random_cache(g, 5, Hkv, page, D)
+    q = torch.randn((1, Tq, Hq, D), generator=g, device="cuda").to(BF)
+    table = _i32([[3, 0, 4, 1, 2]])
+    clean = torch.empty_like(q)
+    ctx.kv4_attention(q, *cache, _i32([n]), clean, block_table=table)
+    bad = [c.clone() for c in cache]
+    bad[1][2, 0, (n - 1) % page, 2] = 255               # the last token's key, kv head 0
+    bad[3][2, 1, (n - 1) % page, 4] = 255               # and its value, kv head 1
+    out, lse = torch.empty_like(q), torch.empty((1, Tq, Hq), device="cuda")
+    ctx.kv4_attention(q, *bad, _i32([n]), out, block_table=table, lse=lse)
+    assert torch.equal(out[:, :-1], clean[:, :-1])
+    assert torch.isnan(out[0, -1, :4]).all() and torch.isnan(lse[0, -1, :4]).all()
+    assert torch.isnan(out[0, -1, 4:, 64:80]).all() and torch.isfinite(lse[0, -1, 4:]).all()
+    keep = torch.ones(D, dtype=torch.bool, device="cuda")
+    keep[64:80] = False
+    assert torch.equal(out[0, -1, 4:, keep], clean[0, -1, 4:, keep])
+    q2 = q.clone()
+    q2[0, 0, 1, 9] = float("nan")
+    bad[1].fill_(255)
+    ctx.kv4_attention(q2, *cache, _i32([n]), out, block_table=table, lse=lse)
+    assert torch.isnan(out[0, 0, 1]).all() and torch.isnan(lse[0, 0, 1])
+    out[0, 0, 1] = clean[0, 0, 1]
+    assert torch.equal(out, clean)
+    ctx.kv4_attention(q, *bad, _i32([n]), out, block_table=table, lse=lse)  # nothing but NaN keys
+    ctx.check_device()
+    assert torch.isnan(out).all() and torch.isnan(lse).all()
+
+
 def test_attention_dead_slot_inside_the_pool(ctx):
     """The dead slot may be a real row of the pool: it is skipped all the same."""
     g = torch.Generator(device="cuda").manual_seed(6)
