@@ -1,11 +1,41 @@
-// kvsel_prompt_attention: causal attention over packed prompts with grouped heads.
+// kvsel_prompt_attention: causal attention over packed prompts with grouped heads,
+// on the 5th-generation tensor cores.
 //
 // Sequence s holds tokens [cu[s], cu[s+1]); row i of it sees its rows 0..i:
-//   out = sum_j p_j v_j / sum_j p_j,  p_j = 2^(scale log2e (q_i . k_j - max)),
+//   out = sum_j p_j v_j / sum_j p_j,  p_j = 2^(scale log2e q_i . k_j - ref),
 //   lse = ln sum_j e^(scale q_i . k_j).
-// One block per (token, query head): a thread takes one key's dot product of a chunk
-// of 128, then one dim of the weighted sum, with the softmax's running maximum and
-// sum kept across chunks in fp32.
+//
+// A block takes one query head and 256 consecutive rows of one sequence, as two tiles
+// of 128 rows (TMEM lanes), and goes once over the keys from the diagonal down, 128 at
+// a time:
+//   S = Q K^T   tcgen05.mma, both operands from shared memory, 128 fp32 columns a tile
+//   P = 2^(S sc - ref) in bf16, written over S in TMEM
+//   O += P V    tcgen05.mma, P from TMEM, V from shared memory as it lies (its rows are
+//               the product's K axis: an "MN-major" operand)
+// The two tiles share every K and V tile that is loaded (with one tile a block would
+// ask L2 for 64 bytes a cycle and SM, about what it gives) and take turns: while one
+// tile's softmax runs, the tensor cores work on the other's products.
+//
+// The softmax keeps per row a reference that only follows the running maximum when
+// that has passed it by 8 (log2): weights are then at most 2^8, which bf16 and the fp32
+// sums hold as well as 1, and O is rescaled only then.  P is rounded to bf16 since both
+// operands of the product have one type and V's range is bf16's; its relative rounding
+// of 2^-9 per weight is random and comes to about the output's own rounding.
+//
+// 384 threads: warp 0 loads (TMA), warp 1 issues the MMAs, warps 2-3 look over the V
+// tiles of the diagonal (below), warps 4-7 and 8-11 are the softmax of the two tiles, a
+// row per thread.  TMEM: S of tile 0 and 1 at columns 0 and 128, O at 256 and 384.
+//
+// Masked places.  A weight of zero does not hide a NaN or an infinity in V.  Key tiles
+// below the diagonal are seen by every row of a tile, so only the first two tiles of a
+// block's pass hold values that some rows must not see; there warps 2-3 set such values
+// to zero in shared memory before the product, and if there were any, each row adds
+// those it does see to its output at the end (what the sum would be: infinite or NaN).
+//
+// Every wait is bounded (1 s); on a timeout the block flags KVSEL_ERR_TIMEOUT in the
+// device error word, drains its own copies and MMAs, frees TMEM and returns.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <limits.h>
 
@@ -13,78 +43,476 @@
 
 namespace {
 
-constexpr int kThreads = 128;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kTile = 128;              // rows of a tile, keys of a step
+constexpr int kUnit = 2 * kTile;        // rows of a block
+constexpr int kThreads = 384;
+constexpr float kSlack = 8.f;           // how far (log2) a row's maximum may pass its reference
+constexpr uint64_t kWaitNs = 1000000000ull;
+// Registers per thread: at launch, then after the first warpgroup's setmaxnreg.dec and
+// the softmax warpgroups' .inc.  An .inc beyond the launch's registers would wait
+// forever; the launcher checks the compiled count.
+constexpr int kRegsLaunch = 168, kRegsCtl = 80, kRegsSoft = 208;
+static_assert(kRegsCtl + 2 * kRegsSoft <= 3 * kRegsLaunch && kRegsLaunch * kThreads <= 65536, "register split");
+
+constexpr int kColS = 0, kColO = 256, kTmemCols = 512;
 
 struct PromptArgs {
-    const __nv_bfloat16 *q, *k, *v;
-    int64_t q_stride, k_stride, v_stride;
+    const __nv_bfloat16* v;
+    int64_t v_stride;
     const int32_t* cu;
-    int S, T, Hq, Hkv, D;
-    float scale;
+    int S, T, Hq, Hkv, n_virtual;
+    float scale2;           // scale * log2(e)
     __nv_bfloat16* out;
     float* lse;
     unsigned* err;
 };
 
-__global__ void __launch_bounds__(kThreads) prompt_attention_kernel(const PromptArgs a) {
-    __shared__ float qs[128], ps[kThreads], red[4];
-    const int tid = threadIdx.x, h = blockIdx.y, i = blockIdx.x;
-    const int g = h / (a.Hq / a.Hkv);
-    // the last sequence that starts at or before token i
-    int lo = 0, hi = a.S;
+template <int D>
+struct Cfg {
+    static constexpr int kBlock = kTile * 128;             // 128 rows x 64 dims, 128-byte swizzled
+    static constexpr int kBytes = D / 64 * kBlock;         // one tile of Q, K or V
+    static constexpr int kStages = 5;                      // K and V tiles share the ring
+    struct Tail {
+        uint64_t q_full, full[kStages], empty[kStages], s_full[2], p_full[2], o_done[2], v_ok[2], drained;
+        uint32_t tmem;
+        int abort_flag, odd_v;
+    };
+    static constexpr size_t kSmem = (size_t)(2 + kStages) * kBytes + sizeof(Tail) + 1024;
+    static_assert(kSmem <= 232448, "shared memory per block");
+};
+
+// ---- PTX wrappers ----------------------------------------------------------
+
+__device__ __forceinline__ uint32_t saddr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void mbar_init(uint64_t* b, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(saddr(b)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* b, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(saddr(b)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* b) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(saddr(b)) : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint64_t* b, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(saddr(b)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ uint64_t gtimer() {
+    uint64_t t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+// Bounded wait for a phase; false when this or another role gave up.
+__device__ __forceinline__ bool wait_phase(uint64_t* b, uint32_t parity, volatile int* abort_flag, unsigned* err) {
+    if (mbar_try(b, parity)) return true;
+    const uint64_t t0 = gtimer();
+    for (uint32_t i = 1;; ++i) {
+        if (mbar_try(b, parity)) return true;
+        if ((i & 63) == 0) {
+            if (*abort_flag) return false;
+            if (gtimer() - t0 > kWaitNs) {
+                *abort_flag = 1;
+                atomicOr(err, (unsigned)KVSEL_DEV_TIMEOUT);
+                return false;
+            }
+        }
+    }
+}
+// The same for a whole warp, with one answer for its lanes.
+__device__ __forceinline__ bool wait_warp(uint64_t* b, uint32_t parity, volatile int* abort_flag, unsigned* err) {
+    return __all_sync(0xffffffffu, wait_phase(b, parity, abort_flag, err));
+}
+// Bounded wait that ignores the abort flag: a role's own copies or MMAs before the block ends.
+__device__ __forceinline__ void drain_phase(uint64_t* b, uint32_t parity) {
+    const uint64_t t0 = gtimer();
+    while (!mbar_try(b, parity) && gtimer() - t0 < kWaitNs) {
+    }
+}
+__device__ __forceinline__ void tma_load(const CUtensorMap* map, uint64_t* bar, void* dst, int d, int h, int t) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+            saddr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(saddr(bar)), "r"(d), "r"(h), "r"(t)
+        : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// kind::f16 instruction descriptor: fp32 sums, bf16 operands, M = 128; b_mn: B's rows run along K.
+__host__ __device__ constexpr uint32_t idesc(int n, bool b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
+           ((uint32_t)(kTile >> 4) << 24);
+}
+// Shared-memory descriptor, 128-byte swizzle.  K-major: groups of 8 rows 1024 bytes apart.  MN-major: groups
+// of 8 K rows 1024 bytes apart (stride offset), blocks of 64 columns one tile block apart (leading offset).
+__device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t leading) {
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(leading >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accum) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(id), "r"(accum)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t accum) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(id), "r"(accum)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(saddr(bar)) : "memory");
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+#define O4(a, i) "=r"(a[i]), "=r"(a[i + 1]), "=r"(a[i + 2]), "=r"(a[i + 3])
+#define I4(a, i) "r"(a[i]), "r"(a[i + 1]), "r"(a[i + 2]), "r"(a[i + 3])
+// 32 columns of the thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%"
+        "21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : O4(r, 0), O4(r, 4), O4(r, 8), O4(r, 12), O4(r, 16), O4(r, 20), O4(r, 24), O4(r, 28)
+        : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%"
+        "19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::I4(r, 0),
+        I4(r, 4), I4(r, 8), I4(r, 12), I4(r, 16), I4(r, 20), I4(r, 24), I4(r, 28), "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// ---- the kernel ------------------------------------------------------------
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                            const __grid_constant__ CUtensorMap map_v, const PromptArgs a) {
+    using C = Cfg<D>;
+    constexpr int kStages = C::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    uint8_t* const sq = smem;                     // [2][kBytes]
+    uint8_t* const ring = smem + 2 * C::kBytes;   // [kStages][kBytes]
+    typename C::Tail& t = *reinterpret_cast<typename C::Tail*>(smem + (2 + kStages) * C::kBytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile int* const abort_flag = &t.abort_flag;
+
+    // The block's rows.  Row tiles are numbered by their sequence's start: sequence s has the numbers from
+    // cu[s] / 256 + s on, which leaves it at least ceil(length / 256) of them (some stay empty); long rows first.
+    const int head = blockIdx.x % a.Hq, g = head / (a.Hq / a.Hkv);
+    const int number = a.n_virtual - 1 - (int)(blockIdx.x / a.Hq);
+    int lo = 0, hi = a.S;                         // the last sequence whose first number is not above
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (__ldg(a.cu + mid) <= i) lo = mid; else hi = mid;
+        if (__ldg(a.cu + mid) / kUnit + mid <= number) lo = mid; else hi = mid;
     }
-    const int first = __ldg(a.cu + lo);
-    if (i < first || i >= __ldg(a.cu + lo + 1)) return;
+    const int first = __ldg(a.cu + lo), len = min(__ldg(a.cu + lo + 1), a.T) - first;
+    const int unit = number - (first / kUnit + lo);
     if (first < 0) {
-        if (tid == 0) atomicOr(a.err, (unsigned)KVSEL_DEV_BAD_LENGTH);
+        if (threadIdx.x == 0) atomicOr(a.err, (unsigned)KVSEL_DEV_BAD_LENGTH);
         return;
     }
-    if (tid < a.D) qs[tid] = __bfloat162float(a.q[i * a.q_stride + (int64_t)h * a.D + tid]);
-    float m = -INFINITY, l = 0.f, o = 0.f;
-    const float c = a.scale * kLog2e;
+    if (unit < 0 || (int64_t)unit * kUnit >= len) return;
+    const int row0 = unit * kUnit;
+    const bool two = row0 + kTile < len;          // the second tile has rows
+    const int n = 2 * unit + (two ? 2 : 1);       // steps; step i takes key tile n - 1 - i
+    const int skip0 = two ? 1 : 0;                // tile 0 starts at step skip0
+
+    if (threadIdx.x == 0) {
+        mbar_init(&t.q_full, 1);
+        for (int i = 0; i < kStages; ++i) mbar_init(&t.full[i], 1), mbar_init(&t.empty[i], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&t.s_full[i], 1);
+            mbar_init(&t.p_full[i], 4);
+            mbar_init(&t.o_done[i], 1);
+            mbar_init(&t.v_ok[i], 2);
+        }
+        mbar_init(&t.drained, 1);
+        t.abort_flag = t.odd_v = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&t.tmem)), "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_before();
     __syncthreads();
-    for (int j0 = first; j0 <= i; j0 += kThreads) {
-        const int j = j0 + tid;
-        float x = -INFINITY;
-        if (j <= i) {
-            x = 0.f;
-            const uint4* kr = reinterpret_cast<const uint4*>(a.k + j * a.k_stride + (int64_t)g * a.D);
-            for (int d = 0; d < a.D / 8; ++d) {
-                const uint4 w = __ldg(kr + d);
-                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    tc_after();
+    const uint32_t tmem = t.tmem;
+
+    // Place in the ring of step i's K and V tile: K0, K1, V0, K2, V1, ..., V(n-1).
+    auto at_k = [](int i) { return i == 0 ? 0 : 2 * i - 1; };
+    auto at_v = [n](int i) { return i == n - 1 ? 2 * n - 1 : 2 * i + 2; };
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
+        if (warp == 0 && lane == 0) {
+            // ---- loads ----
+            mbar_expect_tx(&t.q_full, (two ? 2 : 1) * C::kBytes);
+            for (int x = 0; x < (two ? 2 : 1); ++x)
+                for (int b = 0; b < D / 64; ++b)
+                    tma_load(&map_q, &t.q_full, sq + x * C::kBytes + b * C::kBlock, 64 * b, head, first + row0 + x * kTile);
+            int done = 0;
+            for (int pos = 0; pos < 2 * n; ++pos, ++done) {
+                const bool is_v = pos == 2 * n - 1 || (pos > 0 && pos % 2 == 0);
+                const int i = pos == 2 * n - 1 ? n - 1 : is_v ? pos / 2 - 1 : (pos + 1) / 2;
+                const int st = pos % kStages;
+                if (!wait_phase(&t.empty[st], (uint32_t)((pos / kStages) & 1) ^ 1u, abort_flag, a.err)) break;
+                mbar_expect_tx(&t.full[st], C::kBytes);
+                for (int b = 0; b < D / 64; ++b)
+                    tma_load(is_v ? &map_v : &map_k, &t.full[st], ring + st * C::kBytes + b * C::kBlock, 64 * b, g,
+                             first + (n - 1 - i) * kTile);
+            }
+            drain_phase(&t.q_full, 0);
+            for (int pos = done > kStages ? done - kStages : 0; pos < done; ++pos)
+                drain_phase(&t.full[pos % kStages], (uint32_t)((pos / kStages) & 1));
+        } else if (warp == 1 && lane == 0) {
+            // ---- MMAs ----
+            const uint32_t qb = saddr(sq), rb = saddr(ring);
+            auto issue_s = [&](int x, int i) {
+                const uint32_t ab = qb + x * C::kBytes, bb = rb + (at_k(i) % kStages) * C::kBytes;
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    x = fmaf(__uint_as_float(u[b] << 16), qs[d * 8 + 2 * b], x);
-                    x = fmaf(__uint_as_float(u[b] & 0xFFFF0000u), qs[d * 8 + 2 * b + 1], x);
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = (k >> 2) * C::kBlock + (k & 3) * 32;
+                    mma_ss(tmem + kColS + x * kTile, sdesc(ab + off, 16), sdesc(bb + off, 16), idesc(kTile, false), k > 0);
+                }
+                mma_commit(&t.s_full[x]);
+            };
+            bool ok = wait_phase(&t.q_full, 0, abort_flag, a.err) && wait_phase(&t.full[0], 0, abort_flag, a.err);
+            if (ok) {
+                tc_after();
+                if (two) {
+                    issue_s(1, 0);
+                } else {
+                    issue_s(0, 0);
+                }
+                mma_commit(&t.empty[0]);
+            }
+            for (int i = 0; i < n && ok; ++i) {
+                const int kp = at_k(i + 1), vp = at_v(i);
+                const bool more = i + 1 < n;
+                if (more && !(ok = wait_phase(&t.full[kp % kStages], (uint32_t)((kp / kStages) & 1), abort_flag, a.err))) break;
+                if (two && i == 0) issue_s(0, 1);  // tile 0 starts one step later
+                if (!(ok = wait_phase(&t.full[vp % kStages], (uint32_t)((vp / kStages) & 1), abort_flag, a.err))) break;
+                if (i < 2 && !(ok = wait_phase(&t.v_ok[i], 0, abort_flag, a.err))) break;
+                const uint32_t vb = rb + (vp % kStages) * C::kBytes;
+                for (int x = 0; x < 2 && ok; ++x) {
+                    const int from = x == 0 ? skip0 : 0;  // the tile's first step
+                    if ((x == 1 && !two) || i < from) continue;
+                    if (!(ok = wait_phase(&t.p_full[x], (uint32_t)((i - from) & 1), abort_flag, a.err))) break;
+                    tc_after();
+#pragma unroll
+                    for (int k = 0; k < kTile / 16; ++k)
+                        mma_ts(tmem + kColO + x * D, tmem + kColS + x * kTile + k * 8, sdesc(vb + k * 2048, C::kBlock),
+                               idesc(D, true), i > from || k > 0);
+                    mma_commit(&t.o_done[x]);
+                    // writes over the P that the product above reads: one thread's MMAs run in the order of issue
+                    if (more) issue_s(x, i + 1);
+                }
+                if (!ok) break;
+                mma_commit(&t.empty[vp % kStages]);
+                if (more) mma_commit(&t.empty[kp % kStages]);
+            }
+            mma_commit(&t.drained);
+            drain_phase(&t.drained, 0);
+        } else if (warp >= 2) {
+            // ---- V tiles of the first two steps: NaN and infinities to zero ----
+            for (int i = 0; i < 2 && i < n; ++i) {
+                const int vp = at_v(i);
+                if (!wait_phase(&t.full[vp % kStages], (uint32_t)((vp / kStages) & 1), abort_flag, a.err)) break;
+                uint4* const tile = reinterpret_cast<uint4*>(ring + (vp % kStages) * C::kBytes);
+                bool odd = false;
+                for (int e = (warp - 2) * 32 + lane; e < C::kBytes / 16; e += 64) {
+                    uint4 w = tile[e];
+                    uint32_t u[4] = {w.x, w.y, w.z, w.w}, hit = 0;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) hit |= (u[k] & 0x7F807F80u) + 0x00800080u;
+                    if (hit & 0x80008000u) {
+                        odd = true;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if ((u[k] & 0x7F80u) == 0x7F80u) u[k] &= 0xFFFF0000u;
+                            if ((u[k] & 0x7F800000u) == 0x7F800000u) u[k] &= 0x0000FFFFu;
+                        }
+                        tile[e] = make_uint4(u[0], u[1], u[2], u[3]);
+                    }
+                }
+                if (odd) t.odd_v = 1;
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&t.v_ok[i]);
+            }
+        }
+        __syncwarp();
+        tc_before();
+        __syncthreads();
+        tc_after();
+        if (warp == 1)
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+        return;
+    }
+
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+    // ---- softmax: one row per thread ----
+    const int x = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t ts = lane_base + kColS + x * kTile, to = lane_base + kColO + x * D;
+    const int from = x == 0 ? skip0 : 0;
+    const int steps = x == 1 && !two ? 0 : n - from;
+    const float sc = a.scale2;
+    float ref = 0.f;
+    float2 sum = make_float2(0.f, 0.f);
+    bool ok = true;
+    for (int k = 0; k < steps; ++k) {
+        if (!(ok = wait_warp(&t.s_full[x], (uint32_t)(k & 1), abort_flag, a.err))) break;
+        tc_after();
+        uint32_t s[kTile];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, s + 32 * i);
+        tmem_wait_ld();
+        if (k == 0) {  // the diagonal: key c of the tile is seen by rows r >= c
+#pragma unroll
+            for (int c = 0; c < kTile; ++c)
+                if (c > r) s[c] = 0xFF800000u;
+        }
+        float m[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m[i] = __uint_as_float(s[i]);
+#pragma unroll
+        for (int c = 4; c + 8 <= kTile; c += 8)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m[i] = max3(m[i], __uint_as_float(s[c + i]), __uint_as_float(s[c + 4 + i]));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m[i] = fmaxf(m[i], __uint_as_float(s[kTile - 4 + i]));
+        const float top = fmaxf(max3(m[0], m[1], m[2]), m[3]) * sc;
+        if (k == 0) {
+            ref = top == -INFINITY ? 0.f : top;
+        } else if (__any_sync(0xffffffffu, top > ref + kSlack)) {
+            // references move up: the sums so far and O shrink with them
+            const float next = fmaxf(ref, top), f = ex2(ref - next);
+            ref = next;
+            sum.x *= f, sum.y *= f;
+            if (!(ok = wait_warp(&t.o_done[x], (uint32_t)((k - 1) & 1), abort_flag, a.err))) break;
+            tc_after();
+#pragma unroll
+            for (int b = 0; b < D / 32; ++b) {
+                uint32_t o[32];
+                tmem_ld32(to + 32 * b, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st32(to + 32 * b, o);
+            }
+        }
+        const float2 sc2 = make_float2(sc, sc), nr = make_float2(-ref, -ref);
+        uint32_t p[kTile / 2];
+#pragma unroll
+        for (int c = 0; c < kTile / 2; ++c) {
+            const float2 y = __ffma2_rn(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), sc2, nr);
+            const float2 e = make_float2(ex2(y.x), ex2(y.y));
+            sum = __fadd2_rn(sum, e);
+            p[c] = pack_bf16(e.x, e.y);
+        }
+        tmem_st32(ts, p);
+        tmem_st32(ts + 32, p + 32);
+        tmem_wait_st();
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&t.p_full[x]);
+    }
+    // ---- output ----
+    if (ok && steps > 0) ok = wait_warp(&t.o_done[x], (uint32_t)((steps - 1) & 1), abort_flag, a.err);
+    if (ok && steps > 0) {
+        tc_after();
+        bool odd = false;
+        for (int i = 0; i < 2 && i < n && ok; ++i) ok = wait_warp(&t.v_ok[i], 0, abort_flag, a.err);
+        odd = *(volatile int*)&t.odd_v != 0;
+        const int row = row0 + x * kTile + r;
+        const float l = sum.x + sum.y, inv = 1.f / l;
+        const int64_t at = (int64_t)(first + row) * a.Hq + head;
+        const int key0 = n > 1 ? (n - 2) * kTile : 0;   // first key of the tiles that were looked over
+#pragma unroll
+        for (int b = 0; b < D / 32; ++b) {
+            uint32_t o[32];
+            tmem_ld32(to + 32 * b, o);
+            tmem_wait_ld();
+            if (row >= len) continue;
+            if (odd) {
+                for (int j = key0; j <= row; ++j) {
+                    const __nv_bfloat16* v = a.v + (int64_t)(first + j) * a.v_stride + (int64_t)g * D + 32 * b;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float w = __bfloat162float(v[i]);
+                        if (!(fabsf(w) < INFINITY)) o[i] = __float_as_uint(__uint_as_float(o[i]) + w);
+                    }
                 }
             }
-            x *= c;
-        }
-        float mx = x;
+            uint4* const dst = reinterpret_cast<uint4*>(a.out + at * D + 32 * b);
 #pragma unroll
-        for (int k = 16; k; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
-        if ((tid & 31) == 0) red[tid >> 5] = mx;
-        __syncthreads();
-        const float mn = fmaxf(fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])), m);
-        const float base = mn == -INFINITY ? 0.f : mn, corr = exp2f(m - base);
-        m = mn;
-        ps[tid] = j <= i ? exp2f(x - base) : 0.f;
-        l *= corr, o *= corr;
-        __syncthreads();
-        const int cnt = min(kThreads, i + 1 - j0);
-        for (int b = 0; b < cnt; ++b) {
-            const float p = ps[b];
-            l += p;
-            if (tid < a.D) o = fmaf(p, __bfloat162float(a.v[(j0 + b) * a.v_stride + (int64_t)g * a.D + tid]), o);
+            for (int i = 0; i < 4; ++i) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    w[e] = pack_bf16(__uint_as_float(o[8 * i + 2 * e]) * inv, __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
+                dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
         }
-        __syncthreads();
+        if (a.lse && row < len) a.lse[at] = (ref + log2f(l)) * kLn2;
     }
-    if (tid < a.D) a.out[((int64_t)i * a.Hq + h) * a.D + tid] = __float2bfloat16_rn(o / l);
-    if (a.lse && tid == 0) a.lse[(int64_t)i * a.Hq + h] = (m + log2f(l)) * kLn2;
+    tc_before();
+    __syncthreads();
+}
+
+// bf16 rows [T][H][D], tokens `stride` elements apart: boxes of 64 dims of one head, 128 tokens, zero fill.
+bool make_map(CUtensorMap* map, const void* base, int T, int H, int D, int64_t stride) {
+    auto fn = kvsel_tmap_encoder();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T};
+    cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
+    cuuint32_t box[3] = {64, 1, (cuuint32_t)kTile};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const PromptArgs& a, cudaStream_t s) {
+    auto* kernel = prompt_attention_kernel<D>;
+    cudaFuncAttributes fa;
+    cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;  // the register split counts on it
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<D>::kSmem);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)a.n_virtual * a.Hq, kThreads, Cfg<D>::kSmem, s>>>(mq, mk, mv, a);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -110,9 +538,13 @@ extern "C" int kvsel_prompt_attention(kvsel_ctx* ctx, const void* q, const void*
     auto off16 = [](const void* p, int64_t stride) { return (reinterpret_cast<uintptr_t>(p) & 15u) || (stride * 2) % 16; };
     if (off16(q, q_stride) || off16(k, k_stride) || off16(v, v_stride) || off16(out, 0))
         return kvsel_fail(ctx, KVSEL_ERR_ALIGN, "prompt_attention: q, k, v, out and the strides must be 16-byte aligned");
-    const PromptArgs a{(const __nv_bfloat16*)q, (const __nv_bfloat16*)k, (const __nv_bfloat16*)v, q_stride, k_stride,
-                       v_stride, cu_seqlens, S, T, Hq, Hkv, D, scale, (__nv_bfloat16*)out, lse, ctx->dev_err};
-    prompt_attention_kernel<<<dim3(T, Hq), kThreads, 0, (cudaStream_t)stream>>>(a);
-    const cudaError_t e = cudaGetLastError();
+    const int n_virtual = T / kUnit + S;
+    if ((int64_t)n_virtual * Hq > INT_MAX) return kvsel_fail(ctx, KVSEL_ERR_UNSUPPORTED, "prompt_attention: too many rows");
+    CUtensorMap mq, mk, mv;
+    if (!make_map(&mq, q, T, Hq, D, q_stride) || !make_map(&mk, k, T, Hkv, D, k_stride) || !make_map(&mv, v, T, Hkv, D, v_stride))
+        return kvsel_fail(ctx, KVSEL_ERR_CUDA, "prompt_attention: tensor map encoding failed");
+    const PromptArgs a{(const __nv_bfloat16*)v, v_stride, cu_seqlens, S, T, Hq, Hkv, n_virtual, scale * kLog2e,
+                       (__nv_bfloat16*)out, lse, ctx->dev_err};
+    const cudaError_t e = D == 64 ? launch<64>(mq, mk, mv, a, (cudaStream_t)stream) : launch<128>(mq, mk, mv, a, (cudaStream_t)stream);
     return e == cudaSuccess ? KVSEL_OK : kvsel_cuda_fail(ctx, e, "prompt_attention launch");
 }
