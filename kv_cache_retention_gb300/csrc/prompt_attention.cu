@@ -22,13 +22,13 @@
 // operands of the product have one type and V's range is bf16's; its relative rounding
 // of 2^-9 per weight is random and comes to about the output's own rounding.
 //
-// 384 threads: warp 0 loads (TMA), warp 1 issues the MMAs, warps 2-3 look over the V
-// tiles of the diagonal (below), warps 4-7 and 8-11 are the softmax of the two tiles, a
+// 384 threads: warp 0 loads (TMA), warps 1 and 2 issue the MMAs of one tile each, warp 3
+// looks over the V tiles of the diagonal (below), warps 4-7 and 8-11 are the softmax of the two tiles, a
 // row per thread.  TMEM: S of tile 0 and 1 at columns 0 and 128, O at 256 and 384.
 //
 // Masked places.  A weight of zero does not hide a NaN or an infinity in V.  Key tiles
 // below the diagonal are seen by every row of a tile, so only the first two tiles of a
-// block's pass hold values that some rows must not see; there warps 2-3 set such values
+// block's pass hold values that some rows must not see; there warp 3 sets such values
 // to zero in shared memory before the product, and if there were any, each row adds
 // those it does see to its output at the end (what the sum would be: infinite or NaN).
 //
@@ -55,6 +55,8 @@ constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr int kRegsLaunch = 168, kRegsCtl = 80, kRegsSoft = 208;
 static_assert(kRegsCtl + 2 * kRegsSoft <= 3 * kRegsLaunch && kRegsLaunch * kThreads <= 65536, "register split");
 
+// All of TMEM is allocated, so its base is column 0.
+constexpr uint32_t kTmem = 0;
 constexpr int kColS = 0, kColO = 256, kTmemCols = 512;
 
 struct PromptArgs {
@@ -74,7 +76,7 @@ struct Cfg {
     static constexpr int kBytes = D / 64 * kBlock;         // one tile of Q, K or V
     static constexpr int kStages = 5;                      // K and V tiles share the ring
     struct Tail {
-        uint64_t q_full, full[kStages], empty[kStages], s_full[2], p_full[2], o_done[2], v_ok[2], drained;
+        uint64_t q_full, full[kStages], empty[kStages], s_full[2], p_full[2], o_done[2], v_ok[2], turn[2], drained;
         uint32_t tmem;
         int abort_flag, odd_v;
     };
@@ -168,20 +170,28 @@ __device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t leading) {
     return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(leading >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accum) {
+// MMAs and commits are issued by the lane whose `lead` is set; the operands are computed by the whole warp, so
+// that they stay in uniform registers.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accum, uint32_t lead) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(id), "r"(accum)
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(id), "r"(accum), "r"(lead)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t accum) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t accum, uint32_t lead) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-        "r"(a), "l"(b), "r"(id), "r"(accum)
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(id), "r"(accum), "r"(lead)
         : "memory");
 }
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(saddr(bar)) : "memory");
+__device__ __forceinline__ void mma_commit(uint32_t bar, uint32_t lead) {
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar),
+        "r"(lead)
+        : "memory");
 }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -245,14 +255,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         mbar_init(&t.q_full, 1);
-        for (int i = 0; i < kStages; ++i) mbar_init(&t.full[i], 1), mbar_init(&t.empty[i], 1);
+        for (int i = 0; i < kStages; ++i) mbar_init(&t.full[i], 1), mbar_init(&t.empty[i], two ? 2 : 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&t.s_full[i], 1);
             mbar_init(&t.p_full[i], 4);
             mbar_init(&t.o_done[i], 1);
-            mbar_init(&t.v_ok[i], 2);
+            mbar_init(&t.v_ok[i], 1);
+            mbar_init(&t.turn[i], 1);
         }
-        mbar_init(&t.drained, 1);
+        mbar_init(&t.drained, 2);
         t.abort_flag = t.odd_v = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -292,63 +303,79 @@ __global__ void __launch_bounds__(kThreads, 1)
             drain_phase(&t.q_full, 0);
             for (int pos = done > kStages ? done - kStages : 0; pos < done; ++pos)
                 drain_phase(&t.full[pos % kStages], (uint32_t)((pos / kStages) & 1));
-        } else if (warp == 1 && lane == 0) {
-            // ---- MMAs ----
-            const uint32_t qb = saddr(sq), rb = saddr(ring);
-            auto issue_s = [&](int x, int i) {
-                const uint32_t ab = qb + x * C::kBytes, bb = rb + (at_k(i) % kStages) * C::kBytes;
+        } else if (warp == 1 || warp == 2) {
+            // ---- MMAs: a warp per tile ----
+            // Two issuers on two SM sub-partitions: what one spends on barriers and descriptors, between the
+            // softmax's instructions, passes while the other's products run (one issuer for both tiles kept the
+            // tensor pipe 56% busy).
+            const int x = warp - 1;
+            const uint32_t lead = lane == 0;
+            if (x == 0 || two) {
+                const int from = x == 0 ? skip0 : 0;  // the tile's first step
+                const uint64_t dq = sdesc(saddr(sq) + x * C::kBytes, 16);
+                const uint64_t dk0 = sdesc(saddr(ring), 16), dv0 = sdesc(saddr(ring), C::kBlock);
+                constexpr uint32_t kStep = C::kBytes >> 4;  // a stage, in a descriptor's address units
+                const uint32_t ts = kTmem + kColS + x * kTile, to = kTmem + kColO + x * D;
+                auto issue_s = [&](uint32_t st) {
+                    const uint64_t dk = dk0 + st * kStep;
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = (k >> 2) * C::kBlock + (k & 3) * 32;
-                    mma_ss(tmem + kColS + x * kTile, sdesc(ab + off, 16), sdesc(bb + off, 16), idesc(kTile, false), k > 0);
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t off = ((k >> 2) * C::kBlock + (k & 3) * 32) >> 4;
+                        mma_ss(ts, dq + off, dk + off, idesc(kTile, false), k > 0, lead);
+                    }
+                    mma_commit(saddr(&t.s_full[x]), lead);
+                };
+                if (from == 1 && lead) {              // the first K and V tile are the other tile's alone
+                    mbar_arrive(&t.empty[0]);
+                    mbar_arrive(&t.empty[at_v(0) % kStages]);
                 }
-                mma_commit(&t.s_full[x]);
-            };
-            bool ok = wait_phase(&t.q_full, 0, abort_flag, a.err) && wait_phase(&t.full[0], 0, abort_flag, a.err);
-            if (ok) {
-                tc_after();
-                if (two) {
-                    issue_s(1, 0);
-                } else {
-                    issue_s(0, 0);
-                }
-                mma_commit(&t.empty[0]);
-            }
-            for (int i = 0; i < n && ok; ++i) {
-                const int kp = at_k(i + 1), vp = at_v(i);
-                const bool more = i + 1 < n;
-                if (more && !(ok = wait_phase(&t.full[kp % kStages], (uint32_t)((kp / kStages) & 1), abort_flag, a.err))) break;
-                if (two && i == 0) issue_s(0, 1);  // tile 0 starts one step later
-                if (!(ok = wait_phase(&t.full[vp % kStages], (uint32_t)((vp / kStages) & 1), abort_flag, a.err))) break;
-                if (i < 2 && !(ok = wait_phase(&t.v_ok[i], 0, abort_flag, a.err))) break;
-                const uint32_t vb = rb + (vp % kStages) * C::kBytes;
-                for (int x = 0; x < 2 && ok; ++x) {
-                    const int from = x == 0 ? skip0 : 0;  // the tile's first step
-                    if ((x == 1 && !two) || i < from) continue;
-                    if (!(ok = wait_phase(&t.p_full[x], (uint32_t)((i - from) & 1), abort_flag, a.err))) break;
+                bool ok = wait_warp(&t.q_full, 0, abort_flag, a.err) && wait_warp(&t.full[at_k(from)], 0, abort_flag, a.err);
+                if (ok) {
                     tc_after();
+                    issue_s(at_k(from));
+                    mma_commit(saddr(&t.empty[at_k(from)]), lead);
+                }
+                // stages and phases of the tiles of step i: K(i + 1), V(i)
+                uint32_t sk = at_k(from + 1) % kStages, pk = at_k(from + 1) / kStages & 1;
+                uint32_t sv = at_v(from) % kStages, pv = at_v(from) / kStages & 1;
+                for (int i = from; i < n && ok; ++i) {
+                    const bool more = i + 1 < n;
+                    if (i == n - 1) sv = at_v(i) % kStages, pv = at_v(i) / kStages & 1;
+                    if (more && !(ok = wait_warp(&t.full[sk], pk, abort_flag, a.err))) break;
+                    if (!(ok = wait_warp(&t.full[sv], pv, abort_flag, a.err))) break;
+                    if (i < 2 && !(ok = wait_warp(&t.v_ok[i], 0, abort_flag, a.err))) break;
+                    if (!(ok = wait_warp(&t.p_full[x], (uint32_t)((i - from) & 1), abort_flag, a.err))) break;
+                    // the tiles take turns, tile 1 first
+                    if (two && (x == 0 || i > 0) &&
+                        !(ok = wait_warp(&t.turn[x], (uint32_t)((i - 1) & 1), abort_flag, a.err)))
+                        break;
+                    tc_after();
+                    const uint64_t dv = dv0 + sv * kStep;
 #pragma unroll
                     for (int k = 0; k < kTile / 16; ++k)
-                        mma_ts(tmem + kColO + x * D, tmem + kColS + x * kTile + k * 8, sdesc(vb + k * 2048, C::kBlock),
-                               idesc(D, true), i > from || k > 0);
-                    mma_commit(&t.o_done[x]);
+                        mma_ts(to, ts + k * 8, dv + k * (2048 >> 4), idesc(D, true), i > from || k > 0, lead);
+                    mma_commit(saddr(&t.o_done[x]), lead);
                     // writes over the P that the product above reads: one thread's MMAs run in the order of issue
-                    if (more) issue_s(x, i + 1);
+                    if (more) issue_s(sk);
+                    if (two && lead) mbar_arrive(&t.turn[1 - x]);
+                    mma_commit(saddr(&t.empty[sv]), lead);
+                    if (more) mma_commit(saddr(&t.empty[sk]), lead);
+                    sk += 2, sv += 2;
+                    if (sk >= kStages) sk -= kStages, pk ^= 1;
+                    if (sv >= kStages) sv -= kStages, pv ^= 1;
                 }
-                if (!ok) break;
-                mma_commit(&t.empty[vp % kStages]);
-                if (more) mma_commit(&t.empty[kp % kStages]);
             }
-            mma_commit(&t.drained);
+            mma_commit(saddr(&t.drained), lead);
             drain_phase(&t.drained, 0);
-        } else if (warp >= 2) {
+        } else if (warp == 3) {
             // ---- V tiles of the first two steps: NaN and infinities to zero ----
             for (int i = 0; i < 2 && i < n; ++i) {
                 const int vp = at_v(i);
                 if (!wait_phase(&t.full[vp % kStages], (uint32_t)((vp / kStages) & 1), abort_flag, a.err)) break;
                 uint4* const tile = reinterpret_cast<uint4*>(ring + (vp % kStages) * C::kBytes);
                 bool odd = false;
-                for (int e = (warp - 2) * 32 + lane; e < C::kBytes / 16; e += 64) {
+                #pragma unroll 4
+                for (int e = lane; e < C::kBytes / 16; e += 32) {
                     uint4 w = tile[e];
                     uint32_t u[4] = {w.x, w.y, w.z, w.w}, hit = 0;
 #pragma unroll
@@ -381,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
     // ---- softmax: one row per thread ----
     const int x = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
-    const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t lane_base = kTmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t ts = lane_base + kColS + x * kTile, to = lane_base + kColO + x * D;
     const int from = x == 0 ? skip0 : 0;
     const int steps = x == 1 && !two ? 0 : n - from;
