@@ -164,26 +164,30 @@ __host__ __device__ constexpr uint32_t idesc(int n, bool b_mn) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
            ((uint32_t)(kTile >> 4) << 24);
 }
-// Shared-memory descriptor, 128-byte swizzle.  K-major: groups of 8 rows 1024 bytes apart.  MN-major: groups
-// of 8 K rows 1024 bytes apart (stride offset), blocks of 64 columns one tile block apart (leading offset).
-__device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t leading) {
-    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(leading >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+// Shared-memory descriptors, 128-byte swizzle: the low word holds the address and the leading offset, the high
+// word the stride offset (1024 bytes), version and swizzle.  K-major: groups of 8 rows 1024 bytes apart.  MN-major:
+// groups of 8 K rows 1024 bytes apart (stride offset), blocks of 64 columns one tile block apart (leading offset).
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t leading) {
+    return ((addr & 0x3FFFFu) >> 4) | ((leading >> 4) << 16);
 }
+// v, the same in every lane, in a uniform register: MMA operands that come from ordinary registers cost a move of
+// about 10 cycles each, four for an MMA of 64.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __reduce_max_sync(0xffffffffu, v); }
 // MMAs and commits are issued by the lane whose `lead` is set; the operands are computed by the whole warp, so
 // that they stay in uniform registers.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accum, uint32_t lead) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t accum, uint32_t lead) {
     asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(id), "r"(accum), "r"(lead)
+        "{\n .reg .pred p, q;\n .reg .b64 x, y;\n mov.b64 x, {%1, %6};\n mov.b64 y, {%2, %6};\n setp.ne.b32 p, %4, 0;\n"
+        " setp.ne.b32 q, %5, 0;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(id), "r"(accum), "r"(lead), "n"(kDescHigh)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t accum, uint32_t lead) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t accum, uint32_t lead) {
     asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-        "r"(a), "l"(b), "r"(id), "r"(accum), "r"(lead)
+        "{\n .reg .pred p, q;\n .reg .b64 y;\n mov.b64 y, {%2, %6};\n setp.ne.b32 p, %4, 0;\n"
+        " setp.ne.b32 q, %5, 0;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(id), "r"(accum), "r"(lead), "n"(kDescHigh)
         : "memory");
 }
 __device__ __forceinline__ void mma_commit(uint32_t bar, uint32_t lead) {
@@ -215,6 +219,75 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Place in the ring of step i's K and V tile: K0, K1, V0, K2, V1, ..., V(n-1).
+__device__ __forceinline__ int at_k(int i) { return i == 0 ? 0 : 2 * i - 1; }
+__device__ __forceinline__ int at_v(int i, int n) { return i == n - 1 ? 2 * n - 1 : 2 * i + 2; }
+
+// ---- MMAs: a warp per tile -------------------------------------------------
+// Two issuers on two SM sub-partitions: what one spends on barriers, between the softmax's instructions, passes
+// while the other's products run.  They take turns, so that one tile's products run beside the other's softmax.
+template <int D, int X>
+__device__ __forceinline__ void issue_tile(typename Cfg<D>::Tail& t, const uint8_t* sq, const uint8_t* ring, int n, bool two,
+                                           int lane, volatile int* abort_flag, unsigned* err) {
+    using C = Cfg<D>;
+    constexpr uint32_t kStages = C::kStages;
+    const uint32_t lead = lane == 0;
+    if (X == 0 || two) {
+        const int from = X == 0 && two ? 1 : 0;   // the tile's first step
+        const uint32_t q = desc_low(saddr(sq) + X * C::kBytes, 16);
+        constexpr uint32_t ts = kTmem + kColS + X * kTile, to = kTmem + kColO + X * D;
+        auto issue_s = [&](uint32_t k_desc) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                const uint32_t off = ((k >> 2) * C::kBlock + (k & 3) * 32) >> 4;
+                mma_ss(ts, q + off, k_desc + off, idesc(kTile, false), k > 0, lead);
+            }
+            mma_commit(saddr(&t.s_full[X]), lead);
+        };
+        auto k_desc = [&](uint32_t st) { return uniform(desc_low(saddr(ring) + st * C::kBytes, 16)); };
+        auto v_desc = [&](uint32_t st) { return uniform(desc_low(saddr(ring) + st * C::kBytes, C::kBlock)); };
+        if (from == 1 && lead) {                  // the first K and V tile are the other tile's alone
+            mbar_arrive(&t.empty[0]);
+            mbar_arrive(&t.empty[at_v(0, n) % kStages]);
+        }
+        bool ok = wait_warp(&t.q_full, 0, abort_flag, err) && wait_warp(&t.full[at_k(from)], 0, abort_flag, err);
+        if (ok) {
+            tc_after();
+            issue_s(k_desc(at_k(from)));
+            mma_commit(saddr(&t.empty[at_k(from)]), lead);
+        }
+        // stages and phases of the tiles of step i: K(i + 1), V(i)
+        uint32_t sk = at_k(from + 1) % kStages, pk = at_k(from + 1) / kStages & 1;
+        uint32_t sv = at_v(from, n) % kStages, pv = at_v(from, n) / kStages & 1;
+        for (int i = from; i < n && ok; ++i) {
+            const bool more = i + 1 < n;
+            if (!more) sv = at_v(i, n) % kStages, pv = at_v(i, n) / kStages & 1;
+            const uint32_t kd = k_desc(sk), vd = v_desc(sv);
+            if (more && !(ok = wait_warp(&t.full[sk], pk, abort_flag, err))) break;
+            if (!(ok = wait_warp(&t.full[sv], pv, abort_flag, err))) break;
+            if (i < 2 && !(ok = wait_warp(&t.v_ok[i], 0, abort_flag, err))) break;
+            if (!(ok = wait_warp(&t.p_full[X], (uint32_t)((i - from) & 1), abort_flag, err))) break;
+            // the tiles' turns, tile 1 first
+            if (two && (X == 0 || i > 0) && !(ok = wait_warp(&t.turn[X], (uint32_t)((i - 1) & 1), abort_flag, err))) break;
+            tc_after();
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k)
+                mma_ts(to, ts + k * 8, vd + k * (2048 >> 4), idesc(D, true), i > from || k > 0, lead);
+            mma_commit(saddr(&t.o_done[X]), lead);
+            // writes over the P that the product above reads: one thread's MMAs run in the order of issue
+            if (more) issue_s(kd);
+            if (two && lead) mbar_arrive(&t.turn[1 - X]);
+            mma_commit(saddr(&t.empty[sv]), lead);
+            if (more) mma_commit(saddr(&t.empty[sk]), lead);
+            sk += 2, sv += 2;
+            if (sk >= kStages) sk -= kStages, pk ^= 1;
+            if (sv >= kStages) sv -= kStages, pv ^= 1;
+        }
+    }
+    mma_commit(saddr(&t.drained), lead);
+    drain_phase(&t.drained, 0);
+}
 
 // ---- the kernel ------------------------------------------------------------
 
@@ -277,10 +350,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_after();
     const uint32_t tmem = t.tmem;
 
-    // Place in the ring of step i's K and V tile: K0, K1, V0, K2, V1, ..., V(n-1).
-    auto at_k = [](int i) { return i == 0 ? 0 : 2 * i - 1; };
-    auto at_v = [n](int i) { return i == n - 1 ? 2 * n - 1 : 2 * i + 2; };
-
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
         if (warp == 0 && lane == 0) {
@@ -303,74 +372,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             drain_phase(&t.q_full, 0);
             for (int pos = done > kStages ? done - kStages : 0; pos < done; ++pos)
                 drain_phase(&t.full[pos % kStages], (uint32_t)((pos / kStages) & 1));
-        } else if (warp == 1 || warp == 2) {
-            // ---- MMAs: a warp per tile ----
-            // Two issuers on two SM sub-partitions: what one spends on barriers and descriptors, between the
-            // softmax's instructions, passes while the other's products run (one issuer for both tiles kept the
-            // tensor pipe 56% busy).
-            const int x = warp - 1;
-            const uint32_t lead = lane == 0;
-            if (x == 0 || two) {
-                const int from = x == 0 ? skip0 : 0;  // the tile's first step
-                const uint64_t dq = sdesc(saddr(sq) + x * C::kBytes, 16);
-                const uint64_t dk0 = sdesc(saddr(ring), 16), dv0 = sdesc(saddr(ring), C::kBlock);
-                constexpr uint32_t kStep = C::kBytes >> 4;  // a stage, in a descriptor's address units
-                const uint32_t ts = kTmem + kColS + x * kTile, to = kTmem + kColO + x * D;
-                auto issue_s = [&](uint32_t st) {
-                    const uint64_t dk = dk0 + st * kStep;
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t off = ((k >> 2) * C::kBlock + (k & 3) * 32) >> 4;
-                        mma_ss(ts, dq + off, dk + off, idesc(kTile, false), k > 0, lead);
-                    }
-                    mma_commit(saddr(&t.s_full[x]), lead);
-                };
-                if (from == 1 && lead) {              // the first K and V tile are the other tile's alone
-                    mbar_arrive(&t.empty[0]);
-                    mbar_arrive(&t.empty[at_v(0) % kStages]);
-                }
-                bool ok = wait_warp(&t.q_full, 0, abort_flag, a.err) && wait_warp(&t.full[at_k(from)], 0, abort_flag, a.err);
-                if (ok) {
-                    tc_after();
-                    issue_s(at_k(from));
-                    mma_commit(saddr(&t.empty[at_k(from)]), lead);
-                }
-                // stages and phases of the tiles of step i: K(i + 1), V(i)
-                uint32_t sk = at_k(from + 1) % kStages, pk = at_k(from + 1) / kStages & 1;
-                uint32_t sv = at_v(from) % kStages, pv = at_v(from) / kStages & 1;
-                for (int i = from; i < n && ok; ++i) {
-                    const bool more = i + 1 < n;
-                    if (i == n - 1) sv = at_v(i) % kStages, pv = at_v(i) / kStages & 1;
-                    if (more && !(ok = wait_warp(&t.full[sk], pk, abort_flag, a.err))) break;
-                    if (!(ok = wait_warp(&t.full[sv], pv, abort_flag, a.err))) break;
-                    if (i < 2 && !(ok = wait_warp(&t.v_ok[i], 0, abort_flag, a.err))) break;
-                    if (!(ok = wait_warp(&t.p_full[x], (uint32_t)((i - from) & 1), abort_flag, a.err))) break;
-                    // the tiles take turns, tile 1 first
-                    if (two && (x == 0 || i > 0) &&
-                        !(ok = wait_warp(&t.turn[x], (uint32_t)((i - 1) & 1), abort_flag, a.err)))
-                        break;
-                    tc_after();
-                    const uint64_t dv = dv0 + sv * kStep;
-#pragma unroll
-                    for (int k = 0; k < kTile / 16; ++k)
-                        mma_ts(to, ts + k * 8, dv + k * (2048 >> 4), idesc(D, true), i > from || k > 0, lead);
-                    mma_commit(saddr(&t.o_done[x]), lead);
-                    // writes over the P that the product above reads: one thread's MMAs run in the order of issue
-                    if (more) issue_s(sk);
-                    if (two && lead) mbar_arrive(&t.turn[1 - x]);
-                    mma_commit(saddr(&t.empty[sv]), lead);
-                    if (more) mma_commit(saddr(&t.empty[sk]), lead);
-                    sk += 2, sv += 2;
-                    if (sk >= kStages) sk -= kStages, pk ^= 1;
-                    if (sv >= kStages) sv -= kStages, pv ^= 1;
-                }
-            }
-            mma_commit(saddr(&t.drained), lead);
-            drain_phase(&t.drained, 0);
+        } else if (warp == 1) {
+            issue_tile<D, 0>(t, sq, ring, n, two, lane, abort_flag, a.err);
+        } else if (warp == 2) {
+            issue_tile<D, 1>(t, sq, ring, n, two, lane, abort_flag, a.err);
         } else if (warp == 3) {
             // ---- V tiles of the first two steps: NaN and infinities to zero ----
             for (int i = 0; i < 2 && i < n; ++i) {
-                const int vp = at_v(i);
+                const int vp = at_v(i, n);
                 if (!wait_phase(&t.full[vp % kStages], (uint32_t)((vp / kStages) & 1), abort_flag, a.err)) break;
                 uint4* const tile = reinterpret_cast<uint4*>(ring + (vp % kStages) * C::kBytes);
                 bool odd = false;
