@@ -76,7 +76,7 @@ struct Cfg {
     static constexpr int kBytes = D / 64 * kBlock;         // one tile of Q, K or V
     static constexpr int kStages = 5;                      // K and V tiles share the ring
     struct Tail {
-        uint64_t q_full, full[kStages], empty[kStages], s_full[2], p_full[2], o_done[2], v_ok[2], turn[2], drained;
+        uint64_t q_full, full[kStages], empty[kStages], s_full[2], p_full[2][2], o_done[2], v_ok[2], turn[2], drained;
         uint32_t tmem;
         int abort_flag, odd_v;
     };
@@ -237,10 +237,12 @@ __device__ __forceinline__ void issue_tile(typename Cfg<D>::Tail& t, const uint8
         const int from = X == 0 && two ? 1 : 0;   // the tile's first step
         const uint32_t q = desc_low(saddr(sq) + X * C::kBytes, 16);
         constexpr uint32_t ts = kTmem + kColS + X * kTile, to = kTmem + kColO + X * D;
-        auto issue_s = [&](uint32_t k_desc) {
+        auto issue_s = [&](uint32_t k_desc, bool pass) {
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 const uint32_t off = ((k >> 2) * C::kBlock + (k & 3) * 32) >> 4;
+                // the other tile's turn: its issuer is under way while the last of these are issued
+                if (k == D / 32 && pass && lead) mbar_arrive(&t.turn[1 - X]);
                 mma_ss(ts, q + off, k_desc + off, idesc(kTile, false), k > 0, lead);
             }
             mma_commit(saddr(&t.s_full[X]), lead);
@@ -254,7 +256,7 @@ __device__ __forceinline__ void issue_tile(typename Cfg<D>::Tail& t, const uint8
         bool ok = wait_warp(&t.q_full, 0, abort_flag, err) && wait_warp(&t.full[at_k(from)], 0, abort_flag, err);
         if (ok) {
             tc_after();
-            issue_s(k_desc(at_k(from)));
+            issue_s(k_desc(at_k(from)), false);
             mma_commit(saddr(&t.empty[at_k(from)]), lead);
         }
         // stages and phases of the tiles of step i: K(i + 1), V(i)
@@ -264,22 +266,29 @@ __device__ __forceinline__ void issue_tile(typename Cfg<D>::Tail& t, const uint8
             const bool more = i + 1 < n;
             if (!more) sv = at_v(i, n) % kStages, pv = at_v(i, n) / kStages & 1;
             const uint32_t kd = k_desc(sk), vd = v_desc(sv);
-            if (more && !(ok = wait_warp(&t.full[sk], pk, abort_flag, err))) break;
-            if (!(ok = wait_warp(&t.full[sv], pv, abort_flag, err))) break;
-            if (i < 2 && !(ok = wait_warp(&t.v_ok[i], 0, abort_flag, err))) break;
-            if (!(ok = wait_warp(&t.p_full[X], (uint32_t)((i - from) & 1), abort_flag, err))) break;
+            if (more) ok = wait_phase(&t.full[sk], pk, abort_flag, err) && ok;
+            ok = wait_phase(&t.full[sv], pv, abort_flag, err) && ok;
+            if (i < 2) ok = wait_phase(&t.v_ok[i], 0, abort_flag, err) && ok;
             // the tiles' turns, tile 1 first
-            if (two && (X == 0 || i > 0) && !(ok = wait_warp(&t.turn[X], (uint32_t)((i - 1) & 1), abort_flag, err))) break;
+            if (two && (X == 0 || i > 0)) ok = wait_phase(&t.turn[X], (uint32_t)((i - 1) & 1), abort_flag, err) && ok;
+            ok = wait_phase(&t.p_full[X][0], (uint32_t)((i - from) & 1), abort_flag, err) && ok;
             tc_after();
 #pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)
+            for (int k = 0; k < kTile / 32; ++k)
                 mma_ts(to, ts + k * 8, vd + k * (2048 >> 4), idesc(D, true), i > from || k > 0, lead);
-            mma_commit(saddr(&t.o_done[X]), lead);
+            ok = wait_phase(&t.p_full[X][1], (uint32_t)((i - from) & 1), abort_flag, err) && ok;
+            tc_after();
+#pragma unroll
+            for (int k = kTile / 32; k < kTile / 16; ++k) mma_ts(to, ts + k * 8, vd + k * (2048 >> 4), idesc(D, true), 1, lead);
             // writes over the P that the product above reads: one thread's MMAs run in the order of issue
-            if (more) issue_s(kd);
-            if (two && lead) mbar_arrive(&t.turn[1 - X]);
+            if (more)
+                issue_s(kd, two);  // its commit covers the product above too
+            else
+                mma_commit(saddr(&t.o_done[X]), lead);
+            if (!more && two && lead) mbar_arrive(&t.turn[1 - X]);
             mma_commit(saddr(&t.empty[sv]), lead);
             if (more) mma_commit(saddr(&t.empty[sk]), lead);
+            ok = __all_sync(0xffffffffu, ok);  // one answer for the warp's lanes
             sk += 2, sv += 2;
             if (sk >= kStages) sk -= kStages, pk ^= 1;
             if (sv >= kStages) sv -= kStages, pv ^= 1;
@@ -331,7 +340,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kStages; ++i) mbar_init(&t.full[i], 1), mbar_init(&t.empty[i], two ? 2 : 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&t.s_full[i], 1);
-            mbar_init(&t.p_full[i], 4);
+            mbar_init(&t.p_full[i][0], 4);
+            mbar_init(&t.p_full[i][1], 4);
             mbar_init(&t.o_done[i], 1);
             mbar_init(&t.v_ok[i], 1);
             mbar_init(&t.turn[i], 1);
@@ -454,8 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float next = fmaxf(ref, top), f = ex2(ref - next);
             ref = next;
             sum.x *= f, sum.y *= f;
-            if (!(ok = wait_warp(&t.o_done[x], (uint32_t)((k - 1) & 1), abort_flag, a.err))) break;
-            tc_after();
+            // (the commit that brought this S came after the last step's product: O is at rest)
 #pragma unroll
             for (int b = 0; b < D / 32; ++b) {
                 uint32_t o[32];
@@ -467,23 +476,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         const float2 sc2 = make_float2(sc, sc), nr = make_float2(-ref, -ref);
-        uint32_t p[kTile / 2];
+        // in two halves, so that the product with V starts on the first while the second is worked out
 #pragma unroll
-        for (int c = 0; c < kTile / 2; ++c) {
-            const float2 y = __ffma2_rn(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), sc2, nr);
-            const float2 e = make_float2(ex2(y.x), ex2(y.y));
-            sum = __fadd2_rn(sum, e);
-            p[c] = pack_bf16(e.x, e.y);
+        for (int half = 0; half < 2; ++half) {
+            uint32_t p[kTile / 4];
+#pragma unroll
+            for (int c = 0; c < kTile / 4; ++c) {
+                const int e0 = half * (kTile / 2) + 2 * c;
+                const float2 y = __ffma2_rn(make_float2(__uint_as_float(s[e0]), __uint_as_float(s[e0 + 1])), sc2, nr);
+                const float2 e = make_float2(ex2(y.x), ex2(y.y));
+                sum = __fadd2_rn(sum, e);
+                p[c] = pack_bf16(e.x, e.y);
+            }
+            tmem_st32(ts + 32 * half, p);
+            tmem_wait_st();
+            tc_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&t.p_full[x][half]);
         }
-        tmem_st32(ts, p);
-        tmem_st32(ts + 32, p + 32);
-        tmem_wait_st();
-        tc_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&t.p_full[x]);
     }
     // ---- output ----
-    if (ok && steps > 0) ok = wait_warp(&t.o_done[x], (uint32_t)((steps - 1) & 1), abort_flag, a.err);
+    if (ok && steps > 0) ok = wait_warp(&t.o_done[x], 0, abort_flag, a.err);
     if (ok && steps > 0) {
         tc_after();
         bool odd = false;
