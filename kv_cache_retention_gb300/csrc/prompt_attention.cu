@@ -5,7 +5,7 @@
 //   out = sum_j p_j v_j / sum_j p_j,  p_j = 2^(scale log2e q_i . k_j - ref),
 //   lse = ln sum_j e^(scale q_i . k_j).
 //
-// A block takes one query head and 256 consecutive rows of one sequence, as two tiles
+// A unit of work is one query head and 256 consecutive rows of one sequence, as two tiles
 // of 128 rows (TMEM lanes), and goes once over the keys from the diagonal down, 128 at
 // a time:
 //   S = Q K^T   tcgen05.mma, both operands from shared memory, 128 fp32 columns a tile
@@ -75,10 +75,17 @@ struct Cfg {
     static constexpr int kBlock = kTile * 128;             // 128 rows x 64 dims, 128-byte swizzled
     static constexpr int kBytes = D / 64 * kBlock;         // one tile of Q, K or V
     static constexpr int kStages = 5;                      // K and V tiles share the ring
+    // A unit of work, as warp 3 hands it out; n == 0: there are no more.
+    struct Unit {
+        int first, len, row0, head, n;
+    };
     struct Tail {
-        uint64_t q_full, full[kStages], empty[kStages], s_full[2], p_full[2][2], o_done[2], v_ok[2], turn[2], drained;
+        uint4 claimed;  // the answer of a claim
+        uint64_t q_full, q_empty, full[kStages], empty[kStages], s_full[2], p_full[2][2], o_done[2], o_free[2], v_ok[2][2],
+            turn[2], unit_full[2], unit_empty[2], claim, drained;
         uint32_t tmem;
-        int abort_flag, odd_v;
+        int abort_flag, odd_v[2];
+        Unit unit[2];
     };
     static constexpr size_t kSmem = (size_t)(2 + kStages) * kBytes + sizeof(Tail) + 1024;
     static_assert(kSmem <= 232448, "shared memory per block");
@@ -227,75 +234,163 @@ __device__ __forceinline__ int at_v(int i, int n) { return i == n - 1 ? 2 * n - 
 // ---- MMAs: a warp per tile -------------------------------------------------
 // Two issuers on two SM sub-partitions: what one spends on barriers, between the softmax's instructions, passes
 // while the other's products run.  They take turns, so that one tile's products run beside the other's softmax.
-template <int D, int X>
-__device__ __forceinline__ void issue_tile(typename Cfg<D>::Tail& t, const uint8_t* sq, const uint8_t* ring, int n, bool two,
-                                           int lane, volatile int* abort_flag, unsigned* err) {
+// One copy of the code for both, and one of each run of MMAs: with a copy per tile the kernel's loops passed the
+// instruction cache (4096 tokens: 135 us).
+template <int D>
+__device__ __forceinline__ void issue_tiles(typename Cfg<D>::Tail& t, const uint8_t* sq, const uint8_t* ring, int tile, int lane,
+                                            volatile int* abort_flag, unsigned* err) {
     using C = Cfg<D>;
     constexpr uint32_t kStages = C::kStages;
-    const uint32_t lead = lane == 0;
-    if (X == 0 || two) {
-        const int from = X == 0 && two ? 1 : 0;   // the tile's first step
-        const uint32_t q = desc_low(saddr(sq) + X * C::kBytes, 16);
-        constexpr uint32_t ts = kTmem + kColS + X * kTile, to = kTmem + kColO + X * D;
-        auto issue_s = [&](uint32_t k_desc, bool pass) {
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                const uint32_t off = ((k >> 2) * C::kBlock + (k & 3) * 32) >> 4;
-                // the other tile's turn: its issuer is under way while the last of these are issued
-                if (k == D / 32 && pass && lead) mbar_arrive(&t.turn[1 - X]);
-                mma_ss(ts, q + off, k_desc + off, idesc(kTile, false), k > 0, lead);
-            }
-            mma_commit(saddr(&t.s_full[X]), lead);
+    const uint32_t lead = lane == 0, X = uniform(tile);
+    const uint32_t q = uniform(desc_low(saddr(sq) + X * C::kBytes, 16));
+    const uint32_t ts = uniform(kTmem + kColS + X * kTile), to = uniform(kTmem + kColO + X * D);
+    auto desc = [&](uint32_t st, uint32_t leading) { return uniform(desc_low(saddr(ring) + st * C::kBytes, leading)); };
+    uint32_t base = 0, steps = 0, turns = 0, mine = 0;  // ring places and this tile's steps, turns and units so far
+    bool ok = true;
+    for (uint32_t u = 0; ok; ++u) {
+        if (!(ok = wait_warp(&t.unit_full[u & 1], (u >> 1) & 1, abort_flag, err))) break;
+        const int n = t.unit[u & 1].n;
+        const bool two = t.unit[u & 1].row0 + kTile < t.unit[u & 1].len;
+        __syncwarp();
+        if (lead) mbar_arrive(&t.unit_empty[u & 1]);
+        if (n == 0) break;
+        if (X == 1 && !two) {                         // tile 0's issuer releases everything
+            base += 2 * n;
+            continue;
+        }
+        const int from = X == 0 && two ? 1 : 0;       // the tile's first step
+        const uint32_t releases = X == 0 && !two ? 2 : 1;
+        auto release = [&](uint64_t* b) {             // every barrier of this kind counts both tiles
+            mma_commit(saddr(b), lead);
+            if (releases == 2) mma_commit(saddr(b), lead);
         };
-        auto k_desc = [&](uint32_t st) { return uniform(desc_low(saddr(ring) + st * C::kBytes, 16)); };
-        auto v_desc = [&](uint32_t st) { return uniform(desc_low(saddr(ring) + st * C::kBytes, C::kBlock)); };
-        if (from == 1 && lead) {                  // the first K and V tile are the other tile's alone
-            mbar_arrive(&t.empty[0]);
-            mbar_arrive(&t.empty[at_v(0, n) % kStages]);
-        }
-        bool ok = wait_warp(&t.q_full, 0, abort_flag, err) && wait_warp(&t.full[at_k(from)], 0, abort_flag, err);
-        if (ok) {
-            tc_after();
-            issue_s(k_desc(at_k(from)), false);
-            mma_commit(saddr(&t.empty[at_k(from)]), lead);
-        }
-        // stages and phases of the tiles of step i: K(i + 1), V(i)
-        uint32_t sk = at_k(from + 1) % kStages, pk = at_k(from + 1) / kStages & 1;
-        uint32_t sv = at_v(from, n) % kStages, pv = at_v(from, n) / kStages & 1;
-        for (int i = from; i < n && ok; ++i) {
-            const bool more = i + 1 < n;
-            if (!more) sv = at_v(i, n) % kStages, pv = at_v(i, n) / kStages & 1;
-            const uint32_t kd = k_desc(sk), vd = v_desc(sv);
+        ok = wait_phase(&t.q_full, u & 1, abort_flag, err);
+        // Round i: O += P V of step i (not in the first round, i = from - 1), then S of step i + 1 (not in the last).
+        // Stages and phases of its tiles, K(i + 1) and V(i):
+        uint32_t at = base + at_k(from);
+        uint32_t sk = at % kStages, pk = at / kStages & 1, sv = 0, pv = 0;
+        for (int i = from - 1; i < n && ok; ++i) {
+            const bool more = i + 1 < n, first = i < from;
+            if (first || i == from || !more) {        // the places' step is 2 in between
+                at = base + at_v(max(i, 0), n), sv = at % kStages, pv = at / kStages & 1;
+                at = base + at_k(i + 1), sk = at % kStages, pk = at / kStages & 1;
+            }
+            const uint32_t kd = desc(sk, 16), vd = desc(sv, C::kBlock);
             if (more) ok = wait_phase(&t.full[sk], pk, abort_flag, err) && ok;
-            ok = wait_phase(&t.full[sv], pv, abort_flag, err) && ok;
-            if (i < 2) ok = wait_phase(&t.v_ok[i], 0, abort_flag, err) && ok;
-            // the tiles' turns, tile 1 first
-            if (two && (X == 0 || i > 0)) ok = wait_phase(&t.turn[X], (uint32_t)((i - 1) & 1), abort_flag, err) && ok;
-            ok = wait_phase(&t.p_full[X][0], (uint32_t)((i - from) & 1), abort_flag, err) && ok;
-            tc_after();
+            if (!first) {
+                ok = wait_phase(&t.full[sv], pv, abort_flag, err) && ok;
+                if (i < 2) ok = wait_phase(&t.v_ok[u & 1][i], (u >> 1) & 1, abort_flag, err) && ok;
+                if (i == from && mine) ok = wait_phase(&t.o_free[X], (mine - 1) & 1, abort_flag, err) && ok;
+                // the tiles' turns, tile 1 first
+                if (two && (X == 0 || i > 0)) ok = wait_phase(&t.turn[X], turns++ & 1, abort_flag, err) && ok;
+                ok = wait_phase(&t.p_full[X][0], steps & 1, abort_flag, err) && ok;
+                tc_after();
 #pragma unroll
-            for (int k = 0; k < kTile / 32; ++k)
-                mma_ts(to, ts + k * 8, vd + k * (2048 >> 4), idesc(D, true), i > from || k > 0, lead);
-            ok = wait_phase(&t.p_full[X][1], (uint32_t)((i - from) & 1), abort_flag, err) && ok;
-            tc_after();
+                for (int k = 0; k < kTile / 32; ++k)
+                    mma_ts(to, ts + k * 8, vd + k * (2048 >> 4), idesc(D, true), i > from || k > 0, lead);
+                ok = wait_phase(&t.p_full[X][1], steps & 1, abort_flag, err) && ok;
+                tc_after();
 #pragma unroll
-            for (int k = kTile / 32; k < kTile / 16; ++k) mma_ts(to, ts + k * 8, vd + k * (2048 >> 4), idesc(D, true), 1, lead);
-            // writes over the P that the product above reads: one thread's MMAs run in the order of issue
-            if (more)
-                issue_s(kd, two);  // its commit covers the product above too
-            else
+                for (int k = kTile / 32; k < kTile / 16; ++k)
+                    mma_ts(to, ts + k * 8, vd + k * (2048 >> 4), idesc(D, true), 1, lead);
+                ++steps;
+            } else {
+                tc_after();
+            }
+            if (more) {
+                const bool pass = two && !first && lead;
+                // writes over the P that the product above reads: one thread's MMAs run in the order of issue
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = ((k >> 2) * C::kBlock + (k & 3) * 32) >> 4;
+                    // the other tile's turn: its issuer is under way while the last of these are issued
+                    if (k == D / 32 && pass) mbar_arrive(&t.turn[X ^ 1]);
+                    mma_ss(ts, q + off, kd + off, idesc(kTile, false), k > 0, lead);
+                }
+                mma_commit(saddr(&t.s_full[X]), lead);  // covers the product above too
+                if (i + 2 == n) release(&t.q_empty);
+                release(&t.empty[sk]);
+            } else {
+                if (X == 0 && two && lead) mbar_arrive(&t.turn[1]);
                 mma_commit(saddr(&t.o_done[X]), lead);
-            if (!more && two && lead) mbar_arrive(&t.turn[1 - X]);
-            mma_commit(saddr(&t.empty[sv]), lead);
-            if (more) mma_commit(saddr(&t.empty[sk]), lead);
+            }
+            if (!first) {
+                release(&t.empty[sv]);
+            } else if (from == 1) {                   // the first K and V tile are the other tile's alone
+                for (int k = 0; k < 2; ++k) {
+                    at = base + (k ? at_v(0, n) : 0);
+                    const uint32_t st = at % kStages;
+                    ok = wait_phase(&t.full[st], at / kStages & 1, abort_flag, err) && ok;
+                    if (lead) mbar_arrive(&t.empty[st]);
+                }
+            }
             ok = __all_sync(0xffffffffu, ok);  // one answer for the warp's lanes
             sk += 2, sv += 2;
             if (sk >= kStages) sk -= kStages, pk ^= 1;
             if (sv >= kStages) sv -= kStages, pv ^= 1;
         }
+        base += 2 * n;
+        ++mine;
     }
     mma_commit(saddr(&t.drained), lead);
     drain_phase(&t.drained, 0);
+}
+
+// ---- units of work ---------------------------------------------------------
+// Block b's unit: query head b % Hq and a row tile of 256 rows of one sequence.  Row tiles are numbered by their
+// sequence's start: sequence s has the numbers from cu[s] / 256 + s on, which leaves it at least ceil(length / 256) of
+// them (some stay empty); the last numbers come first, a sequence's longest rows before its others.  n = 0: no rows.
+template <int D>
+__device__ __forceinline__ typename Cfg<D>::Unit unit_of(const PromptArgs& a, uint32_t block, int lane) {
+    const int number = a.n_virtual - 1 - (int)(block / a.Hq);
+    int lo = 0, size = a.S;                       // the last sequence whose first number is not above lies in [lo, lo + size)
+    while (size > 1) {
+        const int piece = (size + 31) / 32, i = lane * piece;
+        const bool below = i < size && (lane == 0 || __ldg(a.cu + lo + i) / kUnit + lo + i <= number);
+        const int last = 31 - __clz(__ballot_sync(0xffffffffu, below));
+        lo += last * piece;
+        size = min(piece, size - last * piece);
+    }
+    typename Cfg<D>::Unit w;
+    w.first = __ldg(a.cu + lo);
+    w.len = min(__ldg(a.cu + lo + 1), a.T) - w.first;
+    const int tile = number - (w.first / kUnit + lo);
+    w.row0 = tile * kUnit;
+    w.head = (int)(block % a.Hq);
+    if (w.first < 0 && lane == 0) atomicOr(a.err, (unsigned)KVSEL_DEV_BAD_LENGTH);
+    const bool rows = w.first >= 0 && tile >= 0 && (int64_t)tile * kUnit < w.len;
+    w.n = !rows ? 0 : 2 * tile + (w.row0 + kTile < w.len ? 2 : 1);
+    return w;
+}
+
+// Asks for a block of the grid that has not been launched; the answer lands in t.claimed.
+template <class Tail>
+__device__ __forceinline__ void claim_start(Tail& t) {
+    mbar_expect_tx(&t.claim, 16);
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     saddr(&t.claimed)),
+                 "r"(saddr(&t.claim))
+                 : "memory");
+}
+// The claim's answer: whether there was a block, and which.
+template <class Tail>
+__device__ __forceinline__ bool claim_next(Tail& t, uint32_t& claims, uint32_t& block, int lane, bool start,
+                                           volatile int* abort_flag, unsigned* err) {
+    if (start && lane == 0) claim_start(t);
+    const bool ok = wait_warp(&t.claim, claims++ & 1, abort_flag, err);
+    if (!ok) drain_phase(&t.claim, (claims - 1) & 1);
+    uint32_t got, id;
+    asm volatile(
+        "{\n .reg .b128 h;\n .reg .pred p;\n ld.shared.b128 h, [%2];\n"
+        " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n selp.u32 %0, 1, 0, p;\n mov.u32 %1, 0;\n"
+        " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n}\n"
+        : "=r"(got), "=r"(id)
+        : "r"(saddr(&t.claimed))
+        : "memory");
+    __syncwarp();
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // read before the next answer is written
+    block = id;
+    return ok && got;
 }
 
 // ---- the kernel ------------------------------------------------------------
@@ -314,40 +409,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int* const abort_flag = &t.abort_flag;
 
-    // The block's rows.  Row tiles are numbered by their sequence's start: sequence s has the numbers from
-    // cu[s] / 256 + s on, which leaves it at least ceil(length / 256) of them (some stay empty); long rows first.
-    const int head = blockIdx.x % a.Hq, g = head / (a.Hq / a.Hkv);
-    const int number = a.n_virtual - 1 - (int)(blockIdx.x / a.Hq);
-    int lo = 0, hi = a.S;                         // the last sequence whose first number is not above
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (__ldg(a.cu + mid) / kUnit + mid <= number) lo = mid; else hi = mid;
-    }
-    const int first = __ldg(a.cu + lo), len = min(__ldg(a.cu + lo + 1), a.T) - first;
-    const int unit = number - (first / kUnit + lo);
-    if (first < 0) {
-        if (threadIdx.x == 0) atomicOr(a.err, (unsigned)KVSEL_DEV_BAD_LENGTH);
-        return;
-    }
-    if (unit < 0 || (int64_t)unit * kUnit >= len) return;
-    const int row0 = unit * kUnit;
-    const bool two = row0 + kTile < len;          // the second tile has rows
-    const int n = 2 * unit + (two ? 2 : 1);       // steps; step i takes key tile n - 1 - i
-    const int skip0 = two ? 1 : 0;                // tile 0 starts at step skip0
-
     if (threadIdx.x == 0) {
         mbar_init(&t.q_full, 1);
-        for (int i = 0; i < kStages; ++i) mbar_init(&t.full[i], 1), mbar_init(&t.empty[i], two ? 2 : 1);
+        mbar_init(&t.q_empty, 2);
+        mbar_init(&t.claim, 1);
+        for (int i = 0; i < kStages; ++i) mbar_init(&t.full[i], 1), mbar_init(&t.empty[i], 2);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&t.s_full[i], 1);
             mbar_init(&t.p_full[i][0], 4);
             mbar_init(&t.p_full[i][1], 4);
             mbar_init(&t.o_done[i], 1);
-            mbar_init(&t.v_ok[i], 1);
+            mbar_init(&t.o_free[i], 4);
+            mbar_init(&t.v_ok[i][0], 1);
+            mbar_init(&t.v_ok[i][1], 1);
             mbar_init(&t.turn[i], 1);
+            mbar_init(&t.unit_full[i], 1);
+            mbar_init(&t.unit_empty[i], 1 + 2 + 8);  // the loads, the issuers, the softmax warps
         }
         mbar_init(&t.drained, 2);
-        t.abort_flag = t.odd_v = 0;
+        t.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
@@ -364,55 +444,88 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
         if (warp == 0 && lane == 0) {
             // ---- loads ----
-            mbar_expect_tx(&t.q_full, (two ? 2 : 1) * C::kBytes);
-            for (int x = 0; x < (two ? 2 : 1); ++x)
-                for (int b = 0; b < D / 64; ++b)
-                    tma_load(&map_q, &t.q_full, sq + x * C::kBytes + b * C::kBlock, 64 * b, head, first + row0 + x * kTile);
-            int done = 0;
-            for (int pos = 0; pos < 2 * n; ++pos, ++done) {
-                const bool is_v = pos == 2 * n - 1 || (pos > 0 && pos % 2 == 0);
-                const int i = pos == 2 * n - 1 ? n - 1 : is_v ? pos / 2 - 1 : (pos + 1) / 2;
-                const int st = pos % kStages;
-                if (!wait_phase(&t.empty[st], (uint32_t)((pos / kStages) & 1) ^ 1u, abort_flag, a.err)) break;
-                mbar_expect_tx(&t.full[st], C::kBytes);
-                for (int b = 0; b < D / 64; ++b)
-                    tma_load(is_v ? &map_v : &map_k, &t.full[st], ring + st * C::kBytes + b * C::kBlock, 64 * b, g,
-                             first + (n - 1 - i) * kTile);
-            }
-            drain_phase(&t.q_full, 0);
-            for (int pos = done > kStages ? done - kStages : 0; pos < done; ++pos)
-                drain_phase(&t.full[pos % kStages], (uint32_t)((pos / kStages) & 1));
-        } else if (warp == 1) {
-            issue_tile<D, 0>(t, sq, ring, n, two, lane, abort_flag, a.err);
-        } else if (warp == 2) {
-            issue_tile<D, 1>(t, sq, ring, n, two, lane, abort_flag, a.err);
-        } else if (warp == 3) {
-            // ---- V tiles of the first two steps: NaN and infinities to zero ----
-            for (int i = 0; i < 2 && i < n; ++i) {
-                const int vp = at_v(i, n);
-                if (!wait_phase(&t.full[vp % kStages], (uint32_t)((vp / kStages) & 1), abort_flag, a.err)) break;
-                uint4* const tile = reinterpret_cast<uint4*>(ring + (vp % kStages) * C::kBytes);
-                bool odd = false;
-                #pragma unroll 4
-                for (int e = lane; e < C::kBytes / 16; e += 32) {
-                    uint4 w = tile[e];
-                    uint32_t u[4] = {w.x, w.y, w.z, w.w}, hit = 0;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) hit |= (u[k] & 0x7F807F80u) + 0x00800080u;
-                    if (hit & 0x80008000u) {
-                        odd = true;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            if ((u[k] & 0x7F80u) == 0x7F80u) u[k] &= 0xFFFF0000u;
-                            if ((u[k] & 0x7F800000u) == 0x7F800000u) u[k] &= 0x0000FFFFu;
-                        }
-                        tile[e] = make_uint4(u[0], u[1], u[2], u[3]);
-                    }
+            uint32_t c = 0, loaded_q = 0;  // ring places filled, Q loads
+            bool ok = true;
+            for (uint32_t u = 0; ok; ++u) {
+                if (!(ok = wait_phase(&t.unit_full[u & 1], (u >> 1) & 1, abort_flag, a.err))) break;
+                const typename C::Unit w = t.unit[u & 1];
+                mbar_arrive(&t.unit_empty[u & 1]);
+                if (w.n == 0) break;
+                const int g = w.head / (a.Hq / a.Hkv), tiles = w.row0 + kTile < w.len ? 2 : 1;
+                if (u && !(ok = wait_phase(&t.q_empty, (u - 1) & 1, abort_flag, a.err))) break;
+                mbar_expect_tx(&t.q_full, tiles * C::kBytes);
+                for (int x = 0; x < tiles; ++x)
+                    for (int b = 0; b < D / 64; ++b)
+                        tma_load(&map_q, &t.q_full, sq + x * C::kBytes + b * C::kBlock, 64 * b, w.head, w.first + w.row0 + x * kTile);
+                ++loaded_q;
+                for (int pos = 0; pos < 2 * w.n; ++pos, ++c) {
+                    const bool is_v = pos == 2 * w.n - 1 || (pos > 0 && pos % 2 == 0);
+                    const int i = pos == 2 * w.n - 1 ? w.n - 1 : is_v ? pos / 2 - 1 : (pos + 1) / 2;
+                    const uint32_t st = c % kStages;
+                    if (!(ok = wait_phase(&t.empty[st], (c / kStages & 1) ^ 1u, abort_flag, a.err))) break;
+                    mbar_expect_tx(&t.full[st], C::kBytes);
+                    for (int b = 0; b < D / 64; ++b)
+                        tma_load(is_v ? &map_v : &map_k, &t.full[st], ring + st * C::kBytes + b * C::kBlock, 64 * b, g,
+                                 w.first + (w.n - 1 - i) * kTile);
                 }
-                if (odd) t.odd_v = 1;
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            }
+            if (loaded_q) drain_phase(&t.q_full, (loaded_q - 1) & 1);
+            for (uint32_t pos = c > kStages ? c - kStages : 0; pos < c; ++pos) drain_phase(&t.full[pos % kStages], pos / kStages & 1);
+        } else if (warp == 1 || warp == 2) {
+            issue_tiles<D>(t, sq, ring, warp - 1, lane, abort_flag, a.err);
+        } else if (warp == 3) {
+            // ---- units of work, and the V tiles of each unit's first two steps ----
+            // The block starts with its own unit and then claims those of blocks that have not been launched yet, in
+            // the order of launch, until none is left.
+            uint32_t block = blockIdx.x, base = 0, claims = 0;
+            bool ok = true, any = true;
+            for (uint32_t u = 0; ok; ++u) {
+                typename C::Unit w;
+                w.n = 0;
+                while (any) {
+                    w = unit_of<D>(a, block, lane);
+                    if (w.n) break;
+                    any = claim_next(t, claims, block, lane, true, abort_flag, a.err);
+                }
+                if (u >= 2 && !(ok = wait_warp(&t.unit_empty[u & 1], ((u >> 1) - 1) & 1, abort_flag, a.err))) break;
+                if (lane == 0) {
+                    t.unit[u & 1] = w;
+                    t.odd_v[u & 1] = 0;
+                }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&t.v_ok[i]);
+                if (lane == 0) mbar_arrive(&t.unit_full[u & 1]);
+                if (w.n == 0) break;
+                if (lane == 0) claim_start(t);
+                for (int i = 0; i < 2 && ok; ++i) {  // NaN and infinities to zero
+                    if (i < w.n) {
+                        const uint32_t at = base + at_v(i, w.n), st = at % kStages;
+                        if (!(ok = wait_warp(&t.full[st], at / kStages & 1, abort_flag, a.err))) break;
+                        uint4* const tile = reinterpret_cast<uint4*>(ring + st * C::kBytes);
+                        bool odd = false;
+#pragma unroll 4
+                        for (int e = lane; e < C::kBytes / 16; e += 32) {
+                            const uint4 v = tile[e];
+                            uint32_t x[4] = {v.x, v.y, v.z, v.w}, hit = 0;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) hit |= (x[k] & 0x7F807F80u) + 0x00800080u;
+                            if (hit & 0x80008000u) {
+                                odd = true;
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    if ((x[k] & 0x7F80u) == 0x7F80u) x[k] &= 0xFFFF0000u;
+                                    if ((x[k] & 0x7F800000u) == 0x7F800000u) x[k] &= 0x0000FFFFu;
+                                }
+                                tile[e] = make_uint4(x[0], x[1], x[2], x[3]);
+                            }
+                        }
+                        if (odd) t.odd_v[u & 1] = 1;
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                    }
+                    if (lane == 0) mbar_arrive(&t.v_ok[u & 1][i]);
+                }
+                any = claim_next(t, claims, block, lane, false, abort_flag, a.err);
+                base += 2 * w.n;
             }
         }
         __syncwarp();
@@ -429,14 +542,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int x = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_base = kTmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t ts = lane_base + kColS + x * kTile, to = lane_base + kColO + x * D;
-    const int from = x == 0 ? skip0 : 0;
-    const int steps = x == 1 && !two ? 0 : n - from;
     const float sc = a.scale2;
+    uint32_t done = 0, mine = 0;                      // this tile's steps and units so far
+    bool ok = true;
+    for (uint32_t u = 0; ok; ++u) {
+    if (!(ok = wait_warp(&t.unit_full[u & 1], (u >> 1) & 1, abort_flag, a.err))) break;
+    const typename C::Unit w = t.unit[u & 1];
+    __syncwarp();
+    const bool two = w.row0 + kTile < w.len;
+    const int steps = w.n == 0 || (x == 1 && !two) ? 0 : x == 0 && two ? w.n - 1 : w.n;
     float ref = 0.f;
     float2 sum = make_float2(0.f, 0.f);
-    bool ok = true;
-    for (int k = 0; k < steps; ++k) {
-        if (!(ok = wait_warp(&t.s_full[x], (uint32_t)(k & 1), abort_flag, a.err))) break;
+    for (int k = 0; k < steps; ++k, ++done) {
+        if (!(ok = wait_warp(&t.s_full[x], done & 1, abort_flag, a.err))) break;
         tc_after();
         uint32_t s[kTile];
 #pragma unroll
@@ -465,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ref = next;
             sum.x *= f, sum.y *= f;
             // (the commit that brought this S came after the last step's product: O is at rest)
-#pragma unroll
+#pragma unroll 1
             for (int b = 0; b < D / 32; ++b) {
                 uint32_t o[32];
                 tmem_ld32(to + 32 * b, o);
@@ -496,43 +614,56 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     // ---- output ----
-    if (ok && steps > 0) ok = wait_warp(&t.o_done[x], 0, abort_flag, a.err);
+    if (ok && steps > 0) ok = wait_warp(&t.o_done[x], mine++ & 1, abort_flag, a.err);
     if (ok && steps > 0) {
         tc_after();
-        bool odd = false;
-        for (int i = 0; i < 2 && i < n && ok; ++i) ok = wait_warp(&t.v_ok[i], 0, abort_flag, a.err);
-        odd = *(volatile int*)&t.odd_v != 0;
-        const int row = row0 + x * kTile + r;
+        for (int i = 0; i < 2 && ok; ++i) ok = wait_warp(&t.v_ok[u & 1][i], (u >> 1) & 1, abort_flag, a.err);
+        const bool odd = *(volatile int*)&t.odd_v[u & 1] != 0;
+        const int row = w.row0 + x * kTile + r;
         const float l = sum.x + sum.y, inv = 1.f / l;
-        const int64_t at = (int64_t)(first + row) * a.Hq + head;
-        const int key0 = n > 1 ? (n - 2) * kTile : 0;   // first key of the tiles that were looked over
-#pragma unroll
+        const int64_t at = (int64_t)(w.first + row) * a.Hq + w.head;
+#pragma unroll 1
         for (int b = 0; b < D / 32; ++b) {
             uint32_t o[32];
             tmem_ld32(to + 32 * b, o);
             tmem_wait_ld();
-            if (row >= len) continue;
-            if (odd) {
-                for (int j = key0; j <= row; ++j) {
-                    const __nv_bfloat16* v = a.v + (int64_t)(first + j) * a.v_stride + (int64_t)g * D + 32 * b;
+            if (b == D / 32 - 1) {
+                tc_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&t.o_free[x]);
+            }
+            if (row < w.len) {
+                uint4* const dst = reinterpret_cast<uint4*>(a.out + at * D + 32 * b);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float w = __bfloat162float(v[i]);
-                        if (!(fabsf(w) < INFINITY)) o[i] = __float_as_uint(__uint_as_float(o[i]) + w);
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t e[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        e[k] = pack_bf16(__uint_as_float(o[8 * i + 2 * k]) * inv, __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
+                    dst[i] = make_uint4(e[0], e[1], e[2], e[3]);
                 }
             }
-            uint4* const dst = reinterpret_cast<uint4*>(a.out + at * D + 32 * b);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t w[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    w[e] = pack_bf16(__uint_as_float(o[8 * i + 2 * e]) * inv, __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
-                dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        if (a.lse && row < w.len) a.lse[at] = (ref + log2f(l)) * kLn2;
+        if (odd && row < w.len) {
+            // what the row sees of the values that were set to zero: a sum of infinities and NaN
+            const int key0 = w.n > 1 ? (w.n - 2) * kTile : 0;  // first key of the tiles that were looked over
+            const __nv_bfloat16* v = a.v + (int64_t)(w.first + key0) * a.v_stride + (int64_t)(w.head / (a.Hq / a.Hkv)) * D;
+#pragma unroll 1
+            for (int d = 0; d < D; ++d) {
+                float add = 0.f;
+#pragma unroll 1
+                for (int j = 0; j <= row - key0; ++j) {
+                    const float e = __bfloat162float(v[j * a.v_stride + d]);
+                    if (!(fabsf(e) < INFINITY)) add += e;
+                }
+                if (!(add == 0.f)) a.out[at * D + d] = __float2bfloat16_rn(__bfloat162float(a.out[at * D + d]) + add);
             }
         }
-        if (a.lse && row < len) a.lse[at] = (ref + log2f(l)) * kLn2;
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&t.unit_empty[u & 1]);  // only now: the unit's odd_v has been read
+    if (w.n == 0) break;
     }
     tc_before();
     __syncthreads();
