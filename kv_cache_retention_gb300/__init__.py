@@ -15,7 +15,6 @@ Two layers:
 from __future__ import annotations
 
 import ctypes
-import math
 import os
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkvsel.so")
@@ -278,9 +277,15 @@ def kvsel_prompt_attention(ctx, q, k, v, q_stride, k_stride, v_stride, cu_seqlen
 # tensor-level wrapper
 # ---------------------------------------------------------------------------
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t, dtype=None, name="tensor"):
@@ -299,39 +304,50 @@ def _ptr(t, dtype=None, name="tensor"):
     return t.data_ptr()
 
 
-def _rows(t, lead, dtypes, name):
-    """(data_ptr, elements between tokens) of rows [*lead tokens][heads][D] on a CUDA device whose heads lie back
-    to back and whose tokens are evenly spaced (a contiguous tensor, or a slice of a fused projection)."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch.Tensor")
+def _at(t, dtype, device, name):
+    """data_ptr of a contiguous tensor of `dtype` on CUDA device `device` (None -> NULL): three tests for an argument
+    that is right, the messages of _ptr for one that is not.  The serving calls take up to 13 tensors each and run at
+    µs sizes."""
+    if t is None:
+        return None
+    try:
+        if t.dtype is dtype and t.get_device() == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _ptr(t, dtype, name)
+    raise ValueError(f"{name}: is on {t.device}, the context on cuda:{device}")
+
+
+def _rows(t, lead, dtype, device, name):
+    """(data_ptr, elements between tokens) of rows [*lead tokens][heads][D] on CUDA device `device` whose heads lie
+    back to back and whose tokens are evenly spaced (a contiguous tensor, or a slice of a fused projection)."""
+    try:
+        if t.dtype is dtype and t.get_device() == device:
+            shape, st = t.shape, t.stride()
+            if len(shape) == lead + 2:
+                heads, D = shape[-2:]
+                if t.is_contiguous():
+                    return t.data_ptr(), heads * D
+                if (D == 1 or st[-1] == 1) and (heads == 1 or st[-2] == D):
+                    stride, span = 0, 1  # the spacing, and the tokens that one step of the next axis passes
+                    for i in range(lead - 1, -1, -1):
+                        if shape[i] > 1:
+                            if not stride:
+                                stride = st[i]
+                            if st[i] != stride * span:
+                                raise ValueError(f"{name}: tokens must be evenly spaced")
+                        span *= shape[i]
+                    return t.data_ptr(), stride or heads * D
+                raise ValueError(f"{name}: a token's heads must lie back to back")
+            raise ValueError(f"{name}: expected {lead + 2} dimensions, got {len(shape)}")
+    except AttributeError:
+        raise TypeError(f"{name}: expected a torch.Tensor") from None
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a CUDA tensor (libkvsel has no CPU path)")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name}: expected {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if t.dim() != lead + 2:
-        raise ValueError(f"{name}: expected {lead + 2} dimensions, got {t.dim()}")
-    shape, st = t.shape, t.stride()
-    heads, D = shape[-2], shape[-1]
-    if t.numel() and ((D > 1 and st[-1] != 1) or (heads > 1 and st[-2] != D)):
-        raise ValueError(f"{name}: a token's heads must lie back to back")
-    stride = heads * D
-    step = 0
-    for i in range(lead - 1, -1, -1):  # token axes, innermost first: each must continue the spacing
-        if t.numel() and shape[i] > 1:
-            if not step:
-                step = st[i] // (math.prod(shape[i + 1:lead]) or 1)
-                stride = step
-            if st[i] != step * math.prod(shape[i + 1:lead]):
-                raise ValueError(f"{name}: tokens must be evenly spaced")
-    return t.data_ptr(), stride
-
-
-def _same_device(device, **tensors):
-    """Every tensor given lies on the context's device."""
-    for name, t in tensors.items():
-        if t is not None and t.get_device() != device:
-            raise ValueError(f"{name}: is on {t.device}, the context on cuda:{device}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    raise ValueError(f"{name}: is on {t.device}, the context on cuda:{device}")
 
 
 _raw_stream_getter = None
@@ -649,104 +665,120 @@ class Context:
         """Block tables, slots and positions of the step's new tokens, and slot maps, from the lengths (int32 CUDA
         tensors): cached, new_len [S]; free_pages [n_free]; block_table [S][max_blocks] (in/out); cu_new [S+1];
         new_slots, new_pos [T] (-1 behind the last token); counts [2]; slot_map [S][ld] or None."""
-        i32 = _torch().int32
+        i32, dev = _torch().int32, self.device
         S, T = cached.numel(), new_slots.numel()
         if new_len.numel() != S or cu_new.numel() != S + 1 or new_pos.numel() != T or counts.numel() != 2:
             raise ValueError("plan_slots: new_len, cu_new, new_pos and counts must have S, S+1, T and 2 elements")
-        if block_table.dim() != 2 or block_table.shape[0] != S:
+        shape = block_table.shape
+        if len(shape) != 2 or shape[0] != S:
             raise ValueError("plan_slots: block_table must be [S][max_blocks]")
-        if slot_map is not None and (slot_map.dim() != 2 or slot_map.shape[0] != S):
-            raise ValueError("plan_slots: slot_map must be [S][ld]")
-        _same_device(self.device, cached=cached, new_len=new_len, free_pages=free_pages, block_table=block_table,
-                     cu_new=cu_new, new_slots=new_slots, new_pos=new_pos, counts=counts, slot_map=slot_map)
-        self._check(kvsel_plan_slots(
-            self.handle, _ptr(cached, i32, "cached"), _ptr(new_len, i32, "new_len"), S, int(page), int(P),
-            _ptr(free_pages, i32, "free_pages"), free_pages.numel(), _ptr(block_table, i32, "block_table"),
-            block_table.shape[1], _ptr(cu_new, i32, "cu_new"), _ptr(new_slots, i32, "new_slots"),
-            _ptr(new_pos, i32, "new_pos"), T, _ptr(slot_map, i32, "slot_map"),
-            0 if slot_map is None else slot_map.shape[1], _ptr(counts, i32, "counts"), self._stream(stream)))
+        ld = 0
+        if slot_map is not None:
+            if slot_map.dim() != 2 or slot_map.shape[0] != S:
+                raise ValueError("plan_slots: slot_map must be [S][ld]")
+            ld = slot_map.shape[1]
+        rc = _lib.kvsel_plan_slots(
+            self.handle, _at(cached, i32, dev, "cached"), _at(new_len, i32, dev, "new_len"), S, int(page), int(P),
+            _at(free_pages, i32, dev, "free_pages"), free_pages.numel(), _at(block_table, i32, dev, "block_table"), shape[1],
+            _at(cu_new, i32, dev, "cu_new"), _at(new_slots, i32, dev, "new_slots"), _at(new_pos, i32, dev, "new_pos"), T,
+            _at(slot_map, i32, dev, "slot_map"), ld, _at(counts, i32, dev, "counts"), self._stream(stream))
+        if rc:
+            self._check(rc)
 
     def _kv4_cache(self, k_codes, k_scales, v_codes, v_scales, D):
         """Pointers of the 4-bit caches [P][Hkv][page][D/2] and [P][Hkv][page][D/16] and their P, Hkv, page."""
-        if k_codes.dim() != 4 or k_codes.shape[3] * 2 != D:
-            raise ValueError(f"k_codes: expected [P][Hkv][page][{D // 2}], got {tuple(k_codes.shape)}")
-        P, Hkv, page, _ = k_codes.shape
-        for name, t, last in (("k_scales", k_scales, D // 16), ("v_codes", v_codes, D // 2),
-                              ("v_scales", v_scales, D // 16)):
-            if tuple(t.shape) != (P, Hkv, page, last):
-                raise ValueError(f"{name}: expected {(P, Hkv, page, last)}, got {tuple(t.shape)}")
-        _same_device(self.device, k_codes=k_codes, k_scales=k_scales, v_codes=v_codes, v_scales=v_scales)
-        u8 = _torch().uint8
-        return (_ptr(k_codes, u8, "k_codes"), _ptr(k_scales, u8, "k_scales"), _ptr(v_codes, u8, "v_codes"),
-                _ptr(v_scales, u8, "v_scales")), P, Hkv, page
+        shape = k_codes.shape
+        if len(shape) != 4 or shape[3] * 2 != D:
+            raise ValueError(f"k_codes: expected [P][Hkv][page][{D // 2}], got {tuple(shape)}")
+        P, Hkv, page, _ = shape
+        scales = k_scales.shape
+        if v_codes.shape != shape:
+            raise ValueError(f"v_codes: expected {tuple(shape)}, got {tuple(v_codes.shape)}")
+        if scales != (P, Hkv, page, D // 16) or v_scales.shape != scales:
+            raise ValueError(f"k_scales and v_scales: expected {(P, Hkv, page, D // 16)}, got {tuple(scales)} and "
+                             f"{tuple(v_scales.shape)}")
+        u8, dev = _torch().uint8, self.device
+        return (_at(k_codes, u8, dev, "k_codes"), _at(k_scales, u8, dev, "k_scales"), _at(v_codes, u8, dev, "v_codes"),
+                _at(v_scales, u8, dev, "v_scales")), P, Hkv, page
 
     def kv4_store(self, k, v, slots, k_codes, k_scales, v_codes, v_scales, stream=None):
         """Token i's rows k[i], v[i] ([T][Hkv][D], bf16 or fp32, tokens at any even spacing) to slot slots[i] of the
         4-bit cache (negative: skipped)."""
-        torch = _torch()
-        kp, ks = _rows(k, 1, (torch.bfloat16, torch.float32), "k")
-        vp, vs = _rows(v, 1, (k.dtype,), "v")
-        T, Hkv, D = k.shape
+        torch, dev = _torch(), self.device
+        dt = torch.float32 if getattr(k, "dtype", None) is torch.float32 else torch.bfloat16
+        kp, ks = _rows(k, 1, dt, dev, "k")
+        vp, vs = _rows(v, 1, dt, dev, "v")
+        shape = k.shape
+        T, Hkv, D = shape
         cache, P, heads, page = self._kv4_cache(k_codes, k_scales, v_codes, v_scales, D)
-        if tuple(v.shape) != (T, Hkv, D) or slots.numel() != T or heads != Hkv:
+        if v.shape != shape or slots.numel() != T or heads != Hkv:
             raise ValueError("kv4_store: k, v, slots and the cache differ in tokens or heads")
-        _same_device(self.device, k=k, v=v, slots=slots)
-        self._check(kvsel_kv4_store(self.handle, kp, vp, _code(k), ks, vs, T, Hkv, D, _ptr(slots, torch.int32, "slots"),
-                                    *cache, P, page, self._stream(stream)))
+        rc = _lib.kvsel_kv4_store(self.handle, kp, vp, BF16 if dt is torch.bfloat16 else F32, ks, vs, T, Hkv, D,
+                                  _at(slots, torch.int32, dev, "slots"), *cache, P, page, self._stream(stream))
+        if rc:
+            self._check(rc)
 
     def kv4_load(self, k_codes, k_scales, v_codes, v_scales, slots, k, v, stream=None):
         """The stored rows of slots[i], exact in bf16, to k[i], v[i] ([T][Hkv][D] bf16); zeros for a negative slot."""
-        torch = _torch()
-        kp, ks = _rows(k, 1, (torch.bfloat16,), "k")
-        vp, vs = _rows(v, 1, (torch.bfloat16,), "v")
-        T, Hkv, D = k.shape
+        torch, dev = _torch(), self.device
+        kp, ks = _rows(k, 1, torch.bfloat16, dev, "k")
+        vp, vs = _rows(v, 1, torch.bfloat16, dev, "v")
+        shape = k.shape
+        T, Hkv, D = shape
         cache, P, heads, page = self._kv4_cache(k_codes, k_scales, v_codes, v_scales, D)
-        if tuple(v.shape) != (T, Hkv, D) or slots.numel() != T or heads != Hkv:
+        if v.shape != shape or slots.numel() != T or heads != Hkv:
             raise ValueError("kv4_load: k, v, slots and the cache differ in tokens or heads")
-        _same_device(self.device, k=k, v=v, slots=slots)
-        self._check(kvsel_kv4_load(self.handle, *cache, P, page, _ptr(slots, torch.int32, "slots"), T, Hkv, D, kp, vp, ks,
-                                   vs, self._stream(stream)))
+        rc = _lib.kvsel_kv4_load(self.handle, *cache, P, page, _at(slots, torch.int32, dev, "slots"), T, Hkv, D, kp, vp, ks,
+                                 vs, self._stream(stream))
+        if rc:
+            self._check(rc)
 
     def kv4_attention(self, q, k_codes, k_scales, v_codes, v_scales, seq_lens, out, slot_map=None, block_table=None,
                       dead_slot=None, scale=None, lse=None, stream=None):
         """Attention of q [S][Tq][Hq][D] (bf16), the last Tq of each session's seq_lens[s] tokens, over the 4-bit
         cache; tokens found through slot_map [S][ld] or block_table [S][ld] (int32), slots < 0 and dead_slot skipped.
         out [S][Tq][Hq][D] bf16; lse fp32 [S][Tq][Hq] or None; scale: 1/sqrt(D) when None."""
-        torch = _torch()
-        qp, qs = _rows(q, 2, (torch.bfloat16,), "q")
-        S, Tq, Hq, D = q.shape
+        torch, dev = _torch(), self.device
+        qp, qs = _rows(q, 2, torch.bfloat16, dev, "q")
+        shape = q.shape
+        S, Tq, Hq, D = shape
         cache, P, Hkv, page = self._kv4_cache(k_codes, k_scales, v_codes, v_scales, D)
         tokens = slot_map if slot_map is not None else block_table
         if tokens is None or (slot_map is not None and block_table is not None):
             raise ValueError("kv4_attention: one of slot_map and block_table is needed")
         if tokens.dim() != 2 or tokens.shape[0] != S or seq_lens.numel() != S:
             raise ValueError("kv4_attention: slot_map or block_table must be [S][ld] and seq_lens [S]")
-        if tuple(out.shape) != tuple(q.shape) or (lse is not None and tuple(lse.shape) != (S, Tq, Hq)):
+        if out.shape != shape or (lse is not None and lse.shape != (S, Tq, Hq)):
             raise ValueError("kv4_attention: out must be shaped like q and lse [S][Tq][Hq]")
-        _same_device(self.device, q=q, seq_lens=seq_lens, tokens=tokens, out=out, lse=lse)
-        self._check(kvsel_kv4_attention(
-            self.handle, qp, qs, S, Tq, Hq, Hkv, D, *cache, P, page, _ptr(seq_lens, torch.int32, "seq_lens"),
-            _ptr(slot_map, torch.int32, "slot_map"), _ptr(block_table, torch.int32, "block_table"), tokens.shape[1],
-            -1 if dead_slot is None else int(dead_slot), D ** -0.5 if scale is None else float(scale),
-            _ptr(out, torch.bfloat16, "out"), _ptr(lse, torch.float32, "lse"), self._stream(stream)))
+        i32 = torch.int32
+        rc = _lib.kvsel_kv4_attention(
+            self.handle, qp, qs, S, Tq, Hq, Hkv, D, *cache, P, page, _at(seq_lens, i32, dev, "seq_lens"),
+            _at(slot_map, i32, dev, "slot_map"), _at(block_table, i32, dev, "block_table"), tokens.shape[1],
+            -1 if dead_slot is None else int(dead_slot), D ** -0.5 if scale is None else scale,
+            _at(out, torch.bfloat16, dev, "out"), _at(lse, torch.float32, dev, "lse"), self._stream(stream))
+        if rc:
+            self._check(rc)
 
     def prompt_attention(self, q, k, v, cu_seqlens, out, scale=None, lse=None, stream=None):
         """Causal attention over packed sequences: q [T][Hq][D], k, v [T][Hkv][D] (bf16, tokens at any even spacing,
         so slices of a fused projection do), cu_seqlens int32 [S+1]; out [T][Hq][D] bf16; lse fp32 [T][Hq] or None;
         scale: 1/sqrt(D) when None."""
-        torch = _torch()
-        bf = (torch.bfloat16,)
-        (qp, qs), (kp, ks), (vp, vs) = _rows(q, 1, bf, "q"), _rows(k, 1, bf, "k"), _rows(v, 1, bf, "v")
-        T, Hq, D = q.shape
-        Hkv = k.shape[1]
-        if tuple(k.shape) != (T, Hkv, D) or tuple(v.shape) != (T, Hkv, D):
+        torch, dev = _torch(), self.device
+        bf = torch.bfloat16
+        (qp, qs), (kp, ks), (vp, vs) = _rows(q, 1, bf, dev, "q"), _rows(k, 1, bf, dev, "k"), _rows(v, 1, bf, dev, "v")
+        shape, keys = q.shape, k.shape
+        T, Hq, D = shape
+        Hkv = keys[1]
+        if keys != (T, Hkv, D) or v.shape != keys:
             raise ValueError("prompt_attention: k and v must be [T][Hkv][D]")
-        if tuple(out.shape) != (T, Hq, D) or (lse is not None and tuple(lse.shape) != (T, Hq)):
+        if out.shape != shape or (lse is not None and lse.shape != (T, Hq)):
             raise ValueError("prompt_attention: out must be [T][Hq][D] and lse [T][Hq]")
-        if cu_seqlens.numel() < 1:
+        S = cu_seqlens.numel() - 1
+        if S < 0:
             raise ValueError("prompt_attention: cu_seqlens must have S+1 elements")
-        _same_device(self.device, q=q, k=k, v=v, cu_seqlens=cu_seqlens, out=out, lse=lse)
-        self._check(kvsel_prompt_attention(self.handle, qp, kp, vp, qs, ks, vs, _ptr(cu_seqlens, torch.int32, "cu_seqlens"),
-                                           cu_seqlens.numel() - 1, T, Hq, Hkv, D, D ** -0.5 if scale is None else float(scale),
-                                           _ptr(out, torch.bfloat16, "out"), _ptr(lse, torch.float32, "lse"),
-                                           self._stream(stream)))
+        rc = _lib.kvsel_prompt_attention(
+            self.handle, qp, kp, vp, qs, ks, vs, _at(cu_seqlens, torch.int32, dev, "cu_seqlens"), S, T, Hq, Hkv, D,
+            D ** -0.5 if scale is None else scale, _at(out, bf, dev, "out"), _at(lse, torch.float32, dev, "lse"),
+            self._stream(stream))
+        if rc:
+            self._check(rc)

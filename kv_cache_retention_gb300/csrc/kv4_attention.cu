@@ -695,12 +695,16 @@ __global__ void __launch_bounds__(32 * W, D == 256 ? 1 : 16 / W) kv4_attention_k
 }
 
 template <int D, int NT, int W>
-cudaError_t launch(const AttnArgs& a, int S, int splits, cudaStream_t s) {
+cudaError_t launch(kvsel_ctx* ctx, const AttnArgs& a, int S, int splits, cudaStream_t s) {
     using C = Cfg<D, NT, W>;
     static_assert(C::kPartial <= kPartialFloats, "a block's share of the partials");
     auto* kernel = kv4_attention_kernel<D, NT, W>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
-    if (e != cudaSuccess) return e;
+    constexpr unsigned kBit = 1u << (D / 64 * 2 + NT);  // 3, 4; 5, 6; 9
+    if (!(ctx->ready & kBit)) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+        if (e != cudaSuccess) return e;
+        ctx->ready |= kBit;
+    }
     kernel<<<dim3(splits, a.Hkv * a.row_tiles, S), C::kThreads, C::kSmem, s>>>(a);
     return cudaGetLastError();
 }
@@ -777,10 +781,10 @@ extern "C" int kvsel_kv4_attention(kvsel_ctx* ctx, const void* q, int64_t q_stri
     }
     cudaError_t e;
     if (D == 256)
-        e = launch<256, 1, 8>(a, S, (int)splits, st);
+        e = launch<256, 1, 8>(ctx, a, S, (int)splits, st);
     else if (D == 128)
-        e = wide ? launch<128, 2, 8>(a, S, (int)splits, st) : launch<128, 1, 8>(a, S, (int)splits, st);
+        e = wide ? launch<128, 2, 8>(ctx, a, S, (int)splits, st) : launch<128, 1, 8>(ctx, a, S, (int)splits, st);
     else
-        e = wide ? launch<64, 2, 8>(a, S, (int)splits, st) : launch<64, 1, 8>(a, S, (int)splits, st);
+        e = wide ? launch<64, 2, 8>(ctx, a, S, (int)splits, st) : launch<64, 1, 8>(ctx, a, S, (int)splits, st);
     return e == cudaSuccess ? KVSEL_OK : kvsel_cuda_fail(ctx, e, "kv4_attention launch");
 }

@@ -50,6 +50,7 @@ struct kvsel_ctx {
     // Partial results and arrival counters of kvsel_kv4_attention calls that split a session's
     // tokens; of one size, allocated by the first such call, the counters 0 between launches.
     void* kv4_partials = nullptr;
+    unsigned ready = 0;  // kernels whose attributes are set on this context's device, a bit each
     char err[512] = {0};
 };
 

@@ -683,14 +683,19 @@ bool make_map(CUtensorMap* map, const void* base, int T, int H, int D, int64_t s
 }
 
 template <int D>
-cudaError_t launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const PromptArgs& a, cudaStream_t s) {
+cudaError_t launch(kvsel_ctx* ctx, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const PromptArgs& a,
+                   cudaStream_t s) {
     auto* kernel = prompt_attention_kernel<D>;
-    cudaFuncAttributes fa;
-    cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
-    if (e != cudaSuccess) return e;
-    if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;  // the register split counts on it
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<D>::kSmem);
-    if (e != cudaSuccess) return e;
+    constexpr unsigned kBit = 1u << (D / 64);
+    if (!(ctx->ready & kBit)) {
+        cudaFuncAttributes fa;
+        cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
+        if (e != cudaSuccess) return e;
+        if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;  // the register split counts on it
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<D>::kSmem);
+        if (e != cudaSuccess) return e;
+        ctx->ready |= kBit;
+    }
     kernel<<<(unsigned)a.n_virtual * a.Hq, kThreads, Cfg<D>::kSmem, s>>>(mq, mk, mv, a);
     return cudaGetLastError();
 }
@@ -725,6 +730,6 @@ extern "C" int kvsel_prompt_attention(kvsel_ctx* ctx, const void* q, const void*
         return kvsel_fail(ctx, KVSEL_ERR_CUDA, "prompt_attention: tensor map encoding failed");
     const PromptArgs a{(const __nv_bfloat16*)v, v_stride, cu_seqlens, S, T, Hq, Hkv, n_virtual, scale * kLog2e,
                        (__nv_bfloat16*)out, lse, ctx->dev_err};
-    const cudaError_t e = D == 64 ? launch<64>(mq, mk, mv, a, (cudaStream_t)stream) : launch<128>(mq, mk, mv, a, (cudaStream_t)stream);
+    const cudaError_t e = D == 64 ? launch<64>(ctx, mq, mk, mv, a, (cudaStream_t)stream) : launch<128>(ctx, mq, mk, mv, a, (cudaStream_t)stream);
     return e == cudaSuccess ? KVSEL_OK : kvsel_cuda_fail(ctx, e, "prompt_attention launch");
 }
