@@ -171,13 +171,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// The four bytes of w as pairs of fp16 values.
-__device__ __forceinline__ void pairs4(uint32_t w, uint32_t (&h)[4]) {
-    asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n cvt.rn.f16x2.e2m1x2 %0, a;\n"
-        " cvt.rn.f16x2.e2m1x2 %1, b;\n cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}\n"
-        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-        : "r"(w));
-}
 // fp16 scale of byte b in both halves; of bytes lo and hi in one half each.
 __device__ __forceinline__ uint32_t scale2(uint32_t b) { return (b << 7) * 0x10001u; }
 __device__ __forceinline__ uint32_t scale2(uint32_t lo, uint32_t hi) { return (lo << 7) | (hi << 23); }
@@ -411,7 +404,7 @@ __global__ void __launch_bounds__(32 * W, D == 256 ? 1 : 16 / W) kv4_attention_k
 #pragma unroll
                     for (int k = 0; k < 2 * kU; ++k) {
                         const uint32_t s2 = i < 2 ? scale2(sc[k] & 0xFFu) : scale2(sc[k] >> 8);
-                        pairs4(kw[k][i], h[k]);
+                        kv4_pairs(kw[k][i], h[k]);
 #pragma unroll
                         for (int b = 0; b < 4; ++b) h[k][b] = mul2(h[k][b], s2);
                     }
@@ -516,10 +509,10 @@ __global__ void __launch_bounds__(32 * W, D == 256 ? 1 : 16 / W) kv4_attention_k
                 const uint32_t s23 = hi ? scale2(vsc[2] >> 8, vsc[3] >> 8) : scale2(vsc[2] & 0xFFu, vsc[3] & 0xFFu);
                 constexpr uint32_t kLow = 0x0F0F0F0Fu;
                 uint32_t e01[4], o01[4], e23[4], o23[4];         // even and odd dims, token pairs
-                pairs4((vw[0][i] & kLow) | ((vw[1][i] << 4) & ~kLow), e01);
-                pairs4(((vw[0][i] >> 4) & kLow) | (vw[1][i] & ~kLow), o01);
-                pairs4((vw[2][i] & kLow) | ((vw[3][i] << 4) & ~kLow), e23);
-                pairs4(((vw[2][i] >> 4) & kLow) | (vw[3][i] & ~kLow), o23);
+                kv4_pairs((vw[0][i] & kLow) | ((vw[1][i] << 4) & ~kLow), e01);
+                kv4_pairs(((vw[0][i] >> 4) & kLow) | (vw[1][i] & ~kLow), o01);
+                kv4_pairs((vw[2][i] & kLow) | ((vw[3][i] << 4) & ~kLow), e23);
+                kv4_pairs(((vw[2][i] >> 4) & kLow) | (vw[3][i] & ~kLow), o23);
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
                     const uint32_t a0 = mul2(e01[b], s01), a1 = mul2(o01[b], s01), a2 = mul2(e23[b], s23), a3 = mul2(o23[b], s23);

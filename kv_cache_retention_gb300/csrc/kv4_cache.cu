@@ -3,10 +3,21 @@
 //
 // A group of 16 values x becomes one scale s, the smallest of the format with
 // max|x| <= 6 s, and 16 codes, the nearest E2M1 magnitudes to |x| / s with ties to
-// the even code.  The codes are found by comparing |x| with the borders between
-// magnitudes times s: those products are exact in fp32 (3 bits times 4), so the
-// rounding is exact for fp32 rows too, where a quotient could land on a tie that the
-// values are not on.
+// the even code.  The hardware conversion rounds the quotient so; what has to be
+// exact is on which side of a border between two magnitudes the quotient lies:
+//   q = x (1/s) and one correction by its remainder is the quotient rounded to
+//   nearest, so a quotient that is a border is met exactly.  A bf16 quotient that is
+//   none is at least 2^-9 of it away.
+//   An fp32 quotient can round to a border that it is not: where q has a border's bit
+//   pattern and the remainder x - q s, exact in one fma, is not zero, q is moved by
+//   one unit to its side.
+// Borders have 3 significant bits and scales 4, so border * s is a bf16 value too.
+//
+// Both kernels are bound by memory.  A thread takes one group: its 32 or 64 bytes of
+// a row, 8 bytes of codes, and one scale byte, of which four neighbours' are joined
+// to one store.  A block takes whole tokens, so places come from 32-bit divisions of
+// small numbers (64-bit divisions of the group's number, and codes found by seven
+// comparisons a value, took 86 us for 32768 tokens of 8 heads, 172 MB).
 #include <cuda_bf16.h>
 #include <limits.h>
 
@@ -24,107 +35,142 @@ struct CacheArgs {
     uint8_t* codes[2];
     uint8_t* scales[2];
     const int32_t* slots;
-    int64_t n;                // groups of one of K, V: T * Hkv * D / 16
-    int64_t n_slots;
-    int Hkv, D, page;
+    int T, Hkv, page, page_shift;  // page_shift: log2(page), or -1
+    int n_slots;
+    int per, per_shift;       // groups of a row: D / 16 = 1 << per_shift
+    int groups;               // of a token: Hkv * per
+    int tokens;               // of a block
     unsigned* err;
 };
 
-// Group g of the rows: its token, and where it lies in a row and in the cache.
+// Group `local` of the block's tokens: its token, and where it lies in a row and in the cache.
 struct Place {
-    int64_t token, row, cache;  // row: element of the token's row; cache: group index
-    bool real;
+    int token, row;           // row: element of the token's row
+    int64_t cache;            // group of the cache
+    bool in, real;            // a token of the call; with a slot of the cache
 };
-__device__ __forceinline__ Place place_of(const CacheArgs& a, int64_t g) {
-    const int per = a.D / kKv4Group;
-    const int64_t th = g / per;
-    const int i = (int)(g - th * per);
+__device__ __forceinline__ Place place_of(const CacheArgs& a, unsigned local) {
     Place p;
-    p.token = th / a.Hkv;
-    const int h = (int)(th - p.token * a.Hkv);
-    p.row = (int64_t)h * a.D + i * kKv4Group;
-    const int slot = __ldg(a.slots + p.token);
+    const unsigned t = local / (unsigned)a.groups, g = local - t * a.groups;
+    const int64_t token = (int64_t)blockIdx.x * a.tokens + t;
+    p.in = t < (unsigned)a.tokens && token < a.T;
+    p.token = (int)token;
+    const unsigned h = g >> a.per_shift, i = g & (a.per - 1);
+    p.row = (int)g * kKv4Group;
+    const int slot = p.in ? __ldg(a.slots + p.token) : -1;
     p.real = slot >= 0 && slot < a.n_slots;
-    if (slot >= 0 && !p.real) atomicOr(a.err, (unsigned)KVSEL_DEV_BAD_SLOT);
-    const int pg = slot / a.page;
-    p.cache = (((int64_t)pg * a.Hkv + h) * a.page + (slot - pg * a.page)) * per + i;
+    if (slot >= a.n_slots) atomicOr(a.err, (unsigned)KVSEL_DEV_BAD_SLOT);
+    const int pg = a.page_shift >= 0 ? slot >> a.page_shift : slot / a.page;
+    p.cache = ((((int64_t)pg * a.Hkv + h) * a.page + (slot - pg * a.page)) << a.per_shift) + i;
     return p;
 }
 
-__device__ __forceinline__ void load16(const __nv_bfloat16* src, float (&x)[16]) {
+// 16 values, and the largest magnitude (a NaN if there is one).
+__device__ __forceinline__ float load16(const __nv_bfloat16* src, float (&x)[16]) {
     const uint4 w[2] = {__ldg(reinterpret_cast<const uint4*>(src)), __ldg(reinterpret_cast<const uint4*>(src) + 1)};
     const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
+    uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         x[2 * i] = __uint_as_float(u[i] << 16);
         x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+        asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(top) : "r"(u[i] & 0x7FFF7FFFu));
     }
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(__uint_as_float(top << 16)), "f"(__uint_as_float(top & 0xFFFF0000u)));
+    return m;
 }
-__device__ __forceinline__ void load16(const float* src, float (&x)[16]) {
+__device__ __forceinline__ float load16(const float* src, float (&x)[16]) {
+    float m = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float4 w = __ldg(reinterpret_cast<const float4*>(src) + i);
         x[4 * i] = w.x, x[4 * i + 1] = w.y, x[4 * i + 2] = w.z, x[4 * i + 3] = w.w;
     }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(x[i])));
+    return m;
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) kv4_store_kernel(const CacheArgs a) {
-    const int64_t g = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (g >= a.n) return;
-    const Place p = place_of(a, g);
-    if (!p.real) return;
     const int kv = blockIdx.y;
-    float x[16];
-    load16(static_cast<const T*>(a.src[kv]) + p.token * a.stride[kv] + p.row, x);
-    float top = 0.f;
-    bool broken = false;
+    const unsigned total = (unsigned)a.tokens * a.groups;
+    for (unsigned base = 0; base < total; base += kThreads) {
+        const Place p = place_of(a, base + threadIdx.x);
+        if (!__any_sync(0xffffffffu, p.real)) continue;
+        float x[16], top = 0.f;
+        uint32_t byte = kKv4NanByte, w[2] = {0, 0};
+        if (p.real) top = load16(static_cast<const T*>(a.src[kv]) + (int64_t)p.token * a.stride[kv] + p.row, x);
+        if (p.real && top <= kKv4Max) {
+            byte = kv4_scale_byte(top);
+            const float s = kv4_scale(byte), r = byte ? 1.f / s : 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        top = fmaxf(top, fabsf(x[i]));
-        broken |= !(fabsf(x[i]) <= kKv4Max);  // NaN too
-    }
-    uint32_t byte = kKv4NanByte, w[2] = {0, 0};
-    if (!broken) {
-        byte = kv4_scale_byte(top);
-        const float s = kv4_scale(byte);
-        const float b0 = 0.25f * s, b1 = 0.75f * s, b2 = 1.25f * s, b3 = 1.75f * s, b4 = 2.5f * s, b5 = 3.5f * s,
-                    b6 = 5.f * s;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float m = fabsf(x[i]);
-            uint32_t c = (m > b0) + (m > b2) + (m > b4) + (m > b6);
-            if (byte) c += (m >= b1) + (m >= b3) + (m >= b5);  // ties to the even code above
-            c |= (__float_as_uint(x[i]) >> 28) & 8u;
-            w[i >> 3] |= c << (4 * (i & 7));
+            for (int i = 0; i < 16; ++i) {
+                float q = x[i] * r;
+                q = fmaf(-fmaf(q, s, -x[i]), r, q);  // the signs as they are: a negative zero stays one
+                if constexpr (sizeof(T) == 4) {
+                    const float rest = fmaf(-q, s, x[i]);
+                    const uint32_t b = __float_as_uint(q);
+                    if (rest != 0.f && (b & 0xFFFFFu) == 0 && (b << 1))  // a border's pattern
+                        q = __uint_as_float(b + (((int32_t)(__float_as_uint(rest) ^ b) >> 31) | 1));
+                }
+                x[i] = q;
+            }
+            w[0] = kv4_codes(x);
+            w[1] = kv4_codes(x + 8);
+        }
+        // a row's groups are neighbours, a multiple of four: one store for four scale bytes
+        uint32_t four = byte | __shfl_xor_sync(0xffffffffu, byte, 1) << 8;
+        four |= __shfl_xor_sync(0xffffffffu, four, 2) << 16;
+        if (p.real) {
+            *reinterpret_cast<uint2*>(a.codes[kv] + p.cache * 8) = make_uint2(w[0], w[1]);
+            if ((threadIdx.x & 3) == 0) *reinterpret_cast<uint32_t*>(a.scales[kv] + p.cache) = four;
         }
     }
-    *reinterpret_cast<uint2*>(a.codes[kv] + p.cache * 8) = make_uint2(w[0], w[1]);
-    a.scales[kv][p.cache] = (uint8_t)byte;
 }
 
 __global__ void __launch_bounds__(kThreads) kv4_load_kernel(const CacheArgs a) {
-    const int64_t g = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (g >= a.n) return;
-    const Place p = place_of(a, g);
     const int kv = blockIdx.y;
-    uint32_t o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (p.real) {
-        const uint2 c = __ldg(reinterpret_cast<const uint2*>(a.codes[kv] + p.cache * 8));
-        const float s = kv4_scale(__ldg(a.scales[kv] + p.cache));
+    const unsigned total = (unsigned)a.tokens * a.groups;
+    for (unsigned base = 0; base < total; base += kThreads) {
+        const Place p = place_of(a, base + threadIdx.x);
+        if (!p.in) continue;
+        uint32_t o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (p.real) {
+            const uint2 c = __ldg(reinterpret_cast<const uint2*>(a.codes[kv] + p.cache * 8));
+            const uint32_t s = __ldg(a.scales[kv] + p.cache);
+            const __half2 s2 = __half2half2(__ushort_as_half((uint16_t)(s << 7)));
+            uint32_t h[8];
+            kv4_pairs(c.x, *reinterpret_cast<uint32_t(*)[4]>(h));
+            kv4_pairs(c.y, *reinterpret_cast<uint32_t(*)[4]>(h + 4));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t h2 = kv4_pair(((i < 4 ? c.x : c.y) >> (8 * (i & 3))) & 0xFFu);
-            const float lo = __half2float(__ushort_as_half((uint16_t)(h2 & 0xFFFFu))) * s;
-            const float hi = __half2float(__ushort_as_half((uint16_t)(h2 >> 16))) * s;
-            const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);  // exact
-            o[i] = *reinterpret_cast<const uint32_t*>(&v);
+            for (int i = 0; i < 8; ++i) {  // exact products, exact in bf16
+                const float2 v = __half22float2(__hmul2(*reinterpret_cast<const __half2*>(h + i), s2));
+                const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
+                o[i] = *reinterpret_cast<const uint32_t*>(&b);
+            }
         }
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.dst[kv]) + (int64_t)p.token * a.stride[kv] + p.row);
+        dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.dst[kv]) + p.token * a.stride[kv] + p.row);
-    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
 }
+
+// Fills in the sizes; a block takes about two groups per thread, whole tokens.
+CacheArgs sized(CacheArgs a, int T, int Hkv, int D, int P, int page, unsigned* err) {
+    a.T = T, a.Hkv = Hkv, a.page = page, a.n_slots = P * page, a.err = err;
+    a.page_shift = -1;
+    if ((page & (page - 1)) == 0)
+        for (a.page_shift = 0; (1 << a.page_shift) < page;) ++a.page_shift;
+    a.per = D / kKv4Group;
+    a.per_shift = D == 64 ? 2 : D == 128 ? 3 : 4;
+    a.groups = Hkv * a.per;
+    a.tokens = 2 * kThreads / a.groups;
+    if (a.tokens < 1) a.tokens = 1;
+    return a;
+}
+dim3 grid_of(const CacheArgs& a) { return dim3((unsigned)(((int64_t)a.T + a.tokens - 1) / a.tokens), 2); }
 
 bool misaligned(const void* p, int64_t stride_bytes) { return (reinterpret_cast<uintptr_t>(p) & 15u) || stride_bytes % 16; }
 
@@ -145,9 +191,6 @@ int check(kvsel_ctx* ctx, const char* who, const void* k, const void* v, int64_t
     if (misaligned(k, k_stride * esize) || misaligned(v, v_stride * esize) || misaligned(kc, 0) || misaligned(ks, 0) ||
         misaligned(vc, 0) || misaligned(vs, 0))
         return kvsel_fail(ctx, KVSEL_ERR_ALIGN, "%s: rows, strides and caches must be 16-byte aligned", who);
-    const int64_t groups = (int64_t)T * Hkv * (D / kKv4Group);
-    if ((groups + kThreads - 1) / kThreads > INT_MAX)
-        return kvsel_fail(ctx, KVSEL_ERR_UNSUPPORTED, "%s: too many rows", who);
     return KVSEL_OK;
 }
 
@@ -165,14 +208,12 @@ extern "C" int kvsel_kv4_store(kvsel_ctx* ctx, const void* k, const void* v, int
     rc = check(ctx, "kv4_store", k, v, k_stride, v_stride, src_dtype == KVSEL_BF16 ? 2 : 4, T, Hkv, D, slots, k_codes,
                k_scales, v_codes, v_scales, P, page);
     if (rc || T == 0) return rc;
-    const int64_t n = (int64_t)T * Hkv * (D / kKv4Group);
-    const CacheArgs a{{k, v}, {nullptr, nullptr}, {k_stride, v_stride}, {k_codes, v_codes}, {k_scales, v_scales}, slots,
-                      n, (int64_t)P * page, Hkv, D, page, ctx->dev_err};
-    const dim3 grid((unsigned)((n + kThreads - 1) / kThreads), 2);
+    const CacheArgs a = sized({{k, v}, {nullptr, nullptr}, {k_stride, v_stride}, {k_codes, v_codes}, {k_scales, v_scales}, slots},
+                              T, Hkv, D, P, page, ctx->dev_err);
     if (src_dtype == KVSEL_BF16)
-        kv4_store_kernel<__nv_bfloat16><<<grid, kThreads, 0, (cudaStream_t)stream>>>(a);
+        kv4_store_kernel<__nv_bfloat16><<<grid_of(a), kThreads, 0, (cudaStream_t)stream>>>(a);
     else
-        kv4_store_kernel<float><<<grid, kThreads, 0, (cudaStream_t)stream>>>(a);
+        kv4_store_kernel<float><<<grid_of(a), kThreads, 0, (cudaStream_t)stream>>>(a);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? KVSEL_OK : kvsel_cuda_fail(ctx, e, "kv4_store launch");
 }
@@ -187,13 +228,11 @@ extern "C" int kvsel_kv4_load(kvsel_ctx* ctx, const uint8_t* k_codes, const uint
     rc = check(ctx, "kv4_load", k, v, k_stride, v_stride, 2, T, Hkv, D, slots, k_codes, k_scales, v_codes, v_scales, P,
                page);
     if (rc || T == 0) return rc;
-    const int64_t n = (int64_t)T * Hkv * (D / kKv4Group);
-    const CacheArgs a{{nullptr, nullptr}, {k, v}, {k_stride, v_stride},
-                      {const_cast<uint8_t*>(k_codes), const_cast<uint8_t*>(v_codes)},
-                      {const_cast<uint8_t*>(k_scales), const_cast<uint8_t*>(v_scales)}, slots,
-                      n, (int64_t)P * page, Hkv, D, page, ctx->dev_err};
-    const dim3 grid((unsigned)((n + kThreads - 1) / kThreads), 2);
-    kv4_load_kernel<<<grid, kThreads, 0, (cudaStream_t)stream>>>(a);
+    const CacheArgs a = sized({{nullptr, nullptr}, {k, v}, {k_stride, v_stride},
+                               {const_cast<uint8_t*>(k_codes), const_cast<uint8_t*>(v_codes)},
+                               {const_cast<uint8_t*>(k_scales), const_cast<uint8_t*>(v_scales)}, slots},
+                              T, Hkv, D, P, page, ctx->dev_err);
+    kv4_load_kernel<<<grid_of(a), kThreads, 0, (cudaStream_t)stream>>>(a);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? KVSEL_OK : kvsel_cuda_fail(ctx, e, "kv4_load launch");
 }

@@ -29,11 +29,24 @@ __device__ __forceinline__ uint32_t kv4_scale_byte(float top) {
     return b;
 }
 
-// Two codes (the byte's low four bits first) as exact fp16 values.
-__device__ __forceinline__ uint32_t kv4_pair(uint32_t byte) {
-    uint32_t h2;
-    asm("{\n .reg .b8 t;\n .reg .b16 w;\n cvt.u16.u32 w, %1;\n cvt.u8.u16 t, w;\n cvt.rn.f16x2.e2m1x2 %0, t;\n}\n"
-        : "=r"(h2)
-        : "r"(byte));
-    return h2;
+// The four bytes of w, two codes each (low four bits first), as pairs of exact fp16 values.
+__device__ __forceinline__ void kv4_pairs(uint32_t w, uint32_t (&h)[4]) {
+    asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n cvt.rn.f16x2.e2m1x2 %0, a;\n"
+        " cvt.rn.f16x2.e2m1x2 %1, b;\n cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}\n"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+}
+// The codes of two values (magnitudes up to 6, round to nearest, ties to the even code), lo in the low four bits.
+__device__ __forceinline__ uint32_t kv4_code2(float lo, float hi) {
+    uint32_t w;
+    asm volatile("{\n .reg .b8 t;\n cvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n cvt.u32.u8 %0, t;\n}\n"
+                 : "=r"(w)
+                 : "f"(lo), "f"(hi));
+    return w;
+}
+// The codes of x[0..7] in a word, x[0] lowest.
+__device__ __forceinline__ uint32_t kv4_codes(const float* x) {
+    const uint32_t lo = __byte_perm(kv4_code2(x[0], x[1]), kv4_code2(x[2], x[3]), 0x0040);
+    const uint32_t hi = __byte_perm(kv4_code2(x[4], x[5]), kv4_code2(x[6], x[7]), 0x0040);
+    return __byte_perm(lo, hi, 0x5410);
 }

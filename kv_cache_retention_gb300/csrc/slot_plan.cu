@@ -8,10 +8,13 @@
 // packed place cu_s + i, cu the exclusive sums of n.  A position p of the session
 // has slot  page_of(p / page) * page + p % page.
 //
-// One launch.  A block takes one session and one chunk of its positions; it adds up
-// the lengths of the earlier sessions itself (S loads spread over its threads, from
-// L2), so no block waits for another and no workspace is needed.  The last blocks
-// clear the packed places behind the last token.
+// One launch.  A block takes one session and one chunk of its positions; where the
+// chunk holds new tokens it adds up the lengths of the earlier sessions itself (S
+// loads spread over its threads, from L2), so no block waits for another and no
+// workspace is needed.  The last blocks clear the packed places behind the last token.
+// Small calls are bound by the chain of loads (length, table, free list), large ones by
+// the slot maps' stores: four positions at a time, with one look at the table where
+// they share a page.
 #include <limits.h>
 
 #include "kvsel_internal.h"
@@ -25,7 +28,7 @@ struct PlanArgs {
     const int32_t* cached;
     const int32_t* new_len;
     int S;
-    int page, P;
+    int page, page_shift, P;  // page_shift: log2(page), or -1
     const int32_t* free_pages;
     int n_free;
     int32_t* table;
@@ -41,6 +44,10 @@ struct PlanArgs {
     int n_chunks;  // chunks per session
 };
 
+__device__ __forceinline__ int page_index(const PlanArgs& a, int p) {
+    return a.page_shift >= 0 ? p >> a.page_shift : p / a.page;
+}
+
 // A session's lengths, brought into [0, cap]; bad: they were not there.
 struct Lens {
     int c, n, have, need;
@@ -52,38 +59,44 @@ __device__ __forceinline__ Lens lens_of(const PlanArgs& a, int s, int cap) {
     l.c = min(max(c0, 0), cap);
     l.n = min(max(n0, 0), cap - l.c);
     l.bad = l.c != c0 || l.n != n0;
-    l.have = (l.c + a.page - 1) / a.page;
-    l.need = (l.c + l.n + a.page - 1) / a.page;
+    l.have = page_index(a, l.c + a.page - 1);
+    l.need = page_index(a, l.c + l.n + a.page - 1);
     return l;
 }
 
-__device__ __forceinline__ long long block_sum(long long v, long long* sh) {
+// Sums of x and y over the block.
+__device__ __forceinline__ void block_sum(long long& x, long long& y, long long (*sh)[2]) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+    for (int o = 16; o; o >>= 1) {
+        x += __shfl_xor_sync(0xffffffffu, x, o);
+        y += __shfl_xor_sync(0xffffffffu, y, o);
+    }
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5][0] = x, sh[threadIdx.x >> 5][1] = y;
     __syncthreads();
-    long long t = 0;
+    x = y = 0;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) t += sh[w];
-    __syncthreads();
-    return t;
+    for (int w = 0; w < kThreads / 32; ++w) x += sh[w][0], y += sh[w][1];
 }
 
 __global__ void __launch_bounds__(kThreads) plan_slots_kernel(const PlanArgs a) {
-    __shared__ long long sh[kThreads / 32];
+    __shared__ long long sh[kThreads / 32][2];
     const int cap = a.max_blocks * a.page;  // the launcher keeps it below 2^31
     const int s = min((int)(blockIdx.x / a.n_chunks), a.S);
     unsigned err = 0;
 
-    // sums over the earlier sessions (s == S: over all)
+    // sums over the earlier sessions (s == S: over all), where the block has a use for them
+    const int chunk = blockIdx.x - s * a.n_chunks;
+    Lens l = {};
+    if (s < a.S) l = lens_of(a, s, cap);
     long long n_before = 0, take_before = 0;
-    for (int i = threadIdx.x; i < s; i += kThreads) {
-        const Lens l = lens_of(a, i, cap);
-        n_before += l.n;
-        take_before += l.need - l.have;
+    if (s == a.S || chunk == 0 || (l.n > 0 && (long long)chunk * kChunk < (long long)l.c + l.n && (chunk + 1ll) * kChunk > l.c)) {
+        for (int i = threadIdx.x; i < s; i += kThreads) {
+            const Lens e = lens_of(a, i, cap);
+            n_before += e.n;
+            take_before += e.need - e.have;
+        }
+        block_sum(n_before, take_before, sh);
     }
-    n_before = block_sum(n_before, sh);
-    take_before = block_sum(take_before, sh);
 
     if (s == a.S) {  // behind the last token
         const long long i0 = (long long)(blockIdx.x - (unsigned)a.S * a.n_chunks) * kChunk;
@@ -103,8 +116,6 @@ __global__ void __launch_bounds__(kThreads) plan_slots_kernel(const PlanArgs a) 
         return;
     }
 
-    const Lens l = lens_of(a, s, cap);
-    const int chunk = blockIdx.x - s * a.n_chunks;
     if (chunk == 0 && threadIdx.x == 0) {
         a.cu_new[s + 1] = (int)min(n_before + l.n, (long long)INT_MAX);
         if (l.bad || (a.slot_map && l.c + l.n > a.ld)) err |= KVSEL_DEV_BAD_LENGTH;
@@ -138,7 +149,7 @@ __global__ void __launch_bounds__(kThreads) plan_slots_kernel(const PlanArgs a) 
     for (int p = (int)max(p0, (long long)l.c) + threadIdx.x; p < t1; p += kThreads) {
         const long long i = n_before + (p - l.c);
         if (i >= a.T) break;
-        const int j = p / a.page, pg = page_of(j);
+        const int j = page_index(a, p), pg = page_of(j);
         a.new_slots[i] = pg < 0 ? -1 : pg * a.page + (p - j * a.page);
         a.new_pos[i] = p;
     }
@@ -146,14 +157,26 @@ __global__ void __launch_bounds__(kThreads) plan_slots_kernel(const PlanArgs a) 
     // the session's slot map
     if (a.slot_map) {
         int32_t* const map = a.slot_map + (int64_t)s * a.ld;
-        const int m1 = (int)min(p1, (long long)a.ld);
-        for (int p = (int)p0 + threadIdx.x; p < m1; p += kThreads) {
-            int slot = -1;
-            if (p < l.c + l.n) {
-                const int j = p / a.page, pg = page_of(j);
-                if (pg >= 0) slot = pg * a.page + (p - j * a.page);
+        const int m1 = (int)min(p1, (long long)a.ld), end = l.c + l.n;
+        auto slot_at = [&](int p) {
+            if (p >= end) return -1;
+            const int j = page_index(a, p), pg = page_of(j);
+            return pg < 0 ? -1 : pg * a.page + (p - j * a.page);
+        };
+        // rows of a multiple of four on 16 bytes, pages of a multiple of four: four positions share a page and a store
+        if (a.ld % 4 == 0 && a.page % 4 == 0 && (reinterpret_cast<uintptr_t>(a.slot_map) & 15u) == 0) {
+            for (int p = (int)p0 + 4 * threadIdx.x; p < m1; p += 4 * kThreads) {
+                const int first = slot_at(p);
+                int4 v = make_int4(first, -1, -1, -1);
+                if (first >= 0) {
+                    if (p + 1 < end) v.y = first + 1;
+                    if (p + 2 < end) v.z = first + 2;
+                    if (p + 3 < end) v.w = first + 3;
+                }
+                *reinterpret_cast<int4*>(map + p) = v;
             }
-            map[p] = slot;
+        } else {
+            for (int p = (int)p0 + threadIdx.x; p < m1; p += kThreads) map[p] = slot_at(p);
         }
     }
     if (err) atomicOr(a.err, err);
@@ -184,7 +207,10 @@ extern "C" int kvsel_plan_slots(kvsel_ctx* ctx, const int32_t* cached, const int
     const int64_t tail = T > 0 ? ((int64_t)T + kChunk - 1) / kChunk : 1;
     const int64_t blocks = S * n_chunks + tail;
     if (blocks > INT_MAX) return kvsel_fail(ctx, KVSEL_ERR_UNSUPPORTED, "plan_slots: too many positions");
-    const PlanArgs a{cached, new_len, S, page, P, free_pages, n_free, block_table, max_blocks, cu_new, new_slots,
+    int shift = -1;
+    if ((page & (page - 1)) == 0)
+        for (shift = 0; (1 << shift) < page;) ++shift;
+    const PlanArgs a{cached, new_len, S, page, shift, P, free_pages, n_free, block_table, max_blocks, cu_new, new_slots,
                      new_pos, T, ld > 0 ? slot_map : nullptr, ld, counts, ctx->dev_err, (int)n_chunks};
     plan_slots_kernel<<<(unsigned)blocks, kThreads, 0, (cudaStream_t)stream>>>(a);
     const cudaError_t e = cudaGetLastError();
