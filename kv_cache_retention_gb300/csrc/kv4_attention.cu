@@ -29,13 +29,21 @@
 // the loop has no block barrier.  Slots are read 32 at a time; live ones queue up, so
 // dropped tokens (most of a pruned session's slot map) cost a slot read and no more.
 //
-// The warps of a block take every kWarps-th chunk of 32 positions, the `splits` blocks
-// of one (session, kv head, row tile) the same again.  A block joins its warps through
-// shared memory; with splits > 1 it leaves its sums in the context's partials, and the
-// last of the blocks to arrive (a counter, which it sets back to 0) joins them in the
-// order of their ranks, so results do not depend on the order of arrival.  (A cluster
-// of blocks joined through distributed shared memory needs no partials, but clusters of
-// 16 left half of the SMs idle: 92160 tokens of 8 kv heads took 63 us.)
+// One wave of two blocks per SM.  The work is the chunks of 32 positions of every
+// session, laid end to end; it is cut into equal, contiguous shares, found from the
+// lengths on the device, so that sessions of uneven length keep every SM busy to the end
+// (with blocks for a fixed part of a session, 16 uneven sessions took 146 us, 92160
+// tokens of one 38 us).  A share is a few pieces of sessions, and neighbouring blocks
+// take it for one kv head (and row tile) each: the heads' rows of a page lie side by
+// side, and reading them at about the same time is what DRAM's pages want (laid end to
+// end over the heads as well, the 16 sessions took 169 us).
+// The block's warps take every kWarps-th chunk of a piece and join through shared
+// memory; a unit that several blocks share is joined from their partial results by a
+// second, small kernel, in the order of the blocks, launched as a dependent of the first
+// so that its start costs little.  (Joined by the last block to arrive instead, the join
+// took 4 to 10 us at the end of that block, and its registers came out of the loop's.)
+// Caches of a few thousand positions are not worth sharing: there a block takes whole
+// units, and there is nothing to join.
 #include <cuda_bf16.h>
 #include <limits.h>
 
@@ -50,12 +58,18 @@ constexpr int kTile = 32;   // tokens per stage
 constexpr int kBatch = 4;   // chunks of 32 slots read at a time
 constexpr int kQueue = 256;  // at least 31 + kTile * kBatch
 constexpr unsigned kBulk = 0x80u;
-constexpr int kMaxSplitBlocks = 1024;                        // blocks of a launch that splits
-constexpr int kPartialFloats = 16 * (128 + 2) + 4;           // the largest share of a block
+constexpr int kPartialFloats = 16 * (128 + 2) + 4;           // the largest partial result
+constexpr int64_t kWhole = 256;                              // positions up to which units are not shared
+constexpr int kLeast = 1;                                    // chunks per warp that a share has at least
 constexpr float kUnset = 3e38f;  // ref of a row that has seen nothing
 constexpr float kHead = 10.f;   // log2 of the weight at the reference
 constexpr float kSlack = 5.f;   // how far (log2) a logit may pass the reference: weights stay below 2^15
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// A unit (session, kv head, row tile) that several shares hold a part of: their partials are joined.
+struct Shared {
+    int sharers, session, late;   // late: the first sharer's partial is that of its last piece; sharers 0: no such unit
+};
 
 struct AttnArgs {
     const __nv_bfloat16* q;
@@ -74,8 +88,10 @@ struct AttnArgs {
     __nv_bfloat16* out;
     float* lse;
     unsigned* err;
-    float* partials;          // [blocks][kRows * (D + 2) + 2], splits > 1 only
-    unsigned* arrived;        // one counter for each (session, kv head, row tile), 0 between launches
+    int S;
+    int whole;                // units are not shared
+    float* partials;          // two for each block: of its first piece and of its last, where others share their units
+    struct Shared* shared;    // for each block, its shared unit that starts in its share
 };
 
 // D dims, NT tiles of 8 rows, W warps per block
@@ -93,13 +109,26 @@ struct Cfg {
         uint64_t landed[kStages];   // mbarriers of the stages' bulk copies
     };
     struct Part {
-        int nan_tail, last;
+        int nan_tail;
+        // pieces are worked out by one thread, the next one during the loop over tokens, and kept here
+        struct Piece {
+            int session, chunk0, chunk1, share0, sharers;
+            bool late;              // the session starts in share0, and not with it
+        } piece[2];
+        int session;                // of the next piece, and where that is
+        long long pos, end, before, quota, sums[kWarps];
+        float m[kRows], l[kRows];   // the block's maxima and totals
         float wm[kWarps][kRows], wl[kWarps][kRows];
         uint2 q[NT == 2 ? 2 * D / 16 * 32 : 1];  // query fragments of two row tiles: they would take too many registers
     };
     static constexpr size_t kRing = (size_t)kWarps * kStages * kStage;
     static constexpr size_t kMerge = (size_t)kWarps * kRows * D * 4;  // over the ring when the loop has ended
     static constexpr size_t kBuf = kRing > kMerge ? kRing : kMerge;
+    static constexpr int kElems = kRows * D / 4;
+    // The warps' sums as they lie in the fragments, four values per lane: element e of kElems holds rows n, n + 1 by
+    // dims d, d + 1.
+    static __device__ __forceinline__ int row_at(int e) { return 8 * ((e >> 5) / (D / 16)) + 2 * (e & 3); }
+    static __device__ __forceinline__ int dim_at(int e) { return ((e & 31) >> 2) * (D / 8) + 2 * ((e >> 5) % (D / 16)); }
     static constexpr int kPartial = kRows * (D + 2) + 4;  // floats: sums, maxima, totals, the NaN mark; a multiple of 4
     static constexpr size_t kSmem = kBuf + kWarps * sizeof(Warp) + sizeof(Part);
     static_assert(kSmem <= 232448, "shared memory per block");
@@ -188,9 +217,114 @@ __device__ __forceinline__ uint32_t row_of(const AttnArgs& a, int slot, int g) {
     return (uint32_t)(pg * (a.Hkv - 1) + g) * a.page + slot;
 }
 
-// grid (splits, Hkv * row_tiles, S)
+__device__ __forceinline__ int length_of(const AttnArgs& a, int s) { return min(max(__ldg(a.lens + s), 0), a.max_len); }
+__device__ __forceinline__ int chunks_of(int len) { return max(1, (len + kTile - 1) / kTile); }
+
+// Blocks per SM.
+template <int D, int W>
+constexpr int C_blocks() { return D == 256 ? 1 : 16 / W; }
+
+// Writes element e of unit y of session s; m, l: the rows' maxima and totals.
+template <class C, int D>
+__device__ __forceinline__ void finish(const AttnArgs& a, int s, int y, int e, float4 v, const float* m, const float* l,
+                                       bool nan_tail, unsigned& err) {
+    const int G = a.Hq / a.Hkv, R = a.Tq * G, g = y / a.row_tiles, row0 = (y - g * a.row_tiles) * C::kRows;
+    const int n = C::row_at(e), d = C::dim_at(e);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int row = row0 + n + h;
+        if (row >= R) break;
+        float v0 = h ? v.y : v.x, v1 = h ? v.w : v.z;
+        const float top = m[n + h], sum = l[n + h];
+        const int tok = row / G, head = g * G + row - tok * G;
+        if (nan_tail) {  // NaN groups of tokens that not every row sees
+            const int32_t* const map = a.map + (int64_t)s * a.ld;
+            const int common = length_of(a, s) - a.Tq;
+            for (int j = max(common + 1, 0); j <= common + tok; ++j) {
+                const int slot = raw_slot(a, map, j, err);
+                if (slot >= 0 && slot != a.dead && slot < a.n_slots &&
+                    __ldg(a.vs + (int64_t)row_of(a, slot, g) * C::kScale + d / kKv4Group) == kKv4NanByte)
+                    v0 = v1 = __int_as_float(0x7FC00000);
+            }
+        }
+        const int64_t at = ((int64_t)s * a.Tq + tok) * a.Hq + head;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        *reinterpret_cast<__nv_bfloat162*>(a.out + at * D + d) = __floats2bfloat162_rn(v0 * inv, v1 * inv);
+        if (a.lse && d == 0) a.lse[at] = sum == 0.f ? -INFINITY : (top - kHead + log2f(sum)) * kLn2;
+    }
+}
+
+// Joins block blockIdx.x's shared unit that starts in its share: a quarter of its elements per block.
+template <int D, int NT>
+__global__ void __launch_bounds__(256) kv4_join_kernel(const AttnArgs a) {
+    using C = Cfg<D, NT, 8>;
+    constexpr int kRows = C::kRows, kPart = C::kElems / 4, kGroups = 256 / kPart;  // thread groups take every kGroups-th sharer
+    extern __shared__ __align__(16) float fs[];  // [kRows][sharers] factors, then [256] sums of four
+    __shared__ float m[kRows], l[kRows];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Shared u = a.shared[blockIdx.x];
+    if (!u.sharers) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int Y = a.Hkv * a.row_tiles;
+    auto partial = [&](int k) { return a.partials + (size_t)(2 * ((int)blockIdx.x + k * Y) + (k == 0 && u.late)) * kPartialFloats; };
+    const int group = threadIdx.x / kPart, e = blockIdx.y * kPart + threadIdx.x % kPart;
+    float4 x[8];                            // on their way while the factors are worked out
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        if (group + k * kGroups < u.sharers) x[k] = reinterpret_cast<const float4*>(partial(group + k * kGroups))[e];
+    bool mark = false;
+    for (int n = warp; n < kRows; n += 8) {  // a row per warp: each sharer's maximum becomes its factor
+        float top = -INFINITY, sum = 0.f;
+        for (int k = lane; k < u.sharers; k += 32) {
+            const float* from = partial(k) + kRows * D + n;
+            const float mk = from[0], lk = from[kRows];
+            mark |= from[2 * kRows - n] != 0.f;
+            const float up = fmaxf(top, mk);
+            if (up != -INFINITY) sum = sum * ex2(top - up) + lk * ex2(mk - up);
+            top = up;
+            fs[n * u.sharers + k] = mk;
+        }
+        float all = top;
+#pragma unroll
+        for (int k = 16; k; k >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, k));
+        if (top != -INFINITY) sum *= ex2(top - all);
+#pragma unroll
+        for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+        for (int k = lane; k < u.sharers; k += 32) fs[n * u.sharers + k] = all == -INFINITY ? 0.f : ex2(fs[n * u.sharers + k] - all);
+        if (lane == 0) m[n] = all, l[n] = sum;
+    }
+    const bool nan_tail = __syncthreads_or(mark);
+    const float* const f = fs + C::row_at(e) * u.sharers;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = group; k0 < u.sharers; k0 += 8 * kGroups) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k0 + k * kGroups < u.sharers) {
+                const float z0 = f[k0 + k * kGroups], z1 = f[u.sharers + k0 + k * kGroups];
+                v.x = fmaf(x[k].x, z0, v.x), v.y = fmaf(x[k].y, z1, v.y);
+                v.z = fmaf(x[k].z, z0, v.z), v.w = fmaf(x[k].w, z1, v.w);
+            }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k0 + (k + 8) * kGroups < u.sharers) x[k] = reinterpret_cast<const float4*>(partial(k0 + (k + 8) * kGroups))[e];
+    }
+    float4* const sums = reinterpret_cast<float4*>(fs + (kRows * u.sharers + 3) / 4 * 4);
+    sums[threadIdx.x] = v;
+    __syncthreads();
+    unsigned err = 0;
+    if (threadIdx.x < kPart) {
+#pragma unroll
+        for (int k = 1; k < kGroups; ++k) {
+            const float4 z = sums[k * kPart + threadIdx.x];
+            v.x += z.x, v.y += z.y, v.z += z.z, v.w += z.w;
+        }
+        finish<C, D>(a, u.session, blockIdx.x % Y, e, v, m, l, nan_tail, err);
+    }
+    if (err) atomicOr(a.err, err);
+}
+
 template <int D, int NT, int W>
-__global__ void __launch_bounds__(32 * W, D == 256 ? 1 : 16 / W) kv4_attention_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(32 * W, C_blocks<D, W>()) kv4_attention_kernel(const AttnArgs a) {
     using C = Cfg<D, NT, W>;
     constexpr int kRows = C::kRows, kStages = C::kStages, kWarps = W, kThreads = 32 * W;
     constexpr int MT = D / 16;              // 16-dim tiles of V^T
@@ -200,40 +334,139 @@ __global__ void __launch_bounds__(32 * W, D == 256 ? 1 : 16 / W) kv4_attention_k
     typename C::Part& part = *reinterpret_cast<typename C::Part*>(smem + C::kBuf + kWarps * sizeof(typename C::Warp));
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-    const int splits = gridDim.x, rank = blockIdx.x;
-    const int g = blockIdx.y / a.row_tiles, row0 = (blockIdx.y - g * a.row_tiles) * kRows, s = blockIdx.z;
-    const int G = a.Hq / a.Hkv, R = a.Tq * G;
+    const int G = a.Hq / a.Hkv, R = a.Tq * G, Y = a.Hkv * a.row_tiles;
     typename C::Warp& w = warps[warp];
     uint8_t* const ring = smem + (size_t)warp * kStages * C::kStage;
     unsigned err = 0;
+    unsigned parity = 0;                    // next phase of each stage's barrier, a bit each
+    if (lane < kStages)
+        asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;\nfence.mbarrier_init.release.cluster;" ::"r"(saddr(&w.landed[lane])) : "memory");
 
-    const int len0 = __ldg(a.lens + s);
-    const int len = min(max(len0, 0), a.max_len);
-    if (len != len0) err |= KVSEL_DEV_BAD_LENGTH;
+    // ---- the block's share: `quota` chunks from `start` on ----
+    // Sums of the sessions' chunks up to and with each thread's session, kThreads sessions at a time.
+    auto scan = [&](int s, long long& upto) {
+        long long v = s < a.S ? chunks_of(length_of(a, s)) : 0;
+        const long long own = v;
+#pragma unroll
+        for (int k = 1; k < 32; k <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, v, k);
+            if (lane >= k) v += x;
+        }
+        __syncthreads();
+        if (lane == 31) part.sums[warp] = v;
+        __syncthreads();
+        long long all = 0;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) {
+            if (k < warp) v += part.sums[k];
+            all += part.sums[k];
+        }
+        upto = v;
+        return make_longlong2(own, all);
+    };
+    if (blockIdx.x == 0)
+        for (int s = threadIdx.x; s < a.S; s += kThreads)
+            if (__ldg(a.lens + s) != length_of(a, s)) err |= KVSEL_DEV_BAD_LENGTH;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // Shares of sessions, and the block's: number blockIdx.x / Y, for unit y = blockIdx.x % Y of the sessions in it.
+    // With more units than blocks there is one share, and blocks take every gridDim.x-th y, one after the other.
+    const int shares = max(1, (int)gridDim.x / Y), share = (int)gridDim.x < Y ? 0 : blockIdx.x / Y;
+    int y = (int)gridDim.x < Y ? blockIdx.x : blockIdx.x % Y;
+    if (a.whole) {                                   // sessions share, share + shares, ...
+        if (threadIdx.x == 0) part.pos = share, part.end = a.S, part.quota = shares;
+    } else {
+        long long total = 0, upto = 0;
+        longlong2 mine = make_longlong2(0, 0);
+        for (int s0 = 0; s0 < a.S; s0 += kThreads) {
+            mine = scan(s0 + threadIdx.x, upto);
+            total += mine.y;
+        }
+        long long quota = total < (1ll << 31) ? (unsigned)(total + shares - 1) / (unsigned)shares : (total + shares - 1) / shares;
+        quota = max(quota, (long long)kWarps * kLeast);
+        const long long start = share * quota, end = min(start + quota, total);
+        for (long long s0 = 0, run = 0; s0 < a.S; s0 += kThreads) {
+            if (a.S > kThreads) mine = scan((int)s0 + threadIdx.x, upto);
+            const long long from = run + upto - mine.x;
+            if (mine.x && from <= start && start < from + mine.x) part.session = (int)s0 + threadIdx.x, part.before = from;
+            run += mine.y;
+        }
+        if (threadIdx.x == 0) part.pos = start, part.end = share < shares ? end : 0, part.quota = quota, a.shared[blockIdx.x].sharers = 0;
+    }
+
+    // Piece number k of the share, by thread 0; session -1: there are no more.
+    auto next_piece = [&](int k) {
+        auto& x = part.piece[k & 1];
+        x.session = -1;
+        if (part.pos >= part.end) return;
+        if (a.whole) {
+            x.session = (int)part.pos;
+            x.chunk0 = 0, x.chunk1 = chunks_of(length_of(a, x.session)), x.sharers = 1;
+            part.pos += part.quota;
+            return;
+        }
+        const long long before = part.before, q = part.quota;
+        const int chunks = chunks_of(length_of(a, part.session));
+        int share1;
+        if (before + chunks < (1ll << 31)) {
+            x.share0 = (int)((unsigned)before / (unsigned)q);
+            share1 = (int)((unsigned)(before + chunks - 1) / (unsigned)q);
+        } else {
+            x.share0 = (int)(before / q);
+            share1 = (int)((before + chunks - 1) / q);
+        }
+        x.session = part.session;
+        x.chunk0 = (int)(part.pos - before);
+        x.chunk1 = (int)min((long long)chunks, part.end - before);
+        x.sharers = share1 - x.share0 + 1;
+        x.late = before != x.share0 * q;
+        if (x.sharers > 1 && x.share0 == share) a.shared[blockIdx.x] = Shared{x.sharers, x.session, x.late};
+        part.pos = before + x.chunk1;
+        if (x.chunk1 == chunks) part.before += chunks, ++part.session;
+    };
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        part.nan_tail = 0;
+        next_piece(0);
+    }
+    __syncthreads();
+
+    for (int number = 0;; ++number) {
+    // ---- a piece: chunks [chunk0, chunk1) of unit y of session s ----
+    const auto& piece = part.piece[number & 1];
+    const int s = piece.session;
+    if (s < 0) {
+        if ((int)gridDim.x >= Y || (y += gridDim.x) >= Y) break;
+        __syncthreads();                             // the next y, over the one share's sessions again
+        if (threadIdx.x == 0) {
+            part.pos = 0, part.session = 0, part.before = 0;
+            next_piece(number + 1);
+        }
+        __syncthreads();
+        continue;
+    }
+    const int len = length_of(a, s);
+    const int g = y / a.row_tiles, row0 = (y - g * a.row_tiles) * kRows;
     const int common = len - a.Tq;          // the last token that every query row sees
-    if (threadIdx.x == 0) part.nan_tail = 0;
 
     // ---- the warp's stream of live tokens ----
     // Slots are read four chunks of 32 at a time, one such batch ahead of its use.
     const int32_t* const map = a.map + (int64_t)s * a.ld;
-    const int step = splits * kWarps * kTile;
-    int j0 = (rank * kWarps + warp) * kTile;         // first chunk of the batch in `ahead`
+    constexpr int step = kWarps * kTile;
+    const int last = (int)min((long long)len, (long long)piece.chunk1 * kTile);
+    int j0 = (piece.chunk0 + warp) * kTile;                // first chunk of the batch in `ahead`
     int ahead[kBatch], batch_j = 0;                  // slots read, not looked at yet
     uint32_t rows[kBatch];                           // rows of the current batch's chunks in `bulk`
     unsigned bulk = 0;
     int head = 0, queued = 0;
-    unsigned parity = 0;                             // next phase of each stage's barrier, a bit each
     constexpr uint32_t kRowStep = C::kScale < 16 ? 16 / C::kScale : 1;  // rows at which scales are 16-byte aligned
     auto read_slots = [&](int from) {
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
             const int j = from + k * step + lane;
-            ahead[k] = j < len ? raw_slot(a, map, j, err) : -1;
+            ahead[k] = j < last ? raw_slot(a, map, j, err) : -1;
         }
     };
-    if (j0 < len) read_slots(j0);
-    if (lane < kStages)
-        asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;\nfence.mbarrier_init.release.cluster;" ::"r"(saddr(&w.landed[lane])) : "memory");
+    if (j0 < last) read_slots(j0);
 
     // query fragments: lane (n = r, c) holds row n's dims 128 m + 32 c .. + 31 (D = 64: 16 c .. + 15)
     constexpr bool kQShared = NT == 2;
@@ -293,13 +526,13 @@ __global__ void __launch_bounds__(32 * W, D == 256 ? 1 : 16 / W) kv4_attention_k
     // they come by bulk copies.
     auto produce = [&](int st) -> unsigned {
         const uint32_t base = saddr(ring + st * C::kStage);
-        while (!bulk && queued < kTile && j0 < len) {  // the next batch: whole runs stay in `rows`, other live tokens queue up
+        while (!bulk && queued < kTile && j0 < last) {  // the next batch: whole runs stay in `rows`, other live tokens queue up
             int slot[kBatch];
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) slot[k] = ahead[k];
             batch_j = j0;
             j0 += kBatch * step;
-            if (j0 < len) read_slots(j0);
+            if (j0 < last) read_slots(j0);
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
                 const bool ok = slot[k] >= 0 && slot[k] != a.dead;
@@ -526,7 +759,8 @@ __global__ void __launch_bounds__(32 * W, D == 256 ? 1 : 16 / W) kv4_attention_k
     unsigned counts = 0;                             // produce()'s answers for the stages on their way, a byte each, oldest lowest
 #pragma unroll
     for (int st = 0; st < kStages - 1; ++st) counts |= produce(st) << (8 * st);
-    __syncthreads();                                 // nan_tail and the shared query fragments are set
+    __syncthreads();                                 // the shared query fragments are set
+    if (threadIdx.x == 0) next_piece(number + 1);
     for (int st = 0; counts & 0xFFu;) {
         counts |= produce(st == 0 ? kStages - 1 : st - 1) << (8 * (kStages - 1));
         if (counts & kBulk) {
@@ -561,136 +795,67 @@ __global__ void __launch_bounds__(32 * W, D == 256 ? 1 : 16 / W) kv4_attention_k
             }
         }
     __syncthreads();                                 // also: every warp is done with its ring
-    float* const merge = reinterpret_cast<float*>(smem);  // [kWarps][kRows][D]
+    constexpr int kElems = C::kElems;
+    float4* const merge = reinterpret_cast<float4*>(smem);  // [kWarps][kElems]
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < NT; ++t) {
+        float f[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int n = 8 * t + 2 * c + e;
             float top = part.wm[0][n];
 #pragma unroll
             for (int k = 1; k < kWarps; ++k) top = fmaxf(top, part.wm[k][n]);
-            const float f = top == -INFINITY ? 0.f : ex2(part.wm[warp][n] - top);
-            float* dst = merge + ((size_t)warp * kRows + n) * D + r * (D / 8);
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-                *reinterpret_cast<float2*>(dst + 2 * i) = make_float2(o[t][i][e] * f, o[t][i][2 + e] * f);
+            f[e] = top == -INFINITY ? 0.f : ex2(part.wm[warp][n] - top);
         }
-    __syncthreads();
-    // the block's maximum, total and values of row i / D, four dims from i % D on
-    auto block_sums = [&](int i, float& top, float& sum) {
-        const int n = i / D;
-        top = part.wm[0][n], sum = 0.f;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+            merge[warp * kElems + (t * MT + i) * 32 + lane] =
+                make_float4(o[t][i][0] * f[0], o[t][i][1] * f[1], o[t][i][2] * f[0], o[t][i][3] * f[1]);
+    }
+    if (threadIdx.x < kRows) {
+        const int n = threadIdx.x;
+        float top = part.wm[0][n], sum = 0.f;
 #pragma unroll
         for (int k = 1; k < kWarps; ++k) top = fmaxf(top, part.wm[k][n]);
 #pragma unroll
-        for (int k = 0; k < kWarps; ++k) {
-            sum += top == -INFINITY ? 0.f : part.wl[k][n] * ex2(part.wm[k][n] - top);
-            const float4 x = *reinterpret_cast<const float4*>(merge + (size_t)k * kRows * D + i);
+        for (int k = 0; k < kWarps; ++k) sum += top == -INFINITY ? 0.f : part.wl[k][n] * ex2(part.wm[k][n] - top);
+        part.m[n] = top;
+        part.l[n] = sum;
+    }
+    __syncthreads();
+    auto block_sum = [&](int e) {
+        float4 v = merge[e];
+#pragma unroll
+        for (int k = 1; k < kWarps; ++k) {
+            const float4 x = merge[k * kElems + e];
             v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
         }
         return v;
     };
-    bool nan_tail = part.nan_tail != 0;
-    const float* gathered = nullptr;                 // the blocks' partials, where this block joins them
-    if (splits > 1) {
-        const int unit = blockIdx.z * gridDim.y + blockIdx.y;
-        float* const mine = a.partials + ((size_t)unit * splits + rank) * C::kPartial;
-        for (int i = threadIdx.x * 4; i < kRows * D; i += kThreads * 4) {
-            float top, sum;
-            *reinterpret_cast<float4*>(mine + i) = block_sums(i, top, sum);
-            if (i % D == 0) {
-                mine[kRows * D + i / D] = top;
-                mine[kRows * (D + 1) + i / D] = sum;
-            }
-        }
-        if (threadIdx.x == 0) mine[kRows * (D + 2)] = nan_tail ? 1.f : 0.f;
-        __threadfence();
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            const bool last = atomicAdd(a.arrived + unit, 1u) == (unsigned)splits - 1u;
-            part.last = last;
-            if (last) a.arrived[unit] = 0;
-        }
-        __syncthreads();
-        if (!part.last) {
-            if (err) atomicOr(a.err, err);
-            return;
-        }
-        __threadfence();
-        gathered = a.partials + (size_t)unit * splits * C::kPartial;
-        // each (block, row)'s maximum becomes its factor, its total what it adds to the row's
-        float* const fs = reinterpret_cast<float*>(smem);            // [splits][kRows], over the merge buffer
-        float* const ls = fs + splits * kRows;
-        bool mark = false;
-        for (int i = threadIdx.x; i < splits * kRows; i += kThreads) {
-            const float* from = gathered + (size_t)(i / kRows) * C::kPartial + kRows * D;
-            fs[i] = __ldcg(from + i % kRows);
-            ls[i] = __ldcg(from + kRows + i % kRows);
-            if (i % kRows == 0) mark |= __ldcg(from + 2 * kRows) != 0.f;
-        }
-        nan_tail = __syncthreads_or(mark);
+    if (piece.sharers > 1) {
+        // the partial of the block's first piece, but for a unit that starts within its share
+        float* const own = a.partials + (size_t)(2 * blockIdx.x + (piece.share0 == share && piece.late)) * kPartialFloats;
+        for (int e = threadIdx.x; e < kElems; e += kThreads) reinterpret_cast<float4*>(own)[e] = block_sum(e);
         if (threadIdx.x < kRows) {
-            const int n = threadIdx.x;
-            float top = -INFINITY, sum = 0.f;
-            for (int k = 0; k < splits; ++k) top = fmaxf(top, fs[k * kRows + n]);
-            for (int k = 0; k < splits; ++k) {
-                const float f = top == -INFINITY ? 0.f : ex2(fs[k * kRows + n] - top);
-                fs[k * kRows + n] = f;
-                sum = fmaf(ls[k * kRows + n], f, sum);
-            }
-            part.wm[0][n] = top;
-            part.wl[0][n] = sum;
+            own[kRows * D + threadIdx.x] = part.m[threadIdx.x];
+            own[kRows * (D + 1) + threadIdx.x] = part.l[threadIdx.x];
         }
-        __syncthreads();
+        if (threadIdx.x == 0) own[kRows * (D + 2)] = part.nan_tail ? 1.f : 0.f;
+    } else {
+        for (int e = threadIdx.x; e < kElems; e += kThreads)
+            finish<C, D>(a, s, y, e, block_sum(e), part.m, part.l, part.nan_tail != 0, err);
     }
-    for (int i = threadIdx.x * 4; i < kRows * D; i += kThreads * 4) {
-        const int n = i / D, d = i % D, row = row0 + n;
-        if (row >= R) break;
-        float top, sum;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (!gathered) {
-            v = block_sums(i, top, sum);
-        } else {
-            top = part.wm[0][n], sum = part.wl[0][n];
-            const float* const fs = reinterpret_cast<const float*>(smem) + n;
-            for (int k0 = 0; k0 < splits; k0 += 16) {  // 16 loads on their way at a time
-                float4 x[16];
-#pragma unroll
-                for (int k = 0; k < 16; ++k)
-                    if (k0 + k < splits) x[k] = __ldcg(reinterpret_cast<const float4*>(gathered + (size_t)(k0 + k) * C::kPartial + i));
-#pragma unroll
-                for (int k = 0; k < 16; ++k)
-                    if (k0 + k < splits) {
-                        const float f = fs[(k0 + k) * kRows];
-                        v.x = fmaf(x[k].x, f, v.x), v.y = fmaf(x[k].y, f, v.y);
-                        v.z = fmaf(x[k].z, f, v.z), v.w = fmaf(x[k].w, f, v.w);
-                    }
-            }
-        }
-        const int tok = row / G, h = g * G + row - tok * G;
-        if (nan_tail) {
-            for (int j = max(common + 1, 0); j <= common + tok; ++j) {
-                const int slot = raw_slot(a, map, j, err);
-                if (slot >= 0 && slot != a.dead && slot < a.n_slots && __ldg(a.vs + (int64_t)row_of(a, slot, g) * C::kScale + d / kKv4Group) == kKv4NanByte)
-                    v.x = v.y = v.z = v.w = __int_as_float(0x7FC00000);
-            }
-        }
-        const int64_t at = ((int64_t)s * a.Tq + tok) * a.Hq + h;
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * inv, v.y * inv), hi = __floats2bfloat162_rn(v.z * inv, v.w * inv);
-        *reinterpret_cast<uint2*>(a.out + at * D + d) =
-            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-        if (a.lse && d == 0) a.lse[at] = sum == 0.f ? -INFINITY : (top - kHead + log2f(sum)) * kLn2;
+    __syncthreads();                                 // shared memory is free for the next piece
+    if (threadIdx.x == 0) part.nan_tail = 0;         // (a sync lies between this and the piece's loop)
     }
     if (err) atomicOr(a.err, err);
 }
 
 template <int D, int NT, int W>
-cudaError_t launch(kvsel_ctx* ctx, const AttnArgs& a, int S, int splits, cudaStream_t s) {
+cudaError_t launch(kvsel_ctx* ctx, const AttnArgs& a, cudaStream_t s) {
     using C = Cfg<D, NT, W>;
-    static_assert(C::kPartial <= kPartialFloats, "a block's share of the partials");
+    static_assert(C::kPartial <= kPartialFloats, "a partial result");
     auto* kernel = kv4_attention_kernel<D, NT, W>;
     constexpr unsigned kBit = 1u << (D / 64 * 2 + NT);  // 3, 4; 5, 6; 9
     if (!(ctx->ready & kBit)) {
@@ -698,11 +863,28 @@ cudaError_t launch(kvsel_ctx* ctx, const AttnArgs& a, int S, int splits, cudaStr
         if (e != cudaSuccess) return e;
         ctx->ready |= kBit;
     }
-    kernel<<<dim3(splits, a.Hkv * a.row_tiles, S), C::kThreads, C::kSmem, s>>>(a);
-    return cudaGetLastError();
+    // whole shares of Y blocks, no more than there are sessions to take whole
+    const int Y = a.Hkv * a.row_tiles, most = ctx->num_sms * C_blocks<D, W>();
+    const int blocks = Y >= most ? most : Y * (a.whole && a.S < most / Y ? a.S : most / Y);
+    kernel<<<blocks, C::kThreads, C::kSmem, s>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || a.whole) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks, 4);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = (size_t)(C::kRows * blocks + 4) * sizeof(float) + 256 * sizeof(float4);
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT>, a);
 }
 
 }  // namespace
+
+size_t kv4_partials_bytes(int num_sms) { return (size_t)num_sms * 2 * (2 * kPartialFloats * sizeof(float) + sizeof(Shared)); }
 
 extern "C" int kvsel_kv4_attention(kvsel_ctx* ctx, const void* q, int64_t q_stride, int S, int Tq, int Hq, int Hkv, int D,
                                    const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v_codes,
@@ -744,40 +926,17 @@ extern "C" int kvsel_kv4_attention(kvsel_ctx* ctx, const void* q, int64_t q_stri
     int shift = -1;
     if ((page & (page - 1)) == 0)
         for (shift = 0; (1 << shift) < page;) ++shift;
-    AttnArgs a{(const __nv_bfloat16*)q, q_stride, Tq, Hq, Hkv, k_codes, k_scales, v_codes, v_scales, P, page, shift,
-                     seq_lens, slot_map ? slot_map : block_table, block_table != nullptr, P * page, ld, (int)reach, dead_slot, tiles, scale, (__nv_bfloat16*)out, lse,
-                     ctx->dev_err, nullptr, nullptr};
-    const int64_t work = (int64_t)S * Hkv * tiles;
-    // Splits of a session's tokens: none where the units of work fill the SMs (36 sessions of 8 kv heads: 87 us, split
-    // in two 98); one wave of two blocks per SM for a single session (92160 tokens: 38 us with 38 splits, 45 with 19);
-    // finer for several, whose lengths differ (16 sessions: 145 us with 8 splits, 153 with 3).  At least one chunk of
-    // 32 tokens per warp.
-    int64_t splits = 1;
-    if (work < ctx->num_sms) splits = (S == 1 ? 2 * ctx->num_sms : kMaxSplitBlocks) / work;
-    if (splits > (reach + 255) / 256) splits = (reach + 255) / 256;
-    if (splits < 1) splits = 1;
+    const AttnArgs a{(const __nv_bfloat16*)q, q_stride, Tq, Hq, Hkv, k_codes, k_scales, v_codes, v_scales, P, page, shift,
+                     seq_lens, slot_map ? slot_map : block_table, block_table != nullptr, P * page, ld, (int)reach,
+                     dead_slot, tiles, scale, (__nv_bfloat16*)out, lse, ctx->dev_err, S, reach <= kWhole,
+                     (float*)ctx->kv4_partials, (Shared*)((float*)ctx->kv4_partials + (size_t)ctx->num_sms * 4 * kPartialFloats)};
     const cudaStream_t st = (cudaStream_t)stream;
-    if (splits > 1) {
-        if (!ctx->kv4_partials) {
-            const size_t bytes = (size_t)kMaxSplitBlocks * (kPartialFloats + 1) * 4;
-            cudaError_t e = cudaMalloc(&ctx->kv4_partials, bytes);
-            if (e == cudaSuccess) e = cudaMemset(ctx->kv4_partials, 0, bytes);
-            if (e == cudaSuccess) e = cudaDeviceSynchronize();
-            if (e != cudaSuccess) {
-                if (ctx->kv4_partials) cudaFree(ctx->kv4_partials);
-                ctx->kv4_partials = nullptr;
-                return kvsel_cuda_fail(ctx, e, "kv4_attention: allocation of the partials");
-            }
-        }
-        a.arrived = (unsigned*)ctx->kv4_partials;
-        a.partials = (float*)ctx->kv4_partials + kMaxSplitBlocks;
-    }
     cudaError_t e;
     if (D == 256)
-        e = launch<256, 1, 8>(ctx, a, S, (int)splits, st);
+        e = launch<256, 1, 8>(ctx, a, st);
     else if (D == 128)
-        e = wide ? launch<128, 2, 8>(ctx, a, S, (int)splits, st) : launch<128, 1, 8>(ctx, a, S, (int)splits, st);
+        e = wide ? launch<128, 2, 6>(ctx, a, st) : launch<128, 1, 8>(ctx, a, st);
     else
-        e = wide ? launch<64, 2, 8>(ctx, a, S, (int)splits, st) : launch<64, 1, 8>(ctx, a, S, (int)splits, st);
+        e = wide ? launch<64, 2, 8>(ctx, a, st) : launch<64, 1, 8>(ctx, a, st);
     return e == cudaSuccess ? KVSEL_OK : kvsel_cuda_fail(ctx, e, "kv4_attention launch");
 }

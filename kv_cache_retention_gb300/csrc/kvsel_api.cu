@@ -158,8 +158,11 @@ int kvsel_ctx_create(int device, kvsel_ctx** out) {
     ctx->device = device;
     if (cudaDeviceGetAttribute(&ctx->num_sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess ||
         cudaMalloc(&ctx->dev_err, sizeof(unsigned)) != cudaSuccess ||
-        cudaMemset(ctx->dev_err, 0, sizeof(unsigned)) != cudaSuccess) {
+        cudaMemset(ctx->dev_err, 0, sizeof(unsigned)) != cudaSuccess ||
+        cudaMalloc(&ctx->kv4_partials, kv4_partials_bytes(ctx->num_sms)) != cudaSuccess ||
+        cudaMemset(ctx->kv4_partials, 0, kv4_partials_bytes(ctx->num_sms)) != cudaSuccess) {
         if (ctx->dev_err) cudaFree(ctx->dev_err);
+        if (ctx->kv4_partials) cudaFree(ctx->kv4_partials);
         delete ctx;
         return KVSEL_ERR_CUDA;
     }

@@ -47,8 +47,8 @@ struct kvsel_ctx {
     // Device address of the fixed scratch array of kvsel_rule_scores_noalloc on
     // this context's device, looked up by that call's first use on the context.
     void* noalloc_scratch = nullptr;
-    // Partial results and arrival counters of kvsel_kv4_attention calls that split a session's
-    // tokens; of one size, allocated by the first such call, the counters 0 between launches.
+    // Partial results of kvsel_kv4_attention: of one size, there from the context's creation on, so
+    // that captured graphs may hold its address.
     void* kv4_partials = nullptr;
     unsigned ready = 0;  // kernels whose attributes are set on this context's device, a bit each
     char err[512] = {0};
@@ -120,6 +120,7 @@ int kvsel_check_rule_scores_args(kvsel_ctx* ctx, const char* who, const void* k_
                                  const int32_t* slot_map, int n_slots, int L, int Hq, int Hkv, int N, int D,
                                  int64_t layer_stride, int64_t slot_stride, const float* M, int pi, int q_s, int q_e,
                                  const float* rule);
+size_t kv4_partials_bytes(int num_sms);
 // Frees the staging buffers, events and copy stream of kvsel_stage_restore.
 void kvsel_stager_release(kvsel_ctx* ctx);
 

@@ -306,6 +306,11 @@ ATTENTION = [
     (2, 1, 12, 1, 256, 3, [45, 200]),      # groups of twelve heads
     (1, 40, 8, 2, 128, 16, [300]),         # a short continuation
     (1, 1, 5, 1, 128, 64, [5000]),
+    (2, 130, 16, 8, 64, 16, [150, 131]),   # more row tiles than the GPU takes blocks at a time
+    (1, 600, 12, 12, 64, 8, [601]),
+    (7, 1, 4, 2, 64, 16, [2000, 3, 900, 0, 1, 31, 4097]),
+    (40, 2, 8, 2, 64, 16, [1 + 37 * i for i in range(40)]),
+    (600, 1, 1, 1, 64, 16, [i % 70 for i in range(600)]),
 ]
 
 
