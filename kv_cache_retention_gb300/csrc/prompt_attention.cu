@@ -74,7 +74,8 @@ template <int D>
 struct Cfg {
     static constexpr int kBlock = kTile * 128;             // 128 rows x 64 dims, 128-byte swizzled
     static constexpr int kBytes = D / 64 * kBlock;         // one tile of Q, K or V
-    static constexpr int kStages = 5;                      // K and V tiles share the ring
+    static constexpr int kStages = 4;                      // K and V tiles share the ring
+    static constexpr int kOut = 8 * 32 * 128;              // 32 rows of 64 dims for each softmax warp, on their way out
     // A unit of work, as warp 3 hands it out; n == 0: there are no more.
     struct Unit {
         int first, len, row0, head, n;
@@ -87,7 +88,7 @@ struct Cfg {
         int abort_flag, odd_v[2];
         Unit unit[2];
     };
-    static constexpr size_t kSmem = (size_t)(2 + kStages) * kBytes + sizeof(Tail) + 1024;
+    static constexpr size_t kSmem = (size_t)(2 + kStages) * kBytes + kOut + sizeof(Tail) + 1024;
     static_assert(kSmem <= 232448, "shared memory per block");
 };
 
@@ -405,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     uint8_t* const sq = smem;                     // [2][kBytes]
     uint8_t* const ring = smem + 2 * C::kBytes;   // [kStages][kBytes]
-    typename C::Tail& t = *reinterpret_cast<typename C::Tail*>(smem + (2 + kStages) * C::kBytes);
+    typename C::Tail& t = *reinterpret_cast<typename C::Tail*>(smem + (2 + kStages) * C::kBytes + C::kOut);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int* const abort_flag = &t.abort_flag;
 
@@ -622,27 +623,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row = w.row0 + x * kTile + r;
         const float l = sum.x + sum.y, inv = 1.f / l;
         const int64_t at = (int64_t)(w.first + row) * a.Hq + w.head;
+        // through shared memory, so that a store covers 128 bytes of each of four rows (a row per lane took 3 us a
+        // unit); 16-byte pieces are swizzled by their row against bank conflicts
+        uint8_t* const stage = smem + (2 + kStages) * C::kBytes + (warp - 4) * (32 * 128);
 #pragma unroll 1
-        for (int b = 0; b < D / 32; ++b) {
-            uint32_t o[32];
-            tmem_ld32(to + 32 * b, o);
-            tmem_wait_ld();
-            if (b == D / 32 - 1) {
-                tc_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&t.o_free[x]);
-            }
-            if (row < w.len) {
-                uint4* const dst = reinterpret_cast<uint4*>(a.out + at * D + 32 * b);
+        for (int b = 0; b < D / 64; ++b) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t o[32];
+                tmem_ld32(to + 64 * b + 32 * h, o);
+                tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     uint32_t e[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         e[k] = pack_bf16(__uint_as_float(o[8 * i + 2 * k]) * inv, __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
-                    dst[i] = make_uint4(e[0], e[1], e[2], e[3]);
+                    *reinterpret_cast<uint4*>(stage + lane * 128 + ((4 * h + i) ^ (lane & 7)) * 16) = make_uint4(e[0], e[1], e[2], e[3]);
                 }
             }
+            if (b == D / 64 - 1) tc_before();
+            __syncwarp();
+            if (b == D / 64 - 1 && lane == 0) mbar_arrive(&t.o_free[x]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int rr = 4 * i + (lane >> 3), out_row = w.row0 + x * kTile + quarter * 32 + rr;
+                const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 128 + ((lane & 7) ^ (rr & 7)) * 16);
+                if (out_row < w.len)
+                    *reinterpret_cast<uint4*>(a.out + ((int64_t)(w.first + out_row) * a.Hq + w.head) * D + 64 * b + 8 * (lane & 7)) = v;
+            }
+            __syncwarp();
         }
         if (a.lse && row < w.len) a.lse[at] = (ref + log2f(l)) * kLn2;
         if (odd && row < w.len) {
