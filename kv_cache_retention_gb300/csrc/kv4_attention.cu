@@ -104,7 +104,7 @@ struct Cfg {
     static constexpr int kStage = kTile * 2 * (kCode + kScale);
     static constexpr int kKC = 0, kKS = kTile * kCode, kVC = kKS + kTile * kScale, kVS = kVC + kTile * kCode;
     struct Warp {
-        int slot[kQueue], pos[kQueue];  // live tokens waiting for a stage
+        int2 queue[kQueue];         // live tokens waiting for a stage: slot, position
         int stage_pos[kStages][kTile];
         uint64_t landed[kStages];   // mbarriers of the stages' bulk copies
     };
@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(32 * W, C_blocks<D, W>()) kv4_attention_kernel
     int ahead[kBatch], batch_j = 0;                  // slots read, not looked at yet
     uint32_t rows[kBatch];                           // rows of the current batch's chunks in `bulk`
     unsigned bulk = 0;
-    int head = 0, queued = 0;
+    unsigned head = 0, queued = 0;
     constexpr uint32_t kRowStep = C::kScale < 16 ? 16 / C::kScale : 1;  // rows at which scales are 16-byte aligned
     auto read_slots = [&](int from) {
 #pragma unroll
@@ -466,6 +466,7 @@ __global__ void __launch_bounds__(32 * W, C_blocks<D, W>()) kv4_attention_kernel
             ahead[k] = j < last ? raw_slot(a, map, j, err) : -1;
         }
     };
+    const unsigned below = (1u << lane) - 1;
     if (j0 < last) read_slots(j0);
 
     // query fragments: lane (n = r, c) holds row n's dims 128 m + 32 c .. + 31 (D = 64: 16 c .. + 15)
@@ -526,8 +527,9 @@ __global__ void __launch_bounds__(32 * W, C_blocks<D, W>()) kv4_attention_kernel
     // they come by bulk copies.
     auto produce = [&](int st) -> unsigned {
         const uint32_t base = saddr(ring + st * C::kStage);
-        while (!bulk && queued < kTile && j0 < last) {  // the next batch: whole runs stay in `rows`, other live tokens queue up
+        while (!bulk && queued < (unsigned)kTile && j0 < last) {  // the next batch: whole runs stay in `rows`, other live tokens queue up
             int slot[kBatch];
+            bool bad = false;
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) slot[k] = ahead[k];
             batch_j = j0;
@@ -535,9 +537,8 @@ __global__ void __launch_bounds__(32 * W, C_blocks<D, W>()) kv4_attention_kernel
             if (j0 < last) read_slots(j0);
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
-                const bool ok = slot[k] >= 0 && slot[k] != a.dead;
-                const bool real = ok && slot[k] < a.n_slots;
-                if (ok && !real) err |= KVSEL_DEV_BAD_SLOT;
+                const bool ok = slot[k] >= 0 && slot[k] != a.dead, real = ok && slot[k] < a.n_slots;
+                bad |= ok != real;
                 const unsigned live = __ballot_sync(0xffffffffu, real);
                 if (live == 0xffffffffu) {
                     // two runs of 16 consecutive rows, as whole pages give them?
@@ -549,12 +550,11 @@ __global__ void __launch_bounds__(32 * W, C_blocks<D, W>()) kv4_attention_kernel
                     }
                 }
                 if (real) {
-                    const int at = (head + queued + __popc(live & ((1u << lane) - 1))) % kQueue;
-                    w.slot[at] = slot[k];
-                    w.pos[at] = batch_j + k * step + lane;
+                    w.queue[(head + queued + __popc(live & below)) % kQueue] = make_int2(slot[k], batch_j + k * step + lane);
                 }
                 queued += __popc(live);
             }
+            if (bad) err |= KVSEL_DEV_BAD_SLOT;
         }
         if (bulk) {  // eight bulk copies: codes and scales of K and V, two runs each
             const int k = __ffs(bulk) - 1;
@@ -578,18 +578,18 @@ __global__ void __launch_bounds__(32 * W, C_blocks<D, W>()) kv4_attention_kernel
             return kTile | kBulk;
         }
         __syncwarp();
-        const int n = min(queued, kTile);
+        const int n = min(queued, (unsigned)kTile);
         if (n) {
-            const int at = (head + lane) % kQueue;
-            w.stage_pos[st][lane] = w.pos[at];
-            const uint32_t row = lane < n ? row_of(a, w.slot[at], g) : 0;
+            const int2 token = w.queue[(head + lane) % kQueue];
+            w.stage_pos[st][lane] = token.y;
+            const uint32_t row = lane < n ? row_of(a, token.x, g) : 0;
             constexpr int kPer = C::kCode / 16;      // 16-byte pieces of a row's codes
 #pragma unroll
             for (int k = 0; k < kPer; ++k) {
                 const int i = k * 32 + lane, t = i / kPer;
-                const uint64_t off = (uint64_t)__shfl_sync(0xffffffffu, row, t) * C::kCode + (lane % kPer) * 16;
-                copy_async<16>(base + C::kKC + i * 16, a.kc + off, t < n);
-                copy_async<16>(base + C::kVC + i * 16, a.vc + off, t < n);
+                const uint32_t from = __shfl_sync(0xffffffffu, row, t);
+                copy_async<16>(base + C::kKC + i * 16, a.kc + (lane % kPer) * 16 + (uint64_t)from * C::kCode, t < n);
+                copy_async<16>(base + C::kVC + i * 16, a.vc + (lane % kPer) * 16 + (uint64_t)from * C::kCode, t < n);
             }
             copy_async<C::kScale>(base + C::kKS + lane * C::kScale, a.ks + (uint64_t)row * C::kScale, lane < n);
             copy_async<C::kScale>(base + C::kVS + lane * C::kScale, a.vs + (uint64_t)row * C::kScale, lane < n);
