@@ -330,15 +330,15 @@ def _rows(t, lead, dtype, device, name):
                 if t.is_contiguous():
                     return t.data_ptr(), heads * D
                 if (D == 1 or st[-1] == 1) and (heads == 1 or st[-2] == D):
-                    stride, span = 0, 1  # the spacing, and the tokens that one step of the next axis passes
+                    stride, span = None, 1  # the spacing, and the tokens that one step of the next axis passes
                     for i in range(lead - 1, -1, -1):
                         if shape[i] > 1:
-                            if not stride:
+                            if stride is None:
                                 stride = st[i]
                             if st[i] != stride * span:
                                 raise ValueError(f"{name}: tokens must be evenly spaced")
                         span *= shape[i]
-                    return t.data_ptr(), stride or heads * D
+                    return t.data_ptr(), heads * D if stride is None else stride
                 raise ValueError(f"{name}: a token's heads must lie back to back")
             raise ValueError(f"{name}: expected {lead + 2} dimensions, got {len(shape)}")
     except AttributeError:

@@ -63,6 +63,20 @@ def test_cpu_tensors_are_refused():
                      torch.zeros(2, dtype=torch.int32))
 
 
+def test_row_spacing():
+    """Rows at an even spacing, an expanded token axis (spacing 0, which the library refuses) among them."""
+    bf = torch.bfloat16
+    x = torch.zeros((6, 4, 64), dtype=bf)
+    at = lambda t, lead: kv._rows(t, lead, bf, -1, "x")[1]  # noqa: E731
+    assert at(x, 1) == 256 and at(x[:, 1:3], 1) == 256 and at(x[::2], 1) == 512 and at(x[:1, :2], 1) in (128, 256)
+    assert at(x[:1].expand(5, 4, 64), 1) == 0
+    assert at(x[:1].unsqueeze(1).expand(5, 3, 4, 64), 2) == 0
+    assert at(x.view(3, 2, 4, 64)[:, :, :2], 2) == 256
+    for bad in (x[:3].unsqueeze(1).expand(3, 2, 4, 64), x[:2].unsqueeze(0).expand(3, 2, 4, 64)):
+        with pytest.raises(ValueError, match="evenly spaced"):
+            at(bad, 2)
+
+
 def test_null_context_is_refused():
     z = [None] * 32
     assert kv.kvsel_plan_slots(None, None, None, 1, 16, 1, None, 0, None, 1, None, None, None, 0, None, 0, None,
