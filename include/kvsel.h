@@ -472,7 +472,7 @@ int kvsel_stage_restore(kvsel_ctx* ctx, const void* host_k, const void* host_v, 
  *   session); block_table int32 [S][max_blocks] in/out; cu_new int32 [S+1];
  *   new_slots, new_pos int32 [T]; slot_map int32 [S][ld] or NULL with ld = 0;
  *   counts int32 [2]
- * Requires S <= 16384, P*page and max_blocks*page < 2^31 - 4096.  No workspace.
+ * Requires S <= 16384, P*page < 2^31, max_blocks*page and ld < 2^31 - 4096.  No workspace.
  */
 int kvsel_plan_slots(kvsel_ctx* ctx, const int32_t* cached, const int32_t* new_len, int S, int page, int P,
                      const int32_t* free_pages, int n_free, int32_t* block_table, int max_blocks,
@@ -499,7 +499,8 @@ int kvsel_plan_slots(kvsel_ctx* ctx, const int32_t* cached, const int32_t* new_l
 /*
  * Store rows in the cache: token i's K and V rows go to slot slots[i].  A
  * negative slot skips the token; one at or above P*page is skipped too and
- * sets the device error word.  Tokens of one call should name distinct slots.
+ * sets the device error word.  Tokens of one call name distinct slots: what a
+ * slot holds that is named twice is not defined.
  *   k, v   src_dtype F32 or BF16; token i's Hkv rows lie back to back at
  *          element i*k_stride (i*v_stride)
  * Requires D in {64,128,256}, P*page < 2^31, rows, strides and caches 16-byte
@@ -538,7 +539,11 @@ int kvsel_kv4_load(kvsel_ctx* ctx, const uint8_t* k_codes, const uint8_t* k_scal
  *   out  bf16 [S][Tq][Hq][D]; lse fp32 [S][Tq][Hq] or NULL
  *   ld   row length of slot_map or block_table (int32 [S][ld])
  * Products take K, V exactly and the query rows and softmax weights in fp16
- * after scaling by powers of two; all sums are fp32.
+ * after scaling by powers of two; all sums are fp32.  A softmax weight of less
+ * than 2^-35 of its row's sum may count as zero (a NaN value still counts).
+ * Blocks exchange partial results through memory of a fixed size that the
+ * context holds from its creation on, so a captured call needs no earlier one;
+ * calls on one context must not overlap, replays of graphs with them included.
  * Requires D in {64,128,256}, Hq % Hkv == 0, scale > 0, Tq <= 1024, S and
  * Hq <= 65535, P*page < 2^31, P*page*Hkv < 2^32; q, q_stride, out and the caches 16-byte aligned.
  */
@@ -555,8 +560,9 @@ int kvsel_kv4_attention(kvsel_ctx* ctx, const void* q, int64_t q_stride, int S, 
  *   out[i,h] = softmax_j( scale * q[i,h] . k[j,g(h)] ) v[j,g(h)]
  *   lse[i,h] = ln sum_j exp( scale * q[i,h] . k[j,g(h)] )
  * with g(h) = h / (Hq/Hkv).  Sequences may be empty.  Rows of tokens outside
- * every sequence are not touched.  cu_seqlens must not descend; a negative
- * start sets the device error word.
+ * every sequence are not touched.  A sequence that starts below 0, ends before
+ * it starts or ends behind T sets the device error word (the last is cut to
+ * T; results are then undefined where sequences overlap).
  *   q, k, v  bf16, token i at element i*stride, its heads back to back
  *   out      bf16 [T][Hq][D]; lse fp32 [T][Hq] or NULL
  * The products take bf16 (softmax weights rounded to it), sums are fp32.

@@ -214,7 +214,7 @@ __device__ __forceinline__ int raw_slot(const AttnArgs& a, const int32_t* map, i
 }
 __device__ __forceinline__ uint32_t row_of(const AttnArgs& a, int slot, int g) {
     const int pg = a.page_shift >= 0 ? slot >> a.page_shift : slot / a.page;
-    return (uint32_t)(pg * (a.Hkv - 1) + g) * a.page + slot;
+    return ((uint32_t)pg * (a.Hkv - 1) + g) * a.page + slot;
 }
 
 __device__ __forceinline__ int length_of(const AttnArgs& a, int s) { return min(max(__ldg(a.lens + s), 0), a.max_len); }

@@ -353,13 +353,13 @@ __device__ __forceinline__ typename Cfg<D>::Unit unit_of(const PromptArgs& a, ui
         size = min(piece, size - last * piece);
     }
     typename Cfg<D>::Unit w;
+    const int stop = __ldg(a.cu + lo + 1);
     w.first = __ldg(a.cu + lo);
-    w.len = min(__ldg(a.cu + lo + 1), a.T) - w.first;
+    w.len = w.first < 0 || stop < w.first ? 0 : min(stop, a.T) - w.first;
     const int tile = number - (w.first / kUnit + lo);
-    w.row0 = tile * kUnit;
+    const bool rows = tile >= 0 && (int64_t)tile * kUnit < w.len;
+    w.row0 = rows ? tile * kUnit : 0;
     w.head = (int)(block % a.Hq);
-    if (w.first < 0 && lane == 0) atomicOr(a.err, (unsigned)KVSEL_DEV_BAD_LENGTH);
-    const bool rows = w.first >= 0 && tile >= 0 && (int64_t)tile * kUnit < w.len;
     w.n = !rows ? 0 : 2 * tile + (w.row0 + kTile < w.len ? 2 : 1);
     return w;
 }
@@ -479,11 +479,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             // The block starts with its own unit and then claims those of blocks that have not been launched yet, in
             // the order of launch, until none is left.
             uint32_t block = blockIdx.x, base = 0, claims = 0;
-            bool ok = true, any = true;
+            bool ok = true, any = true, look = false;
             for (uint32_t u = 0; ok; ++u) {
                 typename C::Unit w;
                 w.n = 0;
                 while (any) {
+                    look |= block == 0;
                     w = unit_of<D>(a, block, lane);
                     if (w.n) break;
                     any = claim_next(t, claims, block, lane, true, abort_flag, a.err);
@@ -495,6 +496,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&t.unit_full[u & 1]);
+                if (look) {  // with the first block's unit: do the sequences lie in [0, T], one behind the other?
+                    look = false;
+                    for (int s = lane; s < a.S; s += 32) {
+                        const int start = __ldg(a.cu + s), stop = __ldg(a.cu + s + 1);
+                        if (start < 0 || stop < start || stop > a.T) atomicOr(a.err, (unsigned)KVSEL_DEV_BAD_LENGTH);
+                    }
+                    __syncwarp();
+                }
                 if (w.n == 0) break;
                 if (lane == 0) claim_start(t);
                 for (int i = 0; i < 2 && ok; ++i) {  // NaN and infinities to zero
@@ -577,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 4; ++i) m[i] = fmaxf(m[i], __uint_as_float(s[kTile - 4 + i]));
         const float top = fmaxf(max3(m[0], m[1], m[2]), m[3]) * sc;
         if (k == 0) {
-            ref = top == -INFINITY ? 0.f : top;
+            ref = fmaxf(top, -3e38f);  // of a row whose logits here are all -inf: low, and finite
         } else if (__any_sync(0xffffffffu, top > ref + kSlack)) {
             // references move up: the sums so far and O shrink with them
             const float next = fmaxf(ref, top), f = ex2(ref - next);

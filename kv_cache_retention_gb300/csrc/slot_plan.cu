@@ -59,8 +59,8 @@ __device__ __forceinline__ Lens lens_of(const PlanArgs& a, int s, int cap) {
     l.c = min(max(c0, 0), cap);
     l.n = min(max(n0, 0), cap - l.c);
     l.bad = l.c != c0 || l.n != n0;
-    l.have = page_index(a, l.c + a.page - 1);
-    l.need = page_index(a, l.c + l.n + a.page - 1);
+    l.have = l.c > 0 ? page_index(a, l.c - 1) + 1 : 0;
+    l.need = l.c + l.n > 0 ? page_index(a, l.c + l.n - 1) + 1 : 0;
     return l;
 }
 
@@ -195,7 +195,7 @@ extern "C" int kvsel_plan_slots(kvsel_ctx* ctx, const int32_t* cached, const int
     if (S < 0 || page <= 0 || P < 0 || n_free < 0 || max_blocks < 0 || T < 0 || ld < 0)
         return kvsel_fail(ctx, KVSEL_ERR_SHAPE, "plan_slots: bad sizes");
     if (S > 16384) return kvsel_fail(ctx, KVSEL_ERR_UNSUPPORTED, "plan_slots: S=%d > 16384 sessions", S);
-    if ((int64_t)P * page > INT_MAX || (int64_t)max_blocks * page > INT_MAX - 4096)
+    if ((int64_t)P * page > INT_MAX || (int64_t)max_blocks * page > INT_MAX - 4096 || ld > INT_MAX - 4096)
         return kvsel_fail(ctx, KVSEL_ERR_UNSUPPORTED, "plan_slots: slots and positions must fit 31 bits");
     if (!cu_new || !counts || (S > 0 && (!cached || !new_len)) || (S > 0 && max_blocks > 0 && !block_table) ||
         (n_free > 0 && !free_pages) || (T > 0 && (!new_slots || !new_pos)) || (S > 0 && ld > 0 && !slot_map))

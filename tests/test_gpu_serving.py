@@ -111,6 +111,20 @@ def test_plan_lengths_out_of_range(ctx):
     assert got["slots"].tolist() == [0, 1, 2, 3, 4] and got["counts"].tolist() == [9, 3]
 
 
+def test_plan_pages_of_almost_all_positions(ctx):
+    """One page that takes nearly every 31-bit slot: sums next to 2^31 do not wrap."""
+    page = 2 ** 31 - 4098
+    table = torch.zeros((1, 1), dtype=I32, device="cuda")
+    cu, slots, pos, counts = (torch.empty(n, dtype=I32, device="cuda") for n in (2, 3, 3, 2))
+    ctx.plan_slots(_i32([page - 2]), _i32([2]), _i32([0]), page, 1, table, cu, slots, pos, counts)
+    ctx.check_device()
+    assert counts.tolist() == [2, 0] and cu.tolist() == [0, 2]  # its page is there already
+    assert slots.tolist() == pos.tolist() == [page - 2, page - 1, -1]
+    ctx.plan_slots(_i32([0]), _i32([2]), _i32([0]), page, 1, table, cu, slots, pos, counts)
+    ctx.check_device()
+    assert counts.tolist() == [2, 1] and table.tolist() == [[0]] and slots.tolist() == [0, 1, -1]
+
+
 def test_plan_bad_pages(ctx):
     got = _plan(ctx, [4], [4], [9], 4, 4, 2, 4, 8, [[17, -1]])
     _flagged(ctx, "page out of range")
@@ -648,6 +662,37 @@ def test_prompt_bad_starts_are_flagged(ctx):
     assert (out == 9).all()
 
 
+@pytest.mark.parametrize("cu", [[0, 9], [5, -2 ** 31], [2 ** 31 - 1, 2 ** 31 - 1], [3, 2, 8], [-2 ** 31, 2 ** 31 - 1],
+                                [0, 2 ** 31 - 1, 8], [600, 700], [0, 300, 100, 8]])
+def test_prompt_bad_sequences_are_flagged(ctx, cu):
+    """Sequences outside the rows, or descending: flagged, and nothing outside the rows is written."""
+    T = 8
+    big = torch.ones((1024, 2, 64), dtype=BF, device="cuda")
+    out, lse = torch.full_like(big, 9), torch.full((1024, 2), 9.0, device="cuda")
+    ctx.prompt_attention(big[:T], big[:T], big[:T], _i32(cu), out[:T], lse=lse[:T])
+    _flagged(ctx, "length out of range")
+    assert (out[T:] == 9).all() and (lse[T:] == 9).all()
+
+
+def test_prompt_minus_infinite_logits_of_the_last_keys(ctx):
+    """Keys whose logits are -inf for every row: a softmax over the keys before them, as the formula has it."""
+    g = torch.Generator(device="cuda").manual_seed(23)
+    T, D, cut = 300, 64, 200
+    q, k, v = (torch.randn((T, 1, D), generator=g, device="cuda").to(BF) for _ in range(3))
+    q[..., 0] = 1
+    k[cut:, 0, 0] = -float("inf")
+    q[..., 1] = q[..., 1].abs() + 1
+    k[:cut, 0, 1] = -200  # far below zero where they are finite: logits near -25 to -100
+    out, lse = torch.empty_like(q), torch.empty((T, 1), device="cuda")
+    ctx.prompt_attention(q, k, v, _i32([0, T]), out, lse=lse)
+    ctx.check_device()
+    # rows before the cut as they are; each later row like one that sees the first `cut` keys
+    _check_prompt(q[:cut], k[:cut], v[:cut], [0, cut], D ** -0.5, out[:cut], lse[:cut])
+    for r in (cut, 255, 256, 299):
+        at = [r if i == cut - 1 else i for i in range(cut)]
+        _check_prompt(q[at], k[:cut], v[:cut], [0, cut], D ** -0.5, out[at], lse[at], rows=[cut - 1])
+
+
 # ---------------------------------------------------------------------------
 # refusals
 # ---------------------------------------------------------------------------
@@ -690,7 +735,8 @@ def test_refusals(ctx):
         stream=s), **kw}.values())
     for code, kw in [(kv.ERR_INVALID_ARG, dict(c=None)), (kv.ERR_INVALID_ARG, dict(cu=None)), (kv.ERR_INVALID_ARG, dict(ld=3)),
                      (kv.ERR_SHAPE, dict(page=0)), (kv.ERR_SHAPE, dict(T=-1)), (kv.ERR_UNSUPPORTED, dict(S=16385)),
-                     (kv.ERR_UNSUPPORTED, dict(P=2 ** 30)), (kv.ERR_UNSUPPORTED, dict(mb=2 ** 30))]:
+                     (kv.ERR_UNSUPPORTED, dict(P=2 ** 30)), (kv.ERR_UNSUPPORTED, dict(mb=2 ** 30)),
+                     (kv.ERR_UNSUPPORTED, dict(sm=p, ld=2 ** 31 - 1))]:
         assert pln(**kw) == code, kw
     torch.cuda.synchronize()
     assert not x.any()  # nothing was launched
@@ -701,6 +747,10 @@ def test_refusals(ctx):
         ctx.prompt_attention(q.transpose(0, 1), q, q, _i32([0, 2]), q)
     with pytest.raises(ValueError, match="k and v"):
         ctx.prompt_attention(q, q[:1], q, _i32([0, 2]), q)
+    with pytest.raises(kv.KvselError, match="stride"):  # expanded tokens
+        ctx.prompt_attention(q[:1].expand(2, 4, 64), q, q, _i32([0, 2]), torch.zeros_like(q))
+    with pytest.raises(kv.KvselError, match="stride"):
+        ctx.kv4_store(q[:1].expand(2, 4, 64), q, _i32([0, 1]), *_cache(1, 4, 4, 64))
     with pytest.raises(ValueError, match="evenly spaced"):
         ctx.kv4_attention(torch.zeros((2, 3, 2, 4, 64), dtype=BF, device="cuda")[:, :, 0][:, :2], *_cache(1, 4, 4, 64),
                           _i32([1, 1]), torch.zeros((2, 2, 4, 64), dtype=BF, device="cuda"),
@@ -822,3 +872,38 @@ def test_decode_step_from_a_graph(ctx):
         _check_attention(out, lse, _attention_reference(x[:, :Hq].unsqueeze(1), cache, n, sl, np.ones_like(sl, bool), D ** -0.5))
         cached += 1
     ctx.check_device()
+
+
+def test_two_contexts_on_two_streams(ctx):
+    """Decode and prompt attention of two contexts, on streams that run beside each other, as on one."""
+    g = torch.Generator(device="cuda").manual_seed(24)
+    Hq, Hkv, D, page, P = 8, 2, 128, 16, 256
+    other = kv.Context(0)
+    work = []
+    for c, lens in ((ctx, [3000, 5]), (other, [900, 2500])):
+        cache = _random_cache(g, P, Hkv, page, D)
+        table = torch.randperm(P, generator=g, device="cuda").to(I32)[:2 * 120].view(2, 120) % P
+        table = torch.cat([table, table], 1).contiguous()
+        q = torch.randn((2, 1, Hq, D), generator=g, device="cuda").to(BF)
+        x = torch.randn((700, Hq + 2 * Hkv, D), generator=g, device="cuda").to(BF)
+        work.append((c, q, cache, _i32(lens), table, x, _i32([0, 300, 700]), torch.cuda.Stream()))
+
+    def run(w, stream):
+        c, q, cache, lens, table, x, cu, _ = w
+        outs = []
+        with torch.cuda.stream(stream):
+            for _ in range(5):
+                o, p = torch.empty_like(q), torch.empty((700, Hq, D), dtype=BF, device="cuda")
+                c.kv4_attention(q, *cache, lens, o, block_table=table)
+                c.prompt_attention(x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], cu, p)
+                outs += [o, p]
+        return outs
+
+    want = [run(w, torch.cuda.current_stream()) for w in work]
+    torch.cuda.synchronize()
+    got = [run(w, w[-1]) for w in work]
+    torch.cuda.synchronize()
+    for c, a, b in zip((ctx, other), want, got):
+        c.check_device()
+        assert all(torch.equal(i, j) for i, j in zip(a, b))
+    other.close()
