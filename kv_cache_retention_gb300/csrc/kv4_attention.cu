@@ -28,6 +28,15 @@
 // Tokens come to a warp through cp.async into a ring of two or three buffers of its own, so
 // the loop has no block barrier.  Slots are read 32 at a time; live ones queue up, so
 // dropped tokens (most of a pruned session's slot map) cost a slot read and no more.
+// Where 32 slots are two runs of 16 rows, four pairs of bulk copies bring them instead.
+//
+// What bounds it: instructions, before memory.  For D = 128 a warp executes about 850
+// for 32 tokens of one kv head, 4.6 KB, of which 270 are the conversions and the scales'
+// multiplications and 33 the products, and issues on 60% of the cycles.  Measured: 36
+// sessions of 32 / 8 heads pruned to a quarter, 278 MB: 81.6 us (3.4 TB/s); 16 sessions
+// of 4 query rows, 306 MB: 109 us (2.8 TB/s); one of 92160 tokens, 106 MB: 34 us, of
+// which some 6 us go by before the first tokens arrive and 5 us with the join.  More
+// warps per SM (10 a block, 96 registers) took 104, 115 and 40 us.
 //
 // One wave of two blocks per SM.  The work is the chunks of 32 positions of every
 // session, laid end to end; it is cut into equal, contiguous shares, found from the
@@ -55,8 +64,6 @@
 namespace {
 
 constexpr int kTile = 32;   // tokens per stage
-constexpr int kBatch = 4;   // chunks of 32 slots read at a time
-constexpr int kQueue = 256;  // at least 31 + kTile * kBatch
 constexpr unsigned kBulk = 0x80u;
 constexpr int kPartialFloats = 16 * (128 + 2) + 4;           // the largest partial result
 constexpr int64_t kWhole = 256;                              // positions up to which units are not shared
@@ -78,8 +85,8 @@ struct AttnArgs {
     const uint8_t *kc, *ks, *vc, *vs;
     int P, page, page_shift;  // page_shift: log2(page), or -1
     const int32_t* lens;
-    const int32_t* map;       // slot map, or block table (by_page)
-    int by_page, n_slots;
+    const int32_t* map;       // slot map, or block table
+    int n_slots;
     int ld;                   // row length of map
     int max_len;              // tokens that a row of it reaches
     int dead;
@@ -94,9 +101,14 @@ struct AttnArgs {
     struct Shared* shared;    // for each block, its shared unit that starts in its share
 };
 
-// D dims, NT tiles of 8 rows, W warps per block
-template <int D, int NT, int W>
+// D dims, NT tiles of 8 rows, W warps per block, MAP: tokens found through a slot map, not a block table
+template <int D, int NT, int W, bool MAP>
 struct Cfg {
+    // Chunks of 32 slots read at a time.  Few of a pruned session's slots may be live (36 sessions, a quarter live: 82 us
+    // with four, 103 us with one); a block table's nearly all are, and one makes for less code (16 sessions of 4 query
+    // rows: 111 us with one, 117 us with four).
+    static constexpr int kBatch = MAP ? 4 : 1;
+    static constexpr int kQueue = MAP ? 256 : 64;                // a power of two, at least 31 + kTile * kBatch
     static constexpr int kWarps = W, kThreads = 32 * W;
     static constexpr int kRows = 8 * NT;
     static constexpr int kStages = D == 64 ? 3 : 2;  // two blocks per SM (D = 256: one)
@@ -205,8 +217,9 @@ __device__ __forceinline__ uint32_t scale2(uint32_t b) { return (b << 7) * 0x100
 __device__ __forceinline__ uint32_t scale2(uint32_t lo, uint32_t hi) { return (lo << 7) | (hi << 23); }
 
 // Slot of token j as the map or the block table has it; negative where a page is not live.
+template <bool MAP>
 __device__ __forceinline__ int raw_slot(const AttnArgs& a, const int32_t* map, int j, unsigned& err) {
-    if (!a.by_page) return __ldg(map + j);
+    if constexpr (MAP) return __ldg(map + j);
     const int b = a.page_shift >= 0 ? j >> a.page_shift : j / a.page;
     const int pg = __ldg(map + b);
     if (pg >= a.P) err |= KVSEL_DEV_BAD_PAGE;
@@ -225,7 +238,7 @@ template <int D, int W>
 constexpr int C_blocks() { return D == 256 ? 1 : 16 / W; }
 
 // Writes element e of unit y of session s; m, l: the rows' maxima and totals.
-template <class C, int D>
+template <class C, int D, bool MAP>
 __device__ __forceinline__ void finish(const AttnArgs& a, int s, int y, int e, float4 v, const float* m, const float* l,
                                        bool nan_tail, unsigned& err) {
     const int G = a.Hq / a.Hkv, R = a.Tq * G, g = y / a.row_tiles, row0 = (y - g * a.row_tiles) * C::kRows;
@@ -241,7 +254,7 @@ __device__ __forceinline__ void finish(const AttnArgs& a, int s, int y, int e, f
             const int32_t* const map = a.map + (int64_t)s * a.ld;
             const int common = length_of(a, s) - a.Tq;
             for (int j = max(common + 1, 0); j <= common + tok; ++j) {
-                const int slot = raw_slot(a, map, j, err);
+                const int slot = raw_slot<MAP>(a, map, j, err);
                 if (slot >= 0 && slot != a.dead && slot < a.n_slots &&
                     __ldg(a.vs + (int64_t)row_of(a, slot, g) * C::kScale + d / kKv4Group) == kKv4NanByte)
                     v0 = v1 = __int_as_float(0x7FC00000);
@@ -255,9 +268,9 @@ __device__ __forceinline__ void finish(const AttnArgs& a, int s, int y, int e, f
 }
 
 // Joins block blockIdx.x's shared unit that starts in its share: a quarter of its elements per block.
-template <int D, int NT>
+template <int D, int NT, bool MAP>
 __global__ void __launch_bounds__(256) kv4_join_kernel(const AttnArgs a) {
-    using C = Cfg<D, NT, 8>;
+    using C = Cfg<D, NT, 8, MAP>;
     constexpr int kRows = C::kRows, kPart = C::kElems / 4, kGroups = 256 / kPart;  // thread groups take every kGroups-th sharer
     extern __shared__ __align__(16) float fs[];  // [kRows][sharers] factors, then [256] sums of four
     __shared__ float m[kRows], l[kRows];
@@ -318,14 +331,15 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const AttnArgs a) {
             const float4 z = sums[k * kPart + threadIdx.x];
             v.x += z.x, v.y += z.y, v.z += z.z, v.w += z.w;
         }
-        finish<C, D>(a, u.session, blockIdx.x % Y, e, v, m, l, nan_tail, err);
+        finish<C, D, MAP>(a, u.session, blockIdx.x % Y, e, v, m, l, nan_tail, err);
     }
     if (err) atomicOr(a.err, err);
 }
 
-template <int D, int NT, int W>
+template <int D, int NT, int W, bool MAP>
 __global__ void __launch_bounds__(32 * W, C_blocks<D, W>()) kv4_attention_kernel(const AttnArgs a) {
-    using C = Cfg<D, NT, W>;
+    using C = Cfg<D, NT, W, MAP>;
+    constexpr int kBatch = C::kBatch, kQueue = C::kQueue;
     constexpr int kRows = C::kRows, kStages = C::kStages, kWarps = W, kThreads = 32 * W;
     constexpr int MT = D / 16;              // 16-dim tiles of V^T
     constexpr int KK = D / 16;              // 16-dim steps of K q^T
@@ -463,10 +477,11 @@ __global__ void __launch_bounds__(32 * W, C_blocks<D, W>()) kv4_attention_kernel
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
             const int j = from + k * step + lane;
-            ahead[k] = j < last ? raw_slot(a, map, j, err) : -1;
+            ahead[k] = j < last ? raw_slot<MAP>(a, map, j, err) : -1;
         }
     };
     const unsigned below = (1u << lane) - 1;
+    const bool runs = a.page % 16 == 0;
     if (j0 < last) read_slots(j0);
 
     // query fragments: lane (n = r, c) holds row n's dims 128 m + 32 c .. + 31 (D = 64: 16 c .. + 15)
@@ -537,14 +552,18 @@ __global__ void __launch_bounds__(32 * W, C_blocks<D, W>()) kv4_attention_kernel
             if (j0 < last) read_slots(j0);
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
-                const bool ok = slot[k] >= 0 && slot[k] != a.dead, real = ok && slot[k] < a.n_slots;
+                const bool ok = slot[k] >= 0 && slot[k] != a.dead, real = ok && (!MAP || slot[k] < a.n_slots);
                 bad |= ok != real;
                 const unsigned live = __ballot_sync(0xffffffffu, real);
-                if (live == 0xffffffffu) {
-                    // two runs of 16 consecutive rows, as whole pages give them?
+                // two runs of 16 consecutive rows?  Pages of a multiple of 16 give them, and a map's slots may
+                if (live == 0xffffffffu && (MAP || runs)) {
                     rows[k] = row_of(a, slot[k], g);
-                    const uint32_t first = __shfl_sync(0xffffffffu, rows[k], lane & 16);
-                    if (__all_sync(0xffffffffu, rows[k] == first + (lane & 15) && first % kRowStep == 0)) {
+                    bool run = true;
+                    if constexpr (MAP) {
+                        const uint32_t first = __shfl_sync(0xffffffffu, rows[k], lane & 16);
+                        run = __all_sync(0xffffffffu, rows[k] == first + (lane & 15) && first % kRowStep == 0);
+                    }
+                    if (run) {
                         bulk |= 1u << k;
                         continue;
                     }
@@ -844,7 +863,7 @@ __global__ void __launch_bounds__(32 * W, C_blocks<D, W>()) kv4_attention_kernel
         if (threadIdx.x == 0) own[kRows * (D + 2)] = part.nan_tail ? 1.f : 0.f;
     } else {
         for (int e = threadIdx.x; e < kElems; e += kThreads)
-            finish<C, D>(a, s, y, e, block_sum(e), part.m, part.l, part.nan_tail != 0, err);
+            finish<C, D, MAP>(a, s, y, e, block_sum(e), part.m, part.l, part.nan_tail != 0, err);
     }
     __syncthreads();                                 // shared memory is free for the next piece
     if (threadIdx.x == 0) part.nan_tail = 0;         // (a sync lies between this and the piece's loop)
@@ -852,12 +871,12 @@ __global__ void __launch_bounds__(32 * W, C_blocks<D, W>()) kv4_attention_kernel
     if (err) atomicOr(a.err, err);
 }
 
-template <int D, int NT, int W>
+template <int D, int NT, int W, bool MAP>
 cudaError_t launch(kvsel_ctx* ctx, const AttnArgs& a, cudaStream_t s) {
-    using C = Cfg<D, NT, W>;
+    using C = Cfg<D, NT, W, MAP>;
     static_assert(C::kPartial <= kPartialFloats, "a partial result");
-    auto* kernel = kv4_attention_kernel<D, NT, W>;
-    constexpr unsigned kBit = 1u << (D / 64 * 2 + NT);  // 3, 4; 5, 6; 9
+    auto* kernel = kv4_attention_kernel<D, NT, W, MAP>;
+    constexpr unsigned kBit = 1u << (D / 64 * 2 + NT + (MAP ? 8 : 0));  // 3, 4; 5, 6; 9, and 8 more
     if (!(ctx->ready & kBit)) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
         if (e != cudaSuccess) return e;
@@ -879,7 +898,14 @@ cudaError_t launch(kvsel_ctx* ctx, const AttnArgs& a, cudaStream_t s) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT>, a);
+    return cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT, MAP>, a);
+}
+
+template <bool MAP>
+cudaError_t launch_for(kvsel_ctx* ctx, const AttnArgs& a, int D, bool wide, cudaStream_t s) {
+    if (D == 256) return launch<256, 1, 8, MAP>(ctx, a, s);
+    if (D == 128) return wide ? launch<128, 2, 6, MAP>(ctx, a, s) : launch<128, 1, 8, MAP>(ctx, a, s);
+    return wide ? launch<64, 2, 8, MAP>(ctx, a, s) : launch<64, 1, 8, MAP>(ctx, a, s);
 }
 
 }  // namespace
@@ -927,16 +953,10 @@ extern "C" int kvsel_kv4_attention(kvsel_ctx* ctx, const void* q, int64_t q_stri
     if ((page & (page - 1)) == 0)
         for (shift = 0; (1 << shift) < page;) ++shift;
     const AttnArgs a{(const __nv_bfloat16*)q, q_stride, Tq, Hq, Hkv, k_codes, k_scales, v_codes, v_scales, P, page, shift,
-                     seq_lens, slot_map ? slot_map : block_table, block_table != nullptr, P * page, ld, (int)reach,
+                     seq_lens, slot_map ? slot_map : block_table, P * page, ld, (int)reach,
                      dead_slot, tiles, scale, (__nv_bfloat16*)out, lse, ctx->dev_err, S, reach <= kWhole,
                      (float*)ctx->kv4_partials, (Shared*)((float*)ctx->kv4_partials + (size_t)ctx->num_sms * 4 * kPartialFloats)};
     const cudaStream_t st = (cudaStream_t)stream;
-    cudaError_t e;
-    if (D == 256)
-        e = launch<256, 1, 8>(ctx, a, st);
-    else if (D == 128)
-        e = wide ? launch<128, 2, 6>(ctx, a, st) : launch<128, 1, 8>(ctx, a, st);
-    else
-        e = wide ? launch<64, 2, 8>(ctx, a, st) : launch<64, 1, 8>(ctx, a, st);
+    const cudaError_t e = slot_map ? launch_for<true>(ctx, a, D, wide, st) : launch_for<false>(ctx, a, D, wide, st);
     return e == cudaSuccess ? KVSEL_OK : kvsel_cuda_fail(ctx, e, "kv4_attention launch");
 }
