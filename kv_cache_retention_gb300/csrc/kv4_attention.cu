@@ -51,8 +51,8 @@
 // second, small kernel, in the order of the blocks, launched as a dependent of the first
 // so that its start costs little.  (Joined by the last block to arrive instead, the join
 // took 4 to 10 us at the end of that block, and its registers came out of the loop's.)
-// Caches of a few thousand positions are not worth sharing: there a block takes whole
-// units, and there is nothing to join.
+// Where the maps reach some hundred or few thousand positions only, sharing is not worth
+// it: blocks take whole units, and there is nothing to join.
 #include <cuda_bf16.h>
 #include <limits.h>
 
@@ -66,7 +66,11 @@ namespace {
 constexpr int kTile = 32;   // tokens per stage
 constexpr unsigned kBulk = 0x80u;
 constexpr int kPartialFloats = 16 * (128 + 2) + 4;           // the largest partial result
-constexpr int64_t kWhole = 256;                              // positions up to which units are not shared
+// Positions up to which units are not shared: at most kWhole, or kWholeMany where every share gets a session or more.  A
+// share's further pieces and the join then cost more than even shares save: one session of 700 tokens took 8.9 us whole
+// and 9.5 shared, of 1000 tokens 9.7 and 9.1 (heads 4 / 2, D 64); 64 sessions of 32 / 8 heads, D 128, and 1000 tokens
+// 29 and 36 us, of 50 to 2000 tokens 39 and 42 us.
+constexpr int kWhole = 768, kWholeMany = 2048;
 constexpr int kLeast = 1;                                    // chunks per warp that a share has at least
 constexpr float kUnset = 3e38f;  // ref of a row that has seen nothing
 constexpr float kHead = 10.f;   // log2 of the weight at the reference
@@ -872,7 +876,7 @@ __global__ void __launch_bounds__(32 * W, C_blocks<D, W>()) kv4_attention_kernel
 }
 
 template <int D, int NT, int W, bool MAP>
-cudaError_t launch(kvsel_ctx* ctx, const AttnArgs& a, cudaStream_t s) {
+cudaError_t launch(kvsel_ctx* ctx, AttnArgs a, cudaStream_t s) {
     using C = Cfg<D, NT, W, MAP>;
     static_assert(C::kPartial <= kPartialFloats, "a partial result");
     auto* kernel = kv4_attention_kernel<D, NT, W, MAP>;
@@ -884,6 +888,7 @@ cudaError_t launch(kvsel_ctx* ctx, const AttnArgs& a, cudaStream_t s) {
     }
     // whole shares of Y blocks, no more than there are sessions to take whole
     const int Y = a.Hkv * a.row_tiles, most = ctx->num_sms * C_blocks<D, W>();
+    a.whole = a.max_len <= (a.S >= most / Y ? kWholeMany : kWhole);
     const int blocks = Y >= most ? most : Y * (a.whole && a.S < most / Y ? a.S : most / Y);
     kernel<<<blocks, C::kThreads, C::kSmem, s>>>(a);
     cudaError_t e = cudaGetLastError();
@@ -954,7 +959,7 @@ extern "C" int kvsel_kv4_attention(kvsel_ctx* ctx, const void* q, int64_t q_stri
         for (shift = 0; (1 << shift) < page;) ++shift;
     const AttnArgs a{(const __nv_bfloat16*)q, q_stride, Tq, Hq, Hkv, k_codes, k_scales, v_codes, v_scales, P, page, shift,
                      seq_lens, slot_map ? slot_map : block_table, P * page, ld, (int)reach,
-                     dead_slot, tiles, scale, (__nv_bfloat16*)out, lse, ctx->dev_err, S, reach <= kWhole,
+                     dead_slot, tiles, scale, (__nv_bfloat16*)out, lse, ctx->dev_err, S, 0,
                      (float*)ctx->kv4_partials, (Shared*)((float*)ctx->kv4_partials + (size_t)ctx->num_sms * 4 * kPartialFloats)};
     const cudaStream_t st = (cudaStream_t)stream;
     const cudaError_t e = slot_map ? launch_for<true>(ctx, a, D, wide, st) : launch_for<false>(ctx, a, D, wide, st);
