@@ -13,11 +13,14 @@
 //   one unit to its side.
 // Borders have 3 significant bits and scales 4, so border * s is a bf16 value too.
 //
-// Both kernels are bound by memory.  A thread takes one group: its 32 or 64 bytes of
-// a row, 8 bytes of codes, and one scale byte, of which four neighbours' are joined
-// to one store.  A block takes whole tokens, so places come from 32-bit divisions of
-// small numbers (64-bit divisions of the group's number, and codes found by seven
-// comparisons a value, took 86 us for 32768 tokens of 8 heads, 172 MB).
+// Both kernels are bound by memory.  A thread takes one group at a time: its 32 or 64
+// bytes of a row (in accesses of 32 where they lie on 32: with 16, which touch every
+// sector twice, 38 us instead of 34 below), 8 bytes of codes, and one scale byte, of which
+// four neighbours' are joined to one store.  A block takes whole tokens, so places come
+// from 32-bit divisions of small numbers.  32768 tokens of 8 heads, D 128, bf16, are 172 MB
+// a call, which takes 34 us: 5.1 TB/s, 75% of the rate of a plain copy.  Two groups' loads on
+// their way together in each thread took 36 us, and quotients by division with codes found
+// by seven comparisons a value 86 us.
 #include <cuda_bf16.h>
 #include <limits.h>
 
@@ -26,7 +29,7 @@
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 struct CacheArgs {
     const void* src[2];       // K, V rows (store)
@@ -41,6 +44,7 @@ struct CacheArgs {
     int groups;               // of a token: Hkv * per
     int tokens;               // of a block
     unsigned* err;
+    bool wide[2];             // K, V rows lie on 32 bytes
 };
 
 // Group `local` of the block's tokens: its token, and where it lies in a row and in the cache.
@@ -65,11 +69,32 @@ __device__ __forceinline__ Place place_of(const CacheArgs& a, unsigned local) {
     return p;
 }
 
+// 32 bytes.  wide: they lie on 32, and one access takes them.
+__device__ __forceinline__ void load32(const void* src, uint32_t (&u)[8], bool wide) {
+    if (wide) {
+        asm("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+            : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+            : "l"(src));
+    } else {
+        const uint4 a = __ldg(static_cast<const uint4*>(src)), b = __ldg(static_cast<const uint4*>(src) + 1);
+        u[0] = a.x, u[1] = a.y, u[2] = a.z, u[3] = a.w, u[4] = b.x, u[5] = b.y, u[6] = b.z, u[7] = b.w;
+    }
+}
+__device__ __forceinline__ void store32(void* dst, const uint32_t (&u)[8], bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]),
+                     "r"(u[5]), "r"(u[6]), "r"(u[7]), "l"(dst)
+                     : "memory");
+    } else {
+        static_cast<uint4*>(dst)[0] = make_uint4(u[0], u[1], u[2], u[3]);
+        static_cast<uint4*>(dst)[1] = make_uint4(u[4], u[5], u[6], u[7]);
+    }
+}
+
 // 16 values, and the largest magnitude (a NaN if there is one).
-__device__ __forceinline__ float load16(const __nv_bfloat16* src, float (&x)[16]) {
-    const uint4 w[2] = {__ldg(reinterpret_cast<const uint4*>(src)), __ldg(reinterpret_cast<const uint4*>(src) + 1)};
-    const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
-    uint32_t top = 0;
+__device__ __forceinline__ float load16(const __nv_bfloat16* src, float (&x)[16], bool wide) {
+    uint32_t u[8], top = 0;
+    load32(src, u, wide);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         x[2 * i] = __uint_as_float(u[i] << 16);
@@ -80,15 +105,18 @@ __device__ __forceinline__ float load16(const __nv_bfloat16* src, float (&x)[16]
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(__uint_as_float(top << 16)), "f"(__uint_as_float(top & 0xFFFF0000u)));
     return m;
 }
-__device__ __forceinline__ float load16(const float* src, float (&x)[16]) {
+__device__ __forceinline__ float load16(const float* src, float (&x)[16], bool wide) {
     float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float4 w = __ldg(reinterpret_cast<const float4*>(src) + i);
-        x[4 * i] = w.x, x[4 * i + 1] = w.y, x[4 * i + 2] = w.z, x[4 * i + 3] = w.w;
-    }
+    for (int h = 0; h < 2; ++h) {
+        uint32_t u[8];
+        load32(src + 8 * h, u, wide);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(x[i])));
+        for (int i = 0; i < 8; ++i) {
+            x[8 * h + i] = __uint_as_float(u[i]);
+            asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(x[8 * h + i])));
+        }
+    }
     return m;
 }
 
@@ -101,7 +129,7 @@ __global__ void __launch_bounds__(kThreads) kv4_store_kernel(const CacheArgs a) 
         if (!__any_sync(0xffffffffu, p.real)) continue;
         float x[16], top = 0.f;
         uint32_t byte = kKv4NanByte, w[2] = {0, 0};
-        if (p.real) top = load16(static_cast<const T*>(a.src[kv]) + (int64_t)p.token * a.stride[kv] + p.row, x);
+        if (p.real) top = load16(static_cast<const T*>(a.src[kv]) + (int64_t)p.token * a.stride[kv] + p.row, x, a.wide[kv]);
         if (p.real && top <= kKv4Max) {
             byte = kv4_scale_byte(top);
             const float s = kv4_scale(byte), r = byte ? 1.f / s : 0.f;
@@ -151,22 +179,23 @@ __global__ void __launch_bounds__(kThreads) kv4_load_kernel(const CacheArgs a) {
                 o[i] = *reinterpret_cast<const uint32_t*>(&b);
             }
         }
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.dst[kv]) + (int64_t)p.token * a.stride[kv] + p.row);
-        dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+        store32(static_cast<__nv_bfloat16*>(a.dst[kv]) + (int64_t)p.token * a.stride[kv] + p.row, o, a.wide[kv]);
     }
 }
 
-// Fills in the sizes; a block takes about two groups per thread, whole tokens.
-CacheArgs sized(CacheArgs a, int T, int Hkv, int D, int P, int page, unsigned* err) {
-    a.T = T, a.Hkv = Hkv, a.page = page, a.n_slots = P * page, a.err = err;
+// Fills in the sizes.  A block takes whole tokens, about four groups per thread; one where few blocks would be left (36
+// tokens of 8 heads: 2.0 us a call with one, 2.6 with two; 32768 tokens: 40 us with one, 34 with four, 35 with eight).
+CacheArgs sized(CacheArgs a, const kvsel_ctx* ctx, int esize, int T, int Hkv, int D, int P, int page) {
+    a.T = T, a.Hkv = Hkv, a.page = page, a.n_slots = P * page, a.err = ctx->dev_err;
     a.page_shift = -1;
     if ((page & (page - 1)) == 0)
         for (a.page_shift = 0; (1 << a.page_shift) < page;) ++a.page_shift;
     a.per = D / kKv4Group;
     a.per_shift = D == 64 ? 2 : D == 128 ? 3 : 4;
     a.groups = Hkv * a.per;
-    a.tokens = 2 * kThreads / a.groups;
+    for (int i = 0; i < 2; ++i)
+        a.wide[i] = ((reinterpret_cast<uintptr_t>(a.src[i] ? a.src[i] : a.dst[i]) | (uintptr_t)(a.stride[i] * esize)) & 31u) == 0;
+    a.tokens = ((int64_t)T * a.groups > (int64_t)ctx->num_sms * 16 * kThreads ? 4 : 1) * kThreads / a.groups;
     if (a.tokens < 1) a.tokens = 1;
     return a;
 }
@@ -209,7 +238,7 @@ extern "C" int kvsel_kv4_store(kvsel_ctx* ctx, const void* k, const void* v, int
                k_scales, v_codes, v_scales, P, page);
     if (rc || T == 0) return rc;
     const CacheArgs a = sized({{k, v}, {nullptr, nullptr}, {k_stride, v_stride}, {k_codes, v_codes}, {k_scales, v_scales}, slots},
-                              T, Hkv, D, P, page, ctx->dev_err);
+                              ctx, src_dtype == KVSEL_BF16 ? 2 : 4, T, Hkv, D, P, page);
     if (src_dtype == KVSEL_BF16)
         kv4_store_kernel<__nv_bfloat16><<<grid_of(a), kThreads, 0, (cudaStream_t)stream>>>(a);
     else
@@ -231,7 +260,7 @@ extern "C" int kvsel_kv4_load(kvsel_ctx* ctx, const uint8_t* k_codes, const uint
     const CacheArgs a = sized({{nullptr, nullptr}, {k, v}, {k_stride, v_stride},
                                {const_cast<uint8_t*>(k_codes), const_cast<uint8_t*>(v_codes)},
                                {const_cast<uint8_t*>(k_scales), const_cast<uint8_t*>(v_scales)}, slots},
-                              T, Hkv, D, P, page, ctx->dev_err);
+                              ctx, 2, T, Hkv, D, P, page);
     kv4_load_kernel<<<grid_of(a), kThreads, 0, (cudaStream_t)stream>>>(a);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? KVSEL_OK : kvsel_cuda_fail(ctx, e, "kv4_load launch");

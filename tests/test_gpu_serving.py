@@ -226,6 +226,41 @@ def test_store_strided_rows_and_every_bf16(ctx):
         assert np.array_equal(f64(b), ref.dequantise(*ref.quantise(f64(x))))
 
 
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+@pytest.mark.parametrize("T", [5, 6001])
+def test_store_and_load_rows_on_16_bytes(ctx, dtype, T):
+    """Rows that lie on 16 bytes and not on 32 (K's, V's or both), few tokens and many, are stored like others."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    Hkv, D, page = 8, 64, 16
+    k, v = (torch.randn((T, Hkv, D), generator=g, device="cuda").to(dtype) for _ in range(2))
+    step = 16 // k.element_size()
+    slots = torch.randperm(T + 30, generator=g, device="cuda")[:T].to(I32)
+    P = (T + 30 + page - 1) // page
+
+    def shifted(x, by):
+        y = torch.zeros(x.numel() + by, dtype=x.dtype, device="cuda")[by:].view(x.shape)
+        return y.copy_(x)
+
+    want = _cache(P, Hkv, page, D)
+    ctx.kv4_store(k, v, slots, *want)
+    first = torch.randint(0, T, (5,), generator=g, device="cuda").tolist()
+    for i in first:
+        rc, rs = ref.quantise(f64(k[i]))
+        n = int(slots[i])
+        assert np.array_equal(want[0][n // page, :, n % page].cpu().numpy(), rc)
+        assert np.array_equal(want[1][n // page, :, n % page].cpu().numpy(), rs)
+    kb, vb = torch.empty((T, Hkv, D), dtype=BF, device="cuda"), torch.empty((T, Hkv, D), dtype=BF, device="cuda")
+    ctx.kv4_load(*want, slots, kb, vb)
+    for bk, bv in ((step, 0), (0, step), (step, step)):
+        got = _cache(P, Hkv, page, D)
+        ctx.kv4_store(shifted(k, bk), shifted(v, bv), slots, *got)
+        assert all(torch.equal(i, j) for i, j in zip(got, want))
+        ko, vo = shifted(torch.zeros_like(kb), bk and 8), shifted(torch.zeros_like(vb), bv and 8)
+        ctx.kv4_load(*want, slots, ko, vo)
+        assert torch.equal(ko, kb) and torch.equal(vo, vb)
+    ctx.check_device()
+
+
 def test_every_code_and_scale_loads_exactly(ctx):
     codes = np.arange(256, dtype=np.uint8).reshape(4, 64)[None].repeat(256, 0).reshape(1024, 1, 1, 64)
     scales = np.repeat(np.arange(256, dtype=np.uint8), 4)[:, None].repeat(8, 1).reshape(1024, 1, 1, 8)
