@@ -35,8 +35,9 @@
 // multiplications and 33 the products, and issues on 60% of the cycles.  Measured: 36
 // sessions of 32 / 8 heads pruned to a quarter, 278 MB: 81.6 us (3.4 TB/s); 16 sessions
 // of 4 query rows, 306 MB: 109 us (2.8 TB/s); one of 92160 tokens, 106 MB: 34 us, of
-// which some 6 us go by before the first tokens arrive and 5 us with the join.  More
-// warps per SM (10 a block, 96 registers) took 104, 115 and 40 us.
+// which some 6 us go by before the first tokens arrive and 5 us with the join; one of 2048
+// tokens, 9.2 us.  More warps per SM (10 a block, 96 registers) took 104, 115 and 40 us for
+// the first three.
 //
 // One wave of two blocks per SM.  The work is the chunks of 32 positions of every
 // session, laid end to end; it is cut into equal, contiguous shares, found from the
@@ -906,6 +907,8 @@ cudaError_t launch(kvsel_ctx* ctx, AttnArgs a, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT, MAP>, a);
 }
 
+// Two blocks of 8 warps per SM, or of 6 where two row tiles of D = 128 need the registers (16 sessions of 16 rows: 117 us;
+// 136 us with 8 warps and spilled registers); D = 256: one block.
 template <bool MAP>
 cudaError_t launch_for(kvsel_ctx* ctx, const AttnArgs& a, int D, bool wide, cudaStream_t s) {
     if (D == 256) return launch<256, 1, 8, MAP>(ctx, a, s);
@@ -951,7 +954,9 @@ extern "C" int kvsel_kv4_attention(kvsel_ctx* ctx, const void* q, int64_t q_stri
         off16(v_scales))
         return kvsel_fail(ctx, KVSEL_ERR_ALIGN, "kv4_attention: q, its stride, out and the caches must be 16-byte aligned");
     const int R = Tq * (Hq / Hkv);
-    const bool wide = R > 8 && D != 256;  // two tiles of 8 rows share the decoded K and V
+    // Two tiles of 8 rows share the decoded K and V where there are more than 8 rows (16 sessions of 16 rows: 109 us, and
+    // 151 us with a tile each); for D = 256 their sums would take all registers.
+    const bool wide = R > 8 && D != 256;
     const int tiles = (R + (wide ? 16 : 8) - 1) / (wide ? 16 : 8);
     if ((int64_t)Hkv * tiles > 65535) return kvsel_fail(ctx, KVSEL_ERR_UNSUPPORTED, "kv4_attention: too many rows");
     int shift = -1;

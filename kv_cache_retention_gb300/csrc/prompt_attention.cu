@@ -23,14 +23,26 @@
 // of 2^-9 per weight is random and comes to about the output's own rounding.
 //
 // 384 threads: warp 0 loads (TMA), warps 1 and 2 issue the MMAs of one tile each, warp 3
-// looks over the V tiles of the diagonal (below), warps 4-7 and 8-11 are the softmax of the two tiles, a
-// row per thread.  TMEM: S of tile 0 and 1 at columns 0 and 128, O at 256 and 384.
+// hands out the units and looks over the V tiles of the diagonal (below), warps 4-7 and
+// 8-11 are the softmax of the two tiles, a row per thread.  TMEM: S of tile 0 and 1 at columns 0 and 128, O at 256 and 384.
 //
 // Masked places.  A weight of zero does not hide a NaN or an infinity in V.  Key tiles
 // below the diagonal are seen by every row of a tile, so only the first two tiles of a
 // block's pass hold values that some rows must not see; there warp 3 sets such values
 // to zero in shared memory before the product, and if there were any, each row adds
 // those it does see to its output at the end (what the sum would be: infinite or NaN).
+//
+// Blocks are as many as there are units, the longest first, but one per SM runs: when its
+// unit is done it claims the unit of a block that has not been launched yet (cluster
+// launch control), and the next unit's loads and first products run beside the end of the
+// last.  With a block per unit 4096 tokens took 118 us, 16384 tokens 1.78 ms.
+//
+// What bounds it: the tensor cores within a unit (128 keys for both tiles take 1.5 us, 91%
+// of the rate of a large library product; both operands of S come from shared memory, at
+// its bandwidth's limit), and some 5 us a unit in which they wait: the first softmax, the
+// last product, the output.  Measured for D = 128: 16384 tokens of 40 / 8 heads 1.71 ms
+// (1.6 PFLOP/s counting what the mask leaves, 86% of that rate), 4096 of 32 / 8 heads 114
+// us (65%), 9 prompts of 14700 tokens together 313 us (64%).
 //
 // Every wait is bounded (1 s); on a timeout the block flags KVSEL_ERR_TIMEOUT in the
 // device error word, drains its own copies and MMAs, frees TMEM and returns.
@@ -236,7 +248,7 @@ __device__ __forceinline__ int at_v(int i, int n) { return i == n - 1 ? 2 * n - 
 // Two issuers on two SM sub-partitions: what one spends on barriers, between the softmax's instructions, passes
 // while the other's products run.  They take turns, so that one tile's products run beside the other's softmax.
 // One copy of the code for both, and one of each run of MMAs: with a copy per tile the kernel's loops passed the
-// instruction cache (4096 tokens: 135 us).
+// instruction cache (16384 tokens: 1.92 ms, with one copy 1.73 ms).
 template <int D>
 __device__ __forceinline__ void issue_tiles(typename Cfg<D>::Tail& t, const uint8_t* sq, const uint8_t* ring, int tile, int lane,
                                             volatile int* abort_flag, unsigned* err) {
