@@ -33,15 +33,15 @@
 // What bounds it: instructions, before memory.  For D = 128 a warp executes about 850
 // for 32 tokens of one kv head, 4.6 KB, of which 270 are the conversions and the scales'
 // multiplications and 33 the products, and issues on 60% of the cycles.  Measured: 36
-// sessions of 32 / 8 heads pruned to a quarter, 278 MB: 81.6 us (3.4 TB/s); 16 sessions
-// of 4 query rows, 306 MB: 109 us (2.8 TB/s); one of 92160 tokens, 106 MB: 34 us, of
+// sessions of 32 / 8 heads pruned to a quarter, 278 MB: 80 us (3.5 TB/s); 16 sessions
+// of 4 query rows, 306 MB: 98 us (3.1 TB/s); one of 92160 tokens, 106 MB: 34 us, of
 // which some 6 us go by before the first tokens arrive and 5 us with the join; one of 2048
 // tokens, 9.2 us.  More warps per SM (10 a block, 96 registers) took 104, 115 and 40 us for
-// the first three.
+// the first three when these took 85, 117 and 36.
 //
 // One wave of two blocks per SM.  The work is the chunks of 32 positions of every
-// session, laid end to end; it is cut into equal, contiguous shares, found from the
-// lengths on the device, so that sessions of uneven length keep every SM busy to the end
+// session, laid end to end with some for the start of each; it is cut into equal,
+// contiguous shares, found from the lengths on the device, so that sessions of uneven length keep every SM busy to the end
 // (with blocks for a fixed part of a session, 16 uneven sessions took 146 us, 92160
 // tokens of one 38 us).  A share is a few pieces of sessions, and neighbouring blocks
 // take it for one kv head (and row tile) each: the heads' rows of a page lie side by
@@ -72,6 +72,10 @@ constexpr int kPartialFloats = 16 * (128 + 2) + 4;           // the largest part
 // and 9.5 shared, of 1000 tokens 9.7 and 9.1 (heads 4 / 2, D 64); 64 sessions of 32 / 8 heads, D 128, and 1000 tokens
 // 29 and 36 us, of 50 to 2000 tokens 39 and 42 us.
 constexpr int kWhole = 768, kWholeMany = 2048;
+// Chunks that the start of another session within a share counts as: its queries, first slots and tokens, and the join of
+// the warps.  With 0, 16 sessions of 301 to 32768 tokens and 4 rows took 110 us and 8 of 300 to 8000 tokens 25 us; with 8,
+// 105 and 21; with 20, 98 and 20; with 32, 99 and 21.
+constexpr int kStart = 20;
 constexpr int kLeast = 1;                                    // chunks per warp that a share has at least
 constexpr float kUnset = 3e38f;  // ref of a row that has seen nothing
 constexpr float kHead = 10.f;   // log2 of the weight at the reference
@@ -362,9 +366,10 @@ __global__ void __launch_bounds__(32 * W, C_blocks<D, W>()) kv4_attention_kernel
         asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;\nfence.mbarrier_init.release.cluster;" ::"r"(saddr(&w.landed[lane])) : "memory");
 
     // ---- the block's share: `quota` chunks from `start` on ----
-    // Sums of the sessions' chunks up to and with each thread's session, kThreads sessions at a time.
+    // Session s takes kStart + chunks places, the first session's start lying before place 0.
+    // Sums of the sessions' places up to and with each thread's session, kThreads sessions at a time.
     auto scan = [&](int s, long long& upto) {
-        long long v = s < a.S ? chunks_of(length_of(a, s)) : 0;
+        long long v = s < a.S ? kStart + chunks_of(length_of(a, s)) : 0;
         const long long own = v;
 #pragma unroll
         for (int k = 1; k < 32; k <<= 1) {
@@ -394,7 +399,7 @@ __global__ void __launch_bounds__(32 * W, C_blocks<D, W>()) kv4_attention_kernel
     if (a.whole) {                                   // sessions share, share + shares, ...
         if (threadIdx.x == 0) part.pos = share, part.end = a.S, part.quota = shares;
     } else {
-        long long total = 0, upto = 0;
+        long long total = -kStart, upto = 0;
         longlong2 mine = make_longlong2(0, 0);
         for (int s0 = 0; s0 < a.S; s0 += kThreads) {
             mine = scan(s0 + threadIdx.x, upto);
@@ -403,7 +408,7 @@ __global__ void __launch_bounds__(32 * W, C_blocks<D, W>()) kv4_attention_kernel
         long long quota = total < (1ll << 31) ? (unsigned)(total + shares - 1) / (unsigned)shares : (total + shares - 1) / shares;
         quota = max(quota, (long long)kWarps * kLeast);
         const long long start = share * quota, end = min(start + quota, total);
-        for (long long s0 = 0, run = 0; s0 < a.S; s0 += kThreads) {
+        for (long long s0 = 0, run = -kStart; s0 < a.S; s0 += kThreads) {
             if (a.S > kThreads) mine = scan((int)s0 + threadIdx.x, upto);
             const long long from = run + upto - mine.x;
             if (mine.x && from <= start && start < from + mine.x) part.session = (int)s0 + threadIdx.x, part.before = from;
@@ -423,24 +428,25 @@ __global__ void __launch_bounds__(32 * W, C_blocks<D, W>()) kv4_attention_kernel
             part.pos += part.quota;
             return;
         }
-        const long long before = part.before, q = part.quota;
+        const long long first = part.before + kStart, q = part.quota;  // first: of the session's own chunks
         const int chunks = chunks_of(length_of(a, part.session));
+        if (part.end <= first) return;                 // only the place of its start is left
         int share1;
-        if (before + chunks < (1ll << 31)) {
-            x.share0 = (int)((unsigned)before / (unsigned)q);
-            share1 = (int)((unsigned)(before + chunks - 1) / (unsigned)q);
+        if (first + chunks < (1ll << 31)) {
+            x.share0 = (int)((unsigned)first / (unsigned)q);
+            share1 = (int)((unsigned)(first + chunks - 1) / (unsigned)q);
         } else {
-            x.share0 = (int)(before / q);
-            share1 = (int)((before + chunks - 1) / q);
+            x.share0 = (int)(first / q);
+            share1 = (int)((first + chunks - 1) / q);
         }
         x.session = part.session;
-        x.chunk0 = (int)(part.pos - before);
-        x.chunk1 = (int)min((long long)chunks, part.end - before);
+        x.chunk0 = (int)max(part.pos - first, 0ll);
+        x.chunk1 = (int)min((long long)chunks, part.end - first);
         x.sharers = share1 - x.share0 + 1;
-        x.late = before != x.share0 * q;
+        x.late = part.before > x.share0 * q;
         if (x.sharers > 1 && x.share0 == share) a.shared[blockIdx.x] = Shared{x.sharers, x.session, x.late};
-        part.pos = before + x.chunk1;
-        if (x.chunk1 == chunks) part.before += chunks, ++part.session;
+        part.pos = first + x.chunk1;
+        if (x.chunk1 == chunks) part.before = part.pos, ++part.session;
     };
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -457,7 +463,7 @@ __global__ void __launch_bounds__(32 * W, C_blocks<D, W>()) kv4_attention_kernel
         if ((int)gridDim.x >= Y || (y += gridDim.x) >= Y) break;
         __syncthreads();                             // the next y, over the one share's sessions again
         if (threadIdx.x == 0) {
-            part.pos = 0, part.session = 0, part.before = 0;
+            part.pos = 0, part.session = 0, part.before = -kStart;
             next_piece(number + 1);
         }
         __syncthreads();
@@ -954,8 +960,8 @@ extern "C" int kvsel_kv4_attention(kvsel_ctx* ctx, const void* q, int64_t q_stri
         off16(v_scales))
         return kvsel_fail(ctx, KVSEL_ERR_ALIGN, "kv4_attention: q, its stride, out and the caches must be 16-byte aligned");
     const int R = Tq * (Hq / Hkv);
-    // Two tiles of 8 rows share the decoded K and V where there are more than 8 rows (16 sessions of 16 rows: 109 us, and
-    // 151 us with a tile each); for D = 256 their sums would take all registers.
+    // Two tiles of 8 rows share the decoded K and V where there are more than 8 rows (16 sessions of 16 rows: 151 us
+    // with a tile each, 109 with two); for D = 256 their sums would take all registers.
     const bool wide = R > 8 && D != 256;
     const int tiles = (R + (wide ? 16 : 8) - 1) / (wide ? 16 : 8);
     if ((int64_t)Hkv * tiles > 65535) return kvsel_fail(ctx, KVSEL_ERR_UNSUPPORTED, "kv4_attention: too many rows");
