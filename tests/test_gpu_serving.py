@@ -364,6 +364,7 @@ ATTENTION = [
     (9, 3, 8, 4, 128, 16, [2100, 0, 1, 2100, 40, 0, 1000, 3, 2222]),
     (40, 1, 16, 8, 128, 16, [1 + 50 * i for i in range(40)]),           # sessions of their own blocks, up to 2048
     (3, 1, 2, 1, 128, 16, [767, 768, 769]),
+    (2, 1, 4, 2, 128, 48, [1500, 950]),
     (160, 1, 4, 2, 64, 16, [(i * 397) % 2040 for i in range(160)]),
 ]
 
@@ -553,6 +554,52 @@ def test_attention_long_cache_past_32_bits(ctx):
     ctx.check_device()
     assert torch.equal(*outs)
     assert np.array_equal(f64(back[0]), ref.dequantise(*ref.quantise(f64(x))))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_over_runs_of_slots(ctx, D):
+    """Maps of consecutive slots that start anywhere, whole and with gaps: taken by bulk copies or one by one."""
+    g = torch.Generator(device="cuda").manual_seed(D)
+    S, Hq, Hkv, P, page = 7, 4, 2, 2, 1024
+    cache = _random_cache(g, P, Hkv, page, D)
+    q = torch.randn((S, 2, Hq, D), generator=g, device="cuda").to(BF)
+    j = np.arange(640)
+    slots = np.stack([j + 5 * 64 + s for s in range(S)])  # across the pages' border, at starts of every alignment
+    live = np.ones_like(slots, bool)
+    live[5, 100:103] = live[6, ::5] = False
+    lens = [640, 639, 500, 33, 600, 640, 640]
+    out, lse = torch.empty_like(q), torch.empty((S, 2, Hq), device="cuda")
+    ctx.kv4_attention(q, *cache, _i32(lens), out, slot_map=_i32(np.where(live, slots, -1)), lse=lse)
+    ctx.check_device()
+    _check_attention(out, lse, _attention_reference(q, cache, lens, slots, live, D ** -0.5))
+
+
+def test_attention_graphs_in_turn(ctx):
+    """Two captured calls of one context (shared partial results), replayed in turn with eager calls between them."""
+    g = torch.Generator(device="cuda").manual_seed(31)
+    cases = []
+    for S, Tq, Hq, Hkv, D, n in ((2, 1, 8, 2, 128, 4000), (5, 3, 6, 1, 64, 2500)):
+        rows = n // 16 + 1
+        cache = _random_cache(g, S * rows, Hkv, 16, D)
+        table = torch.randperm(S * rows, generator=g, device="cuda").to(I32).view(S, rows).contiguous()
+        q = torch.randn((S, Tq, Hq, D), generator=g, device="cuda").to(BF)
+        lens = torch.randint(n // 2, n, (S,), generator=g, device="cuda").to(I32)
+        out, lse = torch.empty_like(q), torch.empty((S, Tq, Hq), device="cuda")
+        call = lambda q=q, cache=cache, lens=lens, out=out, table=table, lse=lse: ctx.kv4_attention(  # noqa: E731
+            q, *cache, lens, out, block_table=table, lse=lse)
+        call()
+        torch.cuda.synchronize()
+        want = out.clone(), lse.clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        cases.append((graph, call, out, lse, want))
+    for i in range(6):
+        for graph, call, out, lse, want in cases:
+            out.fill_(7), lse.fill_(7)
+            graph.replay() if (i + (out is cases[0][2])) % 3 else call()
+            assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    ctx.check_device()
 
 
 def test_attention_is_deterministic(ctx):
