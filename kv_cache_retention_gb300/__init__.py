@@ -325,6 +325,8 @@ def _rows(t, lead, dtype, device, name):
     try:
         if t.dtype is dtype and t.get_device() == device:
             shape, st = t.shape, t.stride()
+            if lead == 1 and len(st) == 3 and st[2] == 1 and st[1] == shape[2] and shape[0] > 1:
+                return t.data_ptr(), st[0]  # the common form, and the quickest
             if len(shape) == lead + 2:
                 heads, D = shape[-2:]
                 if t.is_contiguous():
@@ -687,11 +689,10 @@ class Context:
 
     def _kv4_cache(self, k_codes, k_scales, v_codes, v_scales, D):
         """Pointers of the 4-bit caches [P][Hkv][page][D/2] and [P][Hkv][page][D/16] and their P, Hkv, page."""
-        shape = k_codes.shape
+        shape, scales = k_codes.shape, k_scales.shape
         if len(shape) != 4 or shape[3] * 2 != D:
             raise ValueError(f"k_codes: expected [P][Hkv][page][{D // 2}], got {tuple(shape)}")
         P, Hkv, page, _ = shape
-        scales = k_scales.shape
         if v_codes.shape != shape:
             raise ValueError(f"v_codes: expected {tuple(shape)}, got {tuple(v_codes.shape)}")
         if scales != (P, Hkv, page, D // 16) or v_scales.shape != scales:

@@ -994,3 +994,26 @@ def test_two_contexts_on_two_streams(ctx):
         c.check_device()
         assert all(torch.equal(i, j) for i, j in zip(a, b))
     other.close()
+
+
+def test_prompt_from_a_graph(ctx):
+    """Captured once, replayed on other prompts of other lengths in the same buffers."""
+    g = torch.Generator(device="cuda").manual_seed(33)
+    T, Hq, Hkv, D = 900, 6, 2, 128
+    x = torch.randn((T, Hq + 2 * Hkv, D), generator=g, device="cuda").to(BF)
+    q, k, v = x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:]
+    cu = _i32([0, 300, 900])
+    out, lse = torch.empty((T, Hq, D), dtype=BF, device="cuda"), torch.empty((T, Hq), device="cuda")
+    ctx.prompt_attention(q, k, v, cu, out, lse=lse)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ctx.prompt_attention(q, k, v, cu, out, lse=lse)
+    for starts in ([0, 300, 900], [0, 1, 900], [0, 512, 640], [20, 20, 777]):
+        x.copy_(torch.randn(x.shape, generator=g, device="cuda").to(BF))
+        cu.copy_(_i32(starts))
+        out.fill_(9)
+        graph.replay()
+        _check_prompt(q, k, v, starts, D ** -0.5, out, lse)
+        assert (out[:starts[0]] == 9).all() and (out[starts[-1]:] == 9).all()
+    ctx.check_device()
