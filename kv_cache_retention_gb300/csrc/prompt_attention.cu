@@ -6,7 +6,7 @@
 //   lse = ln sum_j e^(scale q_i . k_j).
 //
 // A unit of work is one query head and 256 consecutive rows of one sequence, as two tiles
-// of 128 rows (TMEM lanes), and goes once over the keys from the diagonal down, 128 at
+// of 128 rows (TMEM lanes; 128 rows and one tile where there are few units), and goes once over the keys from the diagonal down, 128 at
 // a time:
 //   S = Q K^T   tcgen05.mma, both operands from shared memory, 128 fp32 columns a tile
 //   P = 2^(S sc - ref) in bf16, written over S in TMEM
@@ -57,7 +57,6 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kTile = 128;              // rows of a tile, keys of a step
-constexpr int kUnit = 2 * kTile;        // rows of a block
 constexpr int kThreads = 384;
 constexpr float kSlack = 8.f;           // how far (log2) a row's maximum may pass its reference
 constexpr uint64_t kWaitNs = 1000000000ull;
@@ -76,6 +75,7 @@ struct PromptArgs {
     int64_t v_stride;
     const int32_t* cu;
     int S, T, Hq, Hkv, n_virtual;
+    int unit;               // rows of a unit: two tiles, or one
     float scale2;           // scale * log2(e)
     __nv_bfloat16* out;
     float* lse;
@@ -90,7 +90,7 @@ struct Cfg {
     static constexpr int kOut = 8 * 32 * 128;              // 32 rows of 64 dims for each softmax warp, on their way out
     // A unit of work, as warp 3 hands it out; n == 0: there are no more.
     struct Unit {
-        int first, len, row0, head, n;
+        int first, len, row0, head, n, two;  // two: it has rows in its second tile
     };
     struct Tail {
         uint4 claimed;  // the answer of a claim
@@ -263,7 +263,7 @@ __device__ __forceinline__ void issue_tiles(typename Cfg<D>::Tail& t, const uint
     for (uint32_t u = 0; ok; ++u) {
         if (!(ok = wait_warp(&t.unit_full[u & 1], (u >> 1) & 1, abort_flag, err))) break;
         const int n = t.unit[u & 1].n;
-        const bool two = t.unit[u & 1].row0 + kTile < t.unit[u & 1].len;
+        const bool two = t.unit[u & 1].two;
         __syncwarp();
         if (lead) mbar_arrive(&t.unit_empty[u & 1]);
         if (n == 0) break;
@@ -350,16 +350,16 @@ __device__ __forceinline__ void issue_tiles(typename Cfg<D>::Tail& t, const uint
 }
 
 // ---- units of work ---------------------------------------------------------
-// Block b's unit: query head b % Hq and a row tile of 256 rows of one sequence.  Row tiles are numbered by their
-// sequence's start: sequence s has the numbers from cu[s] / 256 + s on, which leaves it at least ceil(length / 256) of
-// them (some stay empty); the last numbers come first, a sequence's longest rows before its others.  n = 0: no rows.
+// Block b's unit: query head b % Hq and a row tile of a.unit rows of one sequence.  Row tiles are numbered by their
+// sequence's start: sequence s has the numbers from cu[s] / a.unit + s on, which leaves it at least ceil(length / a.unit)
+// of them (some stay empty); the last numbers come first, a sequence's longest rows before its others.  n = 0: no rows.
 template <int D>
 __device__ __forceinline__ typename Cfg<D>::Unit unit_of(const PromptArgs& a, uint32_t block, int lane) {
     const int number = a.n_virtual - 1 - (int)(block / a.Hq);
     int lo = 0, size = a.S;                       // the last sequence whose first number is not above lies in [lo, lo + size)
     while (size > 1) {
         const int piece = (size + 31) / 32, i = lane * piece;
-        const bool below = i < size && (lane == 0 || __ldg(a.cu + lo + i) / kUnit + lo + i <= number);
+        const bool below = i < size && (lane == 0 || __ldg(a.cu + lo + i) / a.unit + lo + i <= number);
         const int last = 31 - __clz(__ballot_sync(0xffffffffu, below));
         lo += last * piece;
         size = min(piece, size - last * piece);
@@ -368,11 +368,12 @@ __device__ __forceinline__ typename Cfg<D>::Unit unit_of(const PromptArgs& a, ui
     const int stop = __ldg(a.cu + lo + 1);
     w.first = __ldg(a.cu + lo);
     w.len = w.first < 0 || stop < w.first ? 0 : min(stop, a.T) - w.first;
-    const int tile = number - (w.first / kUnit + lo);
-    const bool rows = tile >= 0 && (int64_t)tile * kUnit < w.len;
-    w.row0 = rows ? tile * kUnit : 0;
+    const int tile = number - (w.first / a.unit + lo);
+    const bool rows = tile >= 0 && (int64_t)tile * a.unit < w.len;
+    w.row0 = rows ? tile * a.unit : 0;
     w.head = (int)(block % a.Hq);
-    w.n = !rows ? 0 : 2 * tile + (w.row0 + kTile < w.len ? 2 : 1);
+    w.two = a.unit > kTile && w.row0 + kTile < w.len;
+    w.n = rows ? w.row0 / kTile + 1 + w.two : 0;
     return w;
 }
 
@@ -464,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const typename C::Unit w = t.unit[u & 1];
                 mbar_arrive(&t.unit_empty[u & 1]);
                 if (w.n == 0) break;
-                const int g = w.head / (a.Hq / a.Hkv), tiles = w.row0 + kTile < w.len ? 2 : 1;
+                const int g = w.head / (a.Hq / a.Hkv), tiles = 1 + w.two;
                 if (u && !(ok = wait_phase(&t.q_empty, (u - 1) & 1, abort_flag, a.err))) break;
                 mbar_expect_tx(&t.q_full, tiles * C::kBytes);
                 for (int x = 0; x < tiles; ++x)
@@ -571,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!(ok = wait_warp(&t.unit_full[u & 1], (u >> 1) & 1, abort_flag, a.err))) break;
     const typename C::Unit w = t.unit[u & 1];
     __syncwarp();
-    const bool two = w.row0 + kTile < w.len;
+    const bool two = w.two;
     const int steps = w.n == 0 || (x == 1 && !two) ? 0 : x == 0 && two ? w.n - 1 : w.n;
     float ref = 0.f;
     float2 sum = make_float2(0.f, 0.f);
@@ -754,12 +755,16 @@ extern "C" int kvsel_prompt_attention(kvsel_ctx* ctx, const void* q, const void*
     auto off16 = [](const void* p, int64_t stride) { return (reinterpret_cast<uintptr_t>(p) & 15u) || (stride * 2) % 16; };
     if (off16(q, q_stride) || off16(k, k_stride) || off16(v, v_stride) || off16(out, 0))
         return kvsel_fail(ctx, KVSEL_ERR_ALIGN, "prompt_attention: q, k, v, out and the strides must be 16-byte aligned");
-    const int n_virtual = T / kUnit + S;
+    // Units of one tile where the SMs would not run out of those: nothing is shared, and a step is shorter with no other
+    // tile's between (4096 tokens of 4 heads, D 128: 50 us and 54 with two tiles; of 8 heads, 136 units of two tiles, 67 and
+    // 54).
+    const int unit = (int64_t)(T / (2 * kTile) + S) * Hq <= ctx->num_sms / 2 ? kTile : 2 * kTile;
+    const int n_virtual = T / unit + S;
     if ((int64_t)n_virtual * Hq > INT_MAX) return kvsel_fail(ctx, KVSEL_ERR_UNSUPPORTED, "prompt_attention: too many rows");
     CUtensorMap mq, mk, mv;
     if (!make_map(&mq, q, T, Hq, D, q_stride) || !make_map(&mk, k, T, Hkv, D, k_stride) || !make_map(&mv, v, T, Hkv, D, v_stride))
         return kvsel_fail(ctx, KVSEL_ERR_CUDA, "prompt_attention: tensor map encoding failed");
-    const PromptArgs a{(const __nv_bfloat16*)v, v_stride, cu_seqlens, S, T, Hq, Hkv, n_virtual, scale * kLog2e,
+    const PromptArgs a{(const __nv_bfloat16*)v, v_stride, cu_seqlens, S, T, Hq, Hkv, n_virtual, unit, scale * kLog2e,
                        (__nv_bfloat16*)out, lse, ctx->dev_err};
     const cudaError_t e = D == 64 ? launch<64>(ctx, mq, mk, mv, a, (cudaStream_t)stream) : launch<128>(ctx, mq, mk, mv, a, (cudaStream_t)stream);
     return e == cudaSuccess ? KVSEL_OK : kvsel_cuda_fail(ctx, e, "prompt_attention launch");

@@ -660,6 +660,8 @@ PROMPT = [
     ([1] * 70, 2, 1, 128),
     ([640, 3, 77, 129], 16, 2, 64),
     ([1100], 10, 2, 128),
+    ([700, 0, 128, 257], 9, 3, 64),        # units of one tile of 128 rows, and with more heads of two
+    ([700, 0, 128, 256, 1], 16, 4, 64),
 ]
 
 
@@ -679,11 +681,12 @@ def test_prompt_matches_reference(ctx, lens, Hq, Hkv, D, fused):
     _check_prompt(q, k, v, cu, D ** -0.5, out, lse)
 
 
-def test_prompt_rows_outside_sequences_stay(ctx):
+@pytest.mark.parametrize("Hq,Hkv", [(4, 2), (40, 4)])
+def test_prompt_rows_outside_sequences_stay(ctx, Hq, Hkv):
     """A gap before the first sequence and padding behind the last: outputs there are left, and NaN inputs there and in
     later tokens reach no row."""
     g = torch.Generator(device="cuda").manual_seed(3)
-    T, Hq, Hkv, D = 400, 4, 2, 128
+    T, D = 400, 128
     qkv = torch.randn((T, Hq + 2 * Hkv, D), generator=g, device="cuda").to(BF)
     qkv[:7] = float("nan")
     qkv[330:] = float("inf")
@@ -697,11 +700,12 @@ def test_prompt_rows_outside_sequences_stay(ctx):
     _check_prompt(q, k, v, cu, D ** -0.5, out, lse)
 
 
-def test_prompt_future_nan_is_not_seen(ctx):
+@pytest.mark.parametrize("H", [2, 50])
+def test_prompt_future_nan_is_not_seen(ctx, H):
     """A NaN or infinite key or value reaches the rows at and behind it, and none before it (same tile)."""
     g = torch.Generator(device="cuda").manual_seed(4)
     T, D = 300, 128
-    q, k, v = (torch.randn((T, 2, D), generator=g, device="cuda").to(BF) for _ in range(3))
+    q, k, v = (torch.randn((T, H, D), generator=g, device="cuda").to(BF) for _ in range(3))
     for bad in (float("nan"), float("inf")):
         k2, v2 = k.clone(), v.clone()
         k2[141, 0, 5], v2[205, 1, 7] = float("nan"), bad
@@ -715,15 +719,16 @@ def test_prompt_future_nan_is_not_seen(ctx):
 
 
 @pytest.mark.parametrize("qs,scale", [(1.0, 20.0), (60.0, 1.0), (1e-20, 1.0), (2.0 ** 50, 2.0 ** -50)])
-def test_prompt_extreme_logits(ctx, qs, scale):
+@pytest.mark.parametrize("H", [2, 30])
+def test_prompt_extreme_logits(ctx, H, qs, scale):
     """Logits of thousands (one weight near 1), rising along the sequence, and of nothing (the mean)."""
     g = torch.Generator(device="cuda").manual_seed(13)
     T, D = 700, 64
-    q, k, v = (torch.randn((T, 2, D), generator=g, device="cuda") for _ in range(3))
+    q, k, v = (torch.randn((T, H, D), generator=g, device="cuda") for _ in range(3))
     q = (q * qs).to(BF)
     k = (k * torch.linspace(0.1, 3, T, device="cuda")[:, None, None]).to(BF)
     v = v.to(BF)
-    out, lse = torch.empty_like(v), torch.empty((T, 2), device="cuda")
+    out, lse = torch.empty_like(v), torch.empty((T, H), device="cuda")
     ctx.prompt_attention(q, k, v, _i32([0, T]), out, lse=lse, scale=scale)
     ctx.check_device()
     _check_prompt(q, k, v, [0, T], scale, out, lse)
@@ -761,16 +766,17 @@ def test_prompt_bad_sequences_are_flagged(ctx, cu):
     assert (out[T:] == 9).all() and (lse[T:] == 9).all()
 
 
-def test_prompt_minus_infinite_logits_of_the_last_keys(ctx):
+@pytest.mark.parametrize("H", [1, 50])
+def test_prompt_minus_infinite_logits_of_the_last_keys(ctx, H):
     """Keys whose logits are -inf for every row: a softmax over the keys before them, as the formula has it."""
     g = torch.Generator(device="cuda").manual_seed(23)
     T, D, cut = 300, 64, 200
-    q, k, v = (torch.randn((T, 1, D), generator=g, device="cuda").to(BF) for _ in range(3))
+    q, k, v = (torch.randn((T, H, D), generator=g, device="cuda").to(BF) for _ in range(3))
     q[..., 0] = 1
-    k[cut:, 0, 0] = -float("inf")
+    k[cut:, :, 0] = -float("inf")
     q[..., 1] = q[..., 1].abs() + 1
-    k[:cut, 0, 1] = -200  # far below zero where they are finite: logits near -25 to -100
-    out, lse = torch.empty_like(q), torch.empty((T, 1), device="cuda")
+    k[:cut, :, 1] = -200  # far below zero where they are finite: logits near -25 to -100
+    out, lse = torch.empty_like(q), torch.empty((T, H), device="cuda")
     ctx.prompt_attention(q, k, v, _i32([0, T]), out, lse=lse)
     ctx.check_device()
     # rows before the cut as they are; each later row like one that sees the first `cut` keys
