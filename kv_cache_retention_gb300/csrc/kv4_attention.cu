@@ -52,7 +52,7 @@
 // second, small kernel, in the order of the blocks, launched as a dependent of the first
 // so that its start costs little.  (Joined by the last block to arrive instead, the join
 // took 4 to 10 us at the end of that block, and its registers came out of the loop's.)
-// Where the maps reach some hundred or few thousand positions only, sharing is not worth
+// Where the maps reach some hundred positions only, sharing is not worth
 // it: blocks take whole units, and there is nothing to join.
 #include <cuda_bf16.h>
 #include <limits.h>
@@ -67,11 +67,11 @@ namespace {
 constexpr int kTile = 32;   // tokens per stage
 constexpr unsigned kBulk = 0x80u;
 constexpr int kPartialFloats = 16 * (128 + 2) + 4;           // the largest partial result
-// Positions up to which units are not shared: at most kWhole, or kWholeMany where every share gets a session or more.  A
-// share's further pieces and the join then cost more than even shares save: one session of 700 tokens took 8.9 us whole
-// and 9.5 shared, of 1000 tokens 9.7 and 9.1 (heads 4 / 2, D 64); 64 sessions of 32 / 8 heads, D 128, and 1000 tokens
-// 29 and 36 us, of 50 to 2000 tokens 39 and 42 us.
-constexpr int kWhole = 768, kWholeMany = 2048;
+// Positions up to which units are not shared: kWhole, or kWholeMany where there are kMany sessions.  A share's further
+// pieces and the join then cost more than even shares save: one session of 32 / 8 heads, D 128, and 500 tokens took 8.7 us
+// whole and 10.8 shared, of 1000 tokens 11.6 and 10.5; 8 of 1000 tokens 12.1 and 13.4; 64 of 1000 tokens 29 and 34, of 50 to
+// 1000 tokens 26 and 28, of 50 to 2000 tokens 39 and 36.
+constexpr int kWhole = 768, kWholeMany = 1024, kMany = 8;
 // Chunks that the start of another session within a share counts as: its queries, first slots and tokens, and the join of
 // the warps.  With 0, 16 sessions of 301 to 32768 tokens and 4 rows took 110 us and 8 of 300 to 8000 tokens 25 us; with 8,
 // 105 and 21; with 20, 98 and 20; with 32, 99 and 21.
@@ -895,7 +895,7 @@ cudaError_t launch(kvsel_ctx* ctx, AttnArgs a, cudaStream_t s) {
     }
     // whole shares of Y blocks, no more than there are sessions to take whole
     const int Y = a.Hkv * a.row_tiles, most = ctx->num_sms * C_blocks<D, W>();
-    a.whole = a.max_len <= (a.S >= most / Y ? kWholeMany : kWhole);
+    a.whole = a.max_len <= (a.S >= kMany ? kWholeMany : kWhole);
     const int blocks = Y >= most ? most : Y * (a.whole && a.S < most / Y ? a.S : most / Y);
     kernel<<<blocks, C::kThreads, C::kSmem, s>>>(a);
     cudaError_t e = cudaGetLastError();

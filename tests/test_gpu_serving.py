@@ -362,10 +362,12 @@ ATTENTION = [
     (600, 1, 1, 1, 64, 16, [i % 70 for i in range(600)]),
     (300, 1, 2, 1, 64, 16, [(i * i * 37) % 900 for i in range(299)] + [2500]),
     (9, 3, 8, 4, 128, 16, [2100, 0, 1, 2100, 40, 0, 1000, 3, 2222]),
-    (40, 1, 16, 8, 128, 16, [1 + 50 * i for i in range(40)]),           # sessions of their own blocks, up to 2048
+    (40, 1, 16, 8, 128, 16, [1 + 50 * i for i in range(40)]),
+    (40, 1, 16, 8, 128, 16, [1 + 25 * i for i in range(40)]),           # sessions of their own blocks, up to 1024
     (3, 1, 2, 1, 128, 16, [767, 768, 769]),
     (2, 1, 4, 2, 128, 48, [1500, 950]),
     (160, 1, 4, 2, 64, 16, [(i * 397) % 2040 for i in range(160)]),
+    (160, 1, 4, 2, 64, 16, [(i * 397) % 990 for i in range(160)]),
 ]
 
 
