@@ -31,6 +31,9 @@
 // block's pass hold values that some rows must not see; there warp 3 sets such values
 // to zero in shared memory before the product, and if there were any, each row adds
 // those it does see to its output at the end (what the sum would be: infinite or NaN).
+// Warp 3 runs up to a unit ahead of the ring, whose barriers' parities would tell it
+// nothing there: the V tiles that it looks over land on barriers of their own (v_raw),
+// and its arrival completes their ring stages.
 //
 // Blocks are as many as there are units, the longest first, but one per SM runs: when its
 // unit is done it claims the unit of a block that has not been launched yet (cluster
@@ -94,8 +97,8 @@ struct Cfg {
     };
     struct Tail {
         uint4 claimed;  // the answer of a claim
-        uint64_t q_full, q_empty, full[kStages], empty[kStages], s_full[2], p_full[2][2], o_done[2], o_free[2], v_ok[2][2],
-            turn[2], unit_full[2], unit_empty[2], claim, drained;
+        uint64_t q_full, q_empty, full[kStages], empty[kStages], s_full[2], p_full[2][2], o_done[2], o_free[2], v_raw[2],
+            v_ok[2][2], turn[2], unit_full[2], unit_empty[2], claim, drained;
         uint32_t tmem;
         int abort_flag, odd_v[2];
         Unit unit[2];
@@ -292,7 +295,6 @@ __device__ __forceinline__ void issue_tiles(typename Cfg<D>::Tail& t, const uint
             if (more) ok = wait_phase(&t.full[sk], pk, abort_flag, err) && ok;
             if (!first) {
                 ok = wait_phase(&t.full[sv], pv, abort_flag, err) && ok;
-                if (i < 2) ok = wait_phase(&t.v_ok[u & 1][i], (u >> 1) & 1, abort_flag, err) && ok;
                 if (i == from && mine) ok = wait_phase(&t.o_free[X], (mine - 1) & 1, abort_flag, err) && ok;
                 // the tiles' turns, tile 1 first
                 if (two && (X == 0 || i > 0)) ok = wait_phase(&t.turn[X], turns++ & 1, abort_flag, err) && ok;
@@ -434,6 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&t.p_full[i][1], 4);
             mbar_init(&t.o_done[i], 1);
             mbar_init(&t.o_free[i], 4);
+            mbar_init(&t.v_raw[i], 1);
             mbar_init(&t.v_ok[i][0], 1);
             mbar_init(&t.v_ok[i][1], 1);
             mbar_init(&t.turn[i], 1);
@@ -459,6 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == 0 && lane == 0) {
             // ---- loads ----
             uint32_t c = 0, loaded_q = 0;  // ring places filled, Q loads
+            uint32_t raw = 0, looked_any = 0, looked_phase = 0;  // stages whose last load was on v_raw; v_raw used; its next phases: a bit each
             bool ok = true;
             for (uint32_t u = 0; ok; ++u) {
                 if (!(ok = wait_phase(&t.unit_full[u & 1], (u >> 1) & 1, abort_flag, a.err))) break;
@@ -477,21 +481,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int i = pos == 2 * w.n - 1 ? w.n - 1 : is_v ? pos / 2 - 1 : (pos + 1) / 2;
                     const uint32_t st = c % kStages;
                     if (!(ok = wait_phase(&t.empty[st], (c / kStages & 1) ^ 1u, abort_flag, a.err))) break;
-                    mbar_expect_tx(&t.full[st], C::kBytes);
+                    const bool looked = is_v && i < 2;
+                    uint64_t* const bar = looked ? &t.v_raw[i] : &t.full[st];
+                    mbar_expect_tx(bar, C::kBytes);
                     for (int b = 0; b < D / 64; ++b)
-                        tma_load(is_v ? &map_v : &map_k, &t.full[st], ring + st * C::kBytes + b * C::kBlock, 64 * b, g,
+                        tma_load(is_v ? &map_v : &map_k, bar, ring + st * C::kBytes + b * C::kBlock, 64 * b, g,
                                  w.first + (w.n - 1 - i) * kTile);
+                    raw = (raw & ~(1u << st)) | (uint32_t)looked << st;
+                    if (looked) looked_any |= 1u << i, looked_phase ^= 1u << i;
                 }
             }
             if (loaded_q) drain_phase(&t.q_full, (loaded_q - 1) & 1);
-            for (uint32_t pos = c > kStages ? c - kStages : 0; pos < c; ++pos) drain_phase(&t.full[pos % kStages], pos / kStages & 1);
+            for (int i = 0; i < 2; ++i)
+                if (looked_any >> i & 1) drain_phase(&t.v_raw[i], (looked_phase >> i & 1) ^ 1);
+            for (uint32_t pos = c > kStages ? c - kStages : 0; pos < c; ++pos)
+                if (!(raw >> (pos % kStages) & 1)) drain_phase(&t.full[pos % kStages], pos / kStages & 1);
         } else if (warp == 1 || warp == 2) {
             issue_tiles<D>(t, sq, ring, warp - 1, lane, abort_flag, a.err);
         } else if (warp == 3) {
             // ---- units of work, and the V tiles of each unit's first two steps ----
             // The block starts with its own unit and then claims those of blocks that have not been launched yet, in
             // the order of launch, until none is left.
-            uint32_t block = blockIdx.x, base = 0, claims = 0;
+            uint32_t block = blockIdx.x, base = 0, claims = 0, looked_phase = 0;  // looked_phase: v_raw's next phases, a bit each
             bool ok = true, any = true, look = false;
             for (uint32_t u = 0; ok; ++u) {
                 typename C::Unit w;
@@ -522,7 +533,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < 2 && ok; ++i) {  // NaN and infinities to zero
                     if (i < w.n) {
                         const uint32_t at = base + at_v(i, w.n), st = at % kStages;
-                        if (!(ok = wait_warp(&t.full[st], at / kStages & 1, abort_flag, a.err))) break;
+                        if (!(ok = wait_warp(&t.v_raw[i], looked_phase >> i & 1, abort_flag, a.err))) break;
+                        looked_phase ^= 1u << i;
                         uint4* const tile = reinterpret_cast<uint4*>(ring + st * C::kBytes);
                         bool odd = false;
 #pragma unroll 4
@@ -544,6 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (odd) t.odd_v[u & 1] = 1;
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                         __syncwarp();
+                        if (lane == 0) mbar_arrive(&t.full[st]);
                     }
                     if (lane == 0) mbar_arrive(&t.v_ok[u & 1][i]);
                 }
