@@ -270,16 +270,19 @@ __device__ __forceinline__ void issue_tiles(typename Cfg<D>::Tail& t, const uint
         __syncwarp();
         if (lead) mbar_arrive(&t.unit_empty[u & 1]);
         if (n == 0) break;
-        if (X == 1 && !two) {                         // tile 0's issuer releases everything
-            base += 2 * n;
+        if (X == 1 && !two) {
+            // no rows for this tile: it sees and releases the unit's loads all the same, since a wait of the next unit
+            // would take a phase two before its own for its own
+            ok = wait_warp(&t.q_full, u & 1, abort_flag, err);
+            if (ok && lead) mbar_arrive(&t.q_empty);
+            for (const uint32_t end = base + 2 * n; ok && base < end; ++base) {
+                ok = wait_warp(&t.full[base % kStages], base / kStages & 1, abort_flag, err);
+                if (ok && lead) mbar_arrive(&t.empty[base % kStages]);
+            }
             continue;
         }
         const int from = X == 0 && two ? 1 : 0;       // the tile's first step
-        const uint32_t releases = X == 0 && !two ? 2 : 1;
-        auto release = [&](uint64_t* b) {             // every barrier of this kind counts both tiles
-            mma_commit(saddr(b), lead);
-            if (releases == 2) mma_commit(saddr(b), lead);
-        };
+        auto release = [&](uint64_t* b) { mma_commit(saddr(b), lead); };
         ok = wait_phase(&t.q_full, u & 1, abort_flag, err);
         // Round i: O += P V of step i (not in the first round, i = from - 1), then S of step i + 1 (not in the last).
         // Stages and phases of its tiles, K(i + 1) and V(i):

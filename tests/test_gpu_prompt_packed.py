@@ -96,3 +96,25 @@ def _odd_values(ctx, lens, Hq, Hkv, D, seed):
 @pytest.mark.parametrize("Hq,Hkv,seed", [(16, 4, 1), (24, 8, 2), (16, 16, 3)])
 def test_odd_values_reach_only_the_rows_that_see_them(ctx, D, Hq, Hkv, seed):
     _odd_values(ctx, PAIRS, Hq, Hkv, D, seed)
+
+
+# units of one tile (up to 128 rows are left) before, between and behind units of two, and one-tile units of many keys
+MIXED = [1, 300, 128, 512, 64, 257, 100, 700, 384, 2, 256, 33, 640, 127, 129, 1152, 5, 256, 1, 1, 900, 128, 400, 90, 600, 17]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv,seed", [(16, 4, 4), (24, 3, 5)])
+@pytest.mark.parametrize("turn", [0, 7])
+def test_units_of_one_and_two_tiles_in_turn(ctx, D, Hq, Hkv, seed, turn):
+    lens = MIXED[turn:] + MIXED[:turn]
+    q, k, v, cu = _inputs(lens, Hq, Hkv, D, seed)
+    out, lse = _run(ctx, q, k, v, cu)
+    _check(q, k, v, cu, out, lse, np.random.default_rng(seed), 4)
+    for _ in range(20):  # whichever block takes a unit
+        again, lse2 = _run(ctx, q, k, v, cu)
+        assert torch.equal(again, out) and torch.equal(lse2, lse)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_odd_values_with_units_of_one_tile(ctx, D):
+    _odd_values(ctx, MIXED, 16, 4, D, 6)

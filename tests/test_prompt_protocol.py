@@ -53,10 +53,11 @@ def at_v(i, n):
 class Block:
     """One block's roles.  own: the value tiles of a unit's first two steps land on barriers of their own, and who looks
     them over then completes their ring stages; otherwise they land on the ring's barriers, for which that warp waits as
-    well."""
+    well.  part: tile 1's issuer takes part in units of one tile (sees and releases what they load); otherwise it passes
+    over them and tile 0's issuer releases for both."""
 
-    def __init__(self, units, own=True):
-        self.units, self.own = units, own
+    def __init__(self, units, own=True, part=True):
+        self.units, self.own, self.part = units, own, part
         self.q_full, self.q_empty = Bar(1), Bar(2)
         self.full = [Bar(1) for _ in range(STAGES)]
         self.empty = [Bar(2) for _ in range(STAGES)]
@@ -112,10 +113,16 @@ class Block:
             if n == 0:
                 return
             if x == 1 and not two:
+                if self.part:
+                    yield self.q_full, u
+                    self.q_empty.arrive()
+                    for at in range(base, base + 2 * n):
+                        yield self.full[at % STAGES], at // STAGES
+                        self.empty[at % STAGES].arrive()
                 base += 2 * n
                 continue
             first_step = 1 if x == 0 and two else 0
-            times = 2 if x == 0 and not two else 1
+            times = 2 if x == 0 and not two and not self.part else 1
             yield self.q_full, u
             for i in range(first_step - 1, n):
                 more, first = i + 1 < n, i < first_step
@@ -242,13 +249,18 @@ class Block:
 
 
 def units(seed):
-    """The units of a block over packed prompts: 256 rows of one, each with the keys up to them."""
+    """The units of a block over packed prompts: 256 rows of one, or the up to 128 that are left of it, each with the
+    keys up to them."""
     rnd = random.Random(seed)
-    return [(2 * rnd.choice((0, 0, 0, 1, 2, 5)) + 2, True) for _ in range(rnd.randrange(2, 12))]
+    out = []
+    for _ in range(rnd.randrange(2, 12)):
+        two = rnd.random() < 0.5
+        out.append((2 * rnd.choice((0, 0, 0, 1, 2, 5)) + 1 + two, two))
+    return out
 
 
 def test_every_wait_sees_its_own_phase():
-    for seed in range(1500):
+    for seed in range(3000):
         Block(units(seed)).run(seed)
 
 
@@ -258,3 +270,10 @@ def test_looking_over_by_the_rings_barriers_breaks_it():
     with pytest.raises(AssertionError, match="role 3 takes phase|finds"):
         for seed in range(1500):
             Block(units(seed), own=False).run(seed)
+
+
+def test_an_issuer_that_passes_over_units_breaks_it():
+    """It takes the Q of the unit that it passed over for the next one's, or a ring stage that is two phases behind."""
+    with pytest.raises(AssertionError, match="role 2 takes phase"):
+        for seed in range(3000):
+            Block(units(seed), part=False).run(seed)
