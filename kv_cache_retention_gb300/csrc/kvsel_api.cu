@@ -143,6 +143,17 @@ const kvsel_ctx::RopeTab* kvsel_rope_tables(kvsel_ctx* ctx, int D, double base, 
     return &t;
 }
 
+// Clears the device error word and waits for that, on a stream of its own: a memset on the default stream would run when
+// that stream's earlier work has ended, and streams that do not block on it would set the word or read it before.
+static cudaError_t clear_dev_err(kvsel_ctx* ctx) {
+    cudaStream_t own;
+    cudaError_t e = cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking);
+    if (e != cudaSuccess) return e;
+    e = cudaMemsetAsync(ctx->dev_err, 0, sizeof(unsigned), own);
+    const cudaError_t waited = cudaStreamSynchronize(own), gone = cudaStreamDestroy(own);
+    return e != cudaSuccess ? e : waited != cudaSuccess ? waited : gone;
+}
+
 extern "C" {
 
 int kvsel_version(void) { return KVSEL_VERSION; }
@@ -158,9 +169,8 @@ int kvsel_ctx_create(int device, kvsel_ctx** out) {
     ctx->device = device;
     if (cudaDeviceGetAttribute(&ctx->num_sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess ||
         cudaMalloc(&ctx->dev_err, sizeof(unsigned)) != cudaSuccess ||
-        cudaMemset(ctx->dev_err, 0, sizeof(unsigned)) != cudaSuccess ||
-        cudaMalloc(&ctx->kv4_partials, kv4_partials_bytes(ctx->num_sms)) != cudaSuccess ||
-        cudaMemset(ctx->kv4_partials, 0, kv4_partials_bytes(ctx->num_sms)) != cudaSuccess) {
+        clear_dev_err(ctx) != cudaSuccess ||
+        cudaMalloc(&ctx->kv4_partials, kv4_partials_bytes(ctx->num_sms)) != cudaSuccess) {
         if (ctx->dev_err) cudaFree(ctx->dev_err);
         if (ctx->kv4_partials) cudaFree(ctx->kv4_partials);
         delete ctx;
@@ -201,7 +211,8 @@ int kvsel_check_device(kvsel_ctx* ctx, void* stream) {
     e = cudaMemcpy(&word, ctx->dev_err, sizeof word, cudaMemcpyDeviceToHost);
     if (e != cudaSuccess) return cuda_fail(ctx, e, "read device error word");
     if (!word) return KVSEL_OK;
-    cudaMemset(ctx->dev_err, 0, sizeof(unsigned));
+    e = clear_dev_err(ctx);
+    if (e != cudaSuccess) return cuda_fail(ctx, e, "clear device error word");
     if (word & KVSEL_DEV_TIMEOUT) return fail(ctx, KVSEL_ERR_TIMEOUT, "a bounded device wait gave up (tensor-core pipeline)");
     return fail(ctx, KVSEL_ERR_DEVICE_CHECK, "device check failed:%s%s%s%s%s%s%s",
                 (word & KVSEL_DEV_BAD_SLOT) ? " slot out of range" : "",
