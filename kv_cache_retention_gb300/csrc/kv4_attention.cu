@@ -172,6 +172,9 @@ __device__ __forceinline__ void copy_bulk(uint32_t dst, const void* src, uint32_
                  "l"(src), "r"(bytes), "r"(bar)
                  : "memory");
 }
+// Ordinary writes of this thread to shared memory (stores and cp.async that have landed) come before bulk copies to the
+// same place that are issued after a barrier.
+__device__ __forceinline__ void fence_bulk() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 // Waits for a phase of bar, a second at most.
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity) {
     uint64_t t0 = 0;
@@ -798,6 +801,7 @@ __global__ void __launch_bounds__(32 * W, C_blocks<D, W>()) kv4_attention_kernel
             parity ^= 1u << st;
         } else {
             asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+            fence_bulk();
         }
         __syncwarp();
         const int n = counts & 0x3Fu;
@@ -876,6 +880,7 @@ __global__ void __launch_bounds__(32 * W, C_blocks<D, W>()) kv4_attention_kernel
         for (int e = threadIdx.x; e < kElems; e += kThreads)
             finish<C, D, MAP>(a, s, y, e, block_sum(e), part.m, part.l, part.nan_tail != 0, err);
     }
+    fence_bulk();                                    // the sums lay over the ring
     __syncthreads();                                 // shared memory is free for the next piece
     if (threadIdx.x == 0) part.nan_tail = 0;         // (a sync lies between this and the piece's loop)
     }
