@@ -80,6 +80,7 @@ constexpr int kLeast = 1;                                    // chunks per warp 
 constexpr float kUnset = 3e38f;  // ref of a row that has seen nothing
 constexpr float kHead = 10.f;   // log2 of the weight at the reference
 constexpr float kSlack = 5.f;   // how far (log2) a logit may pass the reference: weights stay below 2^15
+constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // A unit (session, kv head, row tile) that several shares hold a part of: their partials are joined.
@@ -106,6 +107,8 @@ struct AttnArgs {
     unsigned* err;
     int S;
     int whole;                // units are not shared
+    uint64_t wait_ns;         // how long a wait for a bulk copy goes on
+    int stuck;                // each block's first warp waits for what never comes (test entry)
     float* partials;          // two for each block: of its first piece and of its last, where others share their units
     struct Shared* shared;    // for each block, its shared unit that starts in its share
 };
@@ -130,7 +133,8 @@ struct Cfg {
         uint64_t landed[kStages];   // mbarriers of the stages' bulk copies
     };
     struct Part {
-        int nan_tail;
+        int nan_tail, gave_up;
+        uint64_t never;             // a barrier that nothing completes
         // pieces are worked out by one thread, the next one during the loop over tokens, and kept here
         struct Piece {
             int session, chunk0, chunk1, share0, sharers;
@@ -175,8 +179,8 @@ __device__ __forceinline__ void copy_bulk(uint32_t dst, const void* src, uint32_
 // Ordinary writes of this thread to shared memory (stores and cp.async that have landed) come before bulk copies to the
 // same place that are issued after a barrier.
 __device__ __forceinline__ void fence_bulk() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-// Waits for a phase of bar, a second at most.
-__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity) {
+// Waits for a phase of bar, limit_ns (a second) at most; one answer for the warp's lanes.
+__device__ __forceinline__ bool wait_lane(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
     uint64_t t0 = 0;
     for (uint32_t i = 0;; ++i) {
         uint32_t ok;
@@ -191,10 +195,13 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity) {
             asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
             if (!t0)
                 t0 = t;
-            else if (t - t0 > 1000000000ull)
+            else if (t - t0 > limit_ns)
                 return false;
         }
     }
+}
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+    return __all_sync(0xffffffffu, wait_lane(bar, parity, limit_ns));
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -453,7 +460,8 @@ __global__ void __launch_bounds__(32 * W, C_blocks<D, W>()) kv4_attention_kernel
     };
     __syncthreads();
     if (threadIdx.x == 0) {
-        part.nan_tail = 0;
+        part.nan_tail = part.gave_up = 0;
+        asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(saddr(&part.never)) : "memory");
         next_piece(0);
     }
     __syncthreads();
@@ -794,10 +802,14 @@ __global__ void __launch_bounds__(32 * W, C_blocks<D, W>()) kv4_attention_kernel
     for (int st = 0; st < kStages - 1; ++st) counts |= produce(st) << (8 * st);
     __syncthreads();                                 // the shared query fragments are set
     if (threadIdx.x == 0) next_piece(number + 1);
-    for (int st = 0; counts & 0xFFu;) {
+    bool ok = true;
+    if (a.stuck && warp == 0) ok = wait_phase(saddr(&part.never), 0, a.wait_ns);
+    int st = 0;
+    while (ok && (counts & 0xFFu)) {
         counts |= produce(st == 0 ? kStages - 1 : st - 1) << (8 * (kStages - 1));
         if (counts & kBulk) {
-            if (!wait_phase(saddr(&w.landed[st]), (parity >> st) & 1u)) err |= KVSEL_DEV_TIMEOUT;
+            ok = wait_phase(saddr(&w.landed[st]), (parity >> st) & 1u, a.wait_ns);
+            if (!ok) break;
             parity ^= 1u << st;
         } else {
             asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
@@ -814,6 +826,12 @@ __global__ void __launch_bounds__(32 * W, C_blocks<D, W>()) kv4_attention_kernel
         st = st == kStages - 1 ? 0 : st + 1;
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (!ok) {                                       // no more is asked for; what is on its way lands before the block ends
+        err |= KVSEL_DEV_TIMEOUT;
+        part.gave_up = 1;
+        for (; counts; counts >>= 8, st = st == kStages - 1 ? 0 : st + 1)
+            if (counts & kBulk) wait_phase(saddr(&w.landed[st]), (parity >> st) & 1u, kWaitNs);
+    }
 
     // ---- join: warps, then blocks, in fixed order ----
 #pragma unroll
@@ -829,6 +847,7 @@ __global__ void __launch_bounds__(32 * W, C_blocks<D, W>()) kv4_attention_kernel
             }
         }
     __syncthreads();                                 // also: every warp is done with its ring
+    if (part.gave_up) break;                         // the block's other pieces are left out, the error word tells
     constexpr int kElems = C::kElems;
     float4* const merge = reinterpret_cast<float4*>(smem);  // [kWarps][kElems]
 #pragma unroll
@@ -927,16 +946,10 @@ cudaError_t launch_for(kvsel_ctx* ctx, const AttnArgs& a, int D, bool wide, cuda
     return wide ? launch<64, 2, 8, MAP>(ctx, a, s) : launch<64, 1, 8, MAP>(ctx, a, s);
 }
 
-}  // namespace
-
-size_t kv4_partials_bytes(int num_sms) { return (size_t)num_sms * 2 * (2 * kPartialFloats * sizeof(float) + sizeof(Shared)); }
-
-extern "C" int kvsel_kv4_attention(kvsel_ctx* ctx, const void* q, int64_t q_stride, int S, int Tq, int Hq, int Hkv, int D,
-                                   const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v_codes,
-                                   const uint8_t* v_scales, int P, int page, const int32_t* seq_lens,
-                                   const int32_t* slot_map, const int32_t* block_table, int ld, int dead_slot,
-                                   float scale, void* out, float* lse, void* stream) {
-    const kvsel_trace trace_("kvsel_kv4_attention");
+int attention_call(kvsel_ctx* ctx, const void* q, int64_t q_stride, int S, int Tq, int Hq, int Hkv, int D,
+                   const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v_codes, const uint8_t* v_scales, int P,
+                   int page, const int32_t* seq_lens, const int32_t* slot_map, const int32_t* block_table, int ld,
+                   int dead_slot, float scale, void* out, float* lse, void* stream, uint64_t wait_ns, int stuck) {
     const kvsel_device_scope scope_;
     int rc = kvsel_enter(ctx);
     if (rc) return rc;
@@ -975,9 +988,40 @@ extern "C" int kvsel_kv4_attention(kvsel_ctx* ctx, const void* q, int64_t q_stri
         for (shift = 0; (1 << shift) < page;) ++shift;
     const AttnArgs a{(const __nv_bfloat16*)q, q_stride, Tq, Hq, Hkv, k_codes, k_scales, v_codes, v_scales, P, page, shift,
                      seq_lens, slot_map ? slot_map : block_table, P * page, ld, (int)reach,
-                     dead_slot, tiles, scale, (__nv_bfloat16*)out, lse, ctx->dev_err, S, 0,
+                     dead_slot, tiles, scale, (__nv_bfloat16*)out, lse, ctx->dev_err, S, 0, wait_ns, stuck,
                      (float*)ctx->kv4_partials, (Shared*)((float*)ctx->kv4_partials + (size_t)ctx->num_sms * 4 * kPartialFloats)};
     const cudaStream_t st = (cudaStream_t)stream;
     const cudaError_t e = slot_map ? launch_for<true>(ctx, a, D, wide, st) : launch_for<false>(ctx, a, D, wide, st);
     return e == cudaSuccess ? KVSEL_OK : kvsel_cuda_fail(ctx, e, "kv4_attention launch");
+}
+
+}  // namespace
+
+size_t kv4_partials_bytes(int num_sms) { return (size_t)num_sms * 2 * (2 * kPartialFloats * sizeof(float) + sizeof(Shared)); }
+
+extern "C" int kvsel_kv4_attention(kvsel_ctx* ctx, const void* q, int64_t q_stride, int S, int Tq, int Hq, int Hkv, int D,
+                                   const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v_codes,
+                                   const uint8_t* v_scales, int P, int page, const int32_t* seq_lens,
+                                   const int32_t* slot_map, const int32_t* block_table, int ld, int dead_slot,
+                                   float scale, void* out, float* lse, void* stream) {
+    const kvsel_trace trace_("kvsel_kv4_attention");
+    return attention_call(ctx, q, q_stride, S, Tq, Hq, Hkv, D, k_codes, k_scales, v_codes, v_scales, P, page, seq_lens,
+                          slot_map, block_table, ld, dead_slot, scale, out, lse, stream, kWaitNs, 0);
+}
+
+// Test entry (not part of the public header): kvsel_kv4_attention in which the first warp of every block waits on a
+// barrier that nothing completes, while its first bulk copies are on their way, and every wait for copies is limited to
+// wait_ns.  The blocks that have a piece give up: they flag KVSEL_ERR_TIMEOUT, wait for their own copies, and return.  out
+// and lse hold no meaningful values afterwards.
+extern "C" int kvsel_test_kv4_attention_give_up(kvsel_ctx* ctx, const void* q, int64_t q_stride, int S, int Tq, int Hq,
+                                                int Hkv, int D, const uint8_t* k_codes, const uint8_t* k_scales,
+                                                const uint8_t* v_codes, const uint8_t* v_scales, int P, int page,
+                                                const int32_t* seq_lens, const int32_t* slot_map,
+                                                const int32_t* block_table, int ld, int dead_slot, float scale, void* out,
+                                                float* lse, uint64_t wait_ns, void* stream) {
+    const kvsel_trace trace_("kvsel_test_kv4_attention_give_up");
+    if (wait_ns == 0 || wait_ns > kWaitNs)
+        return kvsel_fail(ctx, KVSEL_ERR_INVALID_ARG, "test_kv4_attention_give_up: wait_ns must be in (0, 1 s]");
+    return attention_call(ctx, q, q_stride, S, Tq, Hq, Hkv, D, k_codes, k_scales, v_codes, v_scales, P, page, seq_lens,
+                          slot_map, block_table, ld, dead_slot, scale, out, lse, stream, wait_ns, 1);
 }
