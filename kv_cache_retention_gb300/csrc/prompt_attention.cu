@@ -83,6 +83,14 @@ struct PromptArgs {
     __nv_bfloat16* out;
     float* lse;
     unsigned* err;
+    uint64_t wait_ns;       // how long a wait goes on
+    int stuck;              // tile 0's issuer waits for what never comes (test entry)
+};
+
+// A block's waits: whether one has given up, and how long each goes on.
+struct Stop {
+    volatile int given_up;
+    uint64_t limit_ns;
 };
 
 template <int D>
@@ -99,8 +107,10 @@ struct Cfg {
         uint4 claimed;  // the answer of a claim
         uint64_t q_full, q_empty, full[kStages], empty[kStages], s_full[2], p_full[2][2], o_done[2], o_free[2], v_raw[2],
             v_ok[2][2], turn[2], unit_full[2], unit_empty[2], claim, drained;
+        Stop stop;
+        uint64_t never;         // nothing completes it
         uint32_t tmem;
-        int abort_flag, odd_v[2];
+        int odd_v[2];
         Unit unit[2];
     };
     static constexpr size_t kSmem = (size_t)(2 + kStages) * kBytes + kOut + sizeof(Tail) + 1024;
@@ -134,15 +144,15 @@ __device__ __forceinline__ uint64_t gtimer() {
     return t;
 }
 // Bounded wait for a phase; false when this or another role gave up.
-__device__ __forceinline__ bool wait_phase(uint64_t* b, uint32_t parity, volatile int* abort_flag, unsigned* err) {
+__device__ __forceinline__ bool wait_phase(uint64_t* b, uint32_t parity, Stop* stop, unsigned* err) {
     if (mbar_try(b, parity)) return true;
     const uint64_t t0 = gtimer();
     for (uint32_t i = 1;; ++i) {
         if (mbar_try(b, parity)) return true;
         if ((i & 63) == 0) {
-            if (*abort_flag) return false;
-            if (gtimer() - t0 > kWaitNs) {
-                *abort_flag = 1;
+            if (stop->given_up) return false;
+            if (gtimer() - t0 > stop->limit_ns) {
+                stop->given_up = 1;
                 atomicOr(err, (unsigned)KVSEL_DEV_TIMEOUT);
                 return false;
             }
@@ -150,8 +160,8 @@ __device__ __forceinline__ bool wait_phase(uint64_t* b, uint32_t parity, volatil
     }
 }
 // The same for a whole warp, with one answer for its lanes.
-__device__ __forceinline__ bool wait_warp(uint64_t* b, uint32_t parity, volatile int* abort_flag, unsigned* err) {
-    return __all_sync(0xffffffffu, wait_phase(b, parity, abort_flag, err));
+__device__ __forceinline__ bool wait_warp(uint64_t* b, uint32_t parity, Stop* stop, unsigned* err) {
+    return __all_sync(0xffffffffu, wait_phase(b, parity, stop, err));
 }
 // Bounded wait that ignores the abort flag: a role's own copies or MMAs before the block ends.
 __device__ __forceinline__ void drain_phase(uint64_t* b, uint32_t parity) {
@@ -254,7 +264,7 @@ __device__ __forceinline__ int at_v(int i, int n) { return i == n - 1 ? 2 * n - 
 // instruction cache (16384 tokens: 1.92 ms, with one copy 1.73 ms).
 template <int D>
 __device__ __forceinline__ void issue_tiles(typename Cfg<D>::Tail& t, const uint8_t* sq, const uint8_t* ring, int tile, int lane,
-                                            volatile int* abort_flag, unsigned* err) {
+                                            bool stuck, Stop* stop, unsigned* err) {
     using C = Cfg<D>;
     constexpr uint32_t kStages = C::kStages;
     const uint32_t lead = lane == 0, X = uniform(tile);
@@ -262,9 +272,9 @@ __device__ __forceinline__ void issue_tiles(typename Cfg<D>::Tail& t, const uint
     const uint32_t ts = uniform(kTmem + kColS + X * kTile), to = uniform(kTmem + kColO + X * D);
     auto desc = [&](uint32_t st, uint32_t leading) { return uniform(desc_low(saddr(ring) + st * C::kBytes, leading)); };
     uint32_t base = 0, steps = 0, turns = 0, mine = 0;  // ring places and this tile's steps, turns and units so far
-    bool ok = true;
+    bool ok = !stuck || wait_warp(&t.never, 0, stop, err);
     for (uint32_t u = 0; ok; ++u) {
-        if (!(ok = wait_warp(&t.unit_full[u & 1], (u >> 1) & 1, abort_flag, err))) break;
+        if (!(ok = wait_warp(&t.unit_full[u & 1], (u >> 1) & 1, stop, err))) break;
         const int n = t.unit[u & 1].n;
         const bool two = t.unit[u & 1].two;
         __syncwarp();
@@ -273,17 +283,17 @@ __device__ __forceinline__ void issue_tiles(typename Cfg<D>::Tail& t, const uint
         if (X == 1 && !two) {
             // no rows for this tile: it sees and releases the unit's loads all the same, since a wait of the next unit
             // would take a phase two before its own for its own
-            ok = wait_warp(&t.q_full, u & 1, abort_flag, err);
+            ok = wait_warp(&t.q_full, u & 1, stop, err);
             if (ok && lead) mbar_arrive(&t.q_empty);
             for (const uint32_t end = base + 2 * n; ok && base < end; ++base) {
-                ok = wait_warp(&t.full[base % kStages], base / kStages & 1, abort_flag, err);
+                ok = wait_warp(&t.full[base % kStages], base / kStages & 1, stop, err);
                 if (ok && lead) mbar_arrive(&t.empty[base % kStages]);
             }
             continue;
         }
         const int from = X == 0 && two ? 1 : 0;       // the tile's first step
         auto release = [&](uint64_t* b) { mma_commit(saddr(b), lead); };
-        ok = wait_phase(&t.q_full, u & 1, abort_flag, err);
+        ok = wait_phase(&t.q_full, u & 1, stop, err);
         // Round i: O += P V of step i (not in the first round, i = from - 1), then S of step i + 1 (not in the last).
         // Stages and phases of its tiles, K(i + 1) and V(i):
         uint32_t at = base + at_k(from);
@@ -295,18 +305,18 @@ __device__ __forceinline__ void issue_tiles(typename Cfg<D>::Tail& t, const uint
                 at = base + at_k(i + 1), sk = at % kStages, pk = at / kStages & 1;
             }
             const uint32_t kd = desc(sk, 16), vd = desc(sv, C::kBlock);
-            if (more) ok = wait_phase(&t.full[sk], pk, abort_flag, err) && ok;
+            if (more) ok = wait_phase(&t.full[sk], pk, stop, err) && ok;
             if (!first) {
-                ok = wait_phase(&t.full[sv], pv, abort_flag, err) && ok;
-                if (i == from && mine) ok = wait_phase(&t.o_free[X], (mine - 1) & 1, abort_flag, err) && ok;
+                ok = wait_phase(&t.full[sv], pv, stop, err) && ok;
+                if (i == from && mine) ok = wait_phase(&t.o_free[X], (mine - 1) & 1, stop, err) && ok;
                 // the tiles' turns, tile 1 first
-                if (two && (X == 0 || i > 0)) ok = wait_phase(&t.turn[X], turns++ & 1, abort_flag, err) && ok;
-                ok = wait_phase(&t.p_full[X][0], steps & 1, abort_flag, err) && ok;
+                if (two && (X == 0 || i > 0)) ok = wait_phase(&t.turn[X], turns++ & 1, stop, err) && ok;
+                ok = wait_phase(&t.p_full[X][0], steps & 1, stop, err) && ok;
                 tc_after();
 #pragma unroll
                 for (int k = 0; k < kTile / 32; ++k)
                     mma_ts(to, ts + k * 8, vd + k * (2048 >> 4), idesc(D, true), i > from || k > 0, lead);
-                ok = wait_phase(&t.p_full[X][1], steps & 1, abort_flag, err) && ok;
+                ok = wait_phase(&t.p_full[X][1], steps & 1, stop, err) && ok;
                 tc_after();
 #pragma unroll
                 for (int k = kTile / 32; k < kTile / 16; ++k)
@@ -338,7 +348,7 @@ __device__ __forceinline__ void issue_tiles(typename Cfg<D>::Tail& t, const uint
                 for (int k = 0; k < 2; ++k) {
                     at = base + (k ? at_v(0, n) : 0);
                     const uint32_t st = at % kStages;
-                    ok = wait_phase(&t.full[st], at / kStages & 1, abort_flag, err) && ok;
+                    ok = wait_phase(&t.full[st], at / kStages & 1, stop, err) && ok;
                     if (lead) mbar_arrive(&t.empty[st]);
                 }
             }
@@ -394,9 +404,9 @@ __device__ __forceinline__ void claim_start(Tail& t) {
 // The claim's answer: whether there was a block, and which.
 template <class Tail>
 __device__ __forceinline__ bool claim_next(Tail& t, uint32_t& claims, uint32_t& block, int lane, bool start,
-                                           volatile int* abort_flag, unsigned* err) {
+                                           Stop* stop, unsigned* err) {
     if (start && lane == 0) claim_start(t);
-    const bool ok = wait_warp(&t.claim, claims++ & 1, abort_flag, err);
+    const bool ok = wait_warp(&t.claim, claims++ & 1, stop, err);
     if (!ok) drain_phase(&t.claim, (claims - 1) & 1);
     uint32_t got, id;
     asm volatile(
@@ -426,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* const ring = smem + 2 * C::kBytes;   // [kStages][kBytes]
     typename C::Tail& t = *reinterpret_cast<typename C::Tail*>(smem + (2 + kStages) * C::kBytes + C::kOut);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    volatile int* const abort_flag = &t.abort_flag;
+    Stop* const stop = &t.stop;
 
     if (threadIdx.x == 0) {
         mbar_init(&t.q_full, 1);
@@ -447,7 +457,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&t.unit_empty[i], 1 + 2 + 8);  // the loads, the issuers, the softmax warps
         }
         mbar_init(&t.drained, 2);
-        t.abort_flag = 0;
+        mbar_init(&t.never, 1);
+        t.stop.given_up = 0;
+        t.stop.limit_ns = a.wait_ns;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
@@ -468,12 +480,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t raw = 0, looked_any = 0, looked_phase = 0;  // stages whose last load was on v_raw; v_raw used; its next phases: a bit each
             bool ok = true;
             for (uint32_t u = 0; ok; ++u) {
-                if (!(ok = wait_phase(&t.unit_full[u & 1], (u >> 1) & 1, abort_flag, a.err))) break;
+                if (!(ok = wait_phase(&t.unit_full[u & 1], (u >> 1) & 1, stop, a.err))) break;
                 const typename C::Unit w = t.unit[u & 1];
                 mbar_arrive(&t.unit_empty[u & 1]);
                 if (w.n == 0) break;
                 const int g = w.head / (a.Hq / a.Hkv), tiles = 1 + w.two;
-                if (u && !(ok = wait_phase(&t.q_empty, (u - 1) & 1, abort_flag, a.err))) break;
+                if (u && !(ok = wait_phase(&t.q_empty, (u - 1) & 1, stop, a.err))) break;
                 mbar_expect_tx(&t.q_full, tiles * C::kBytes);
                 for (int x = 0; x < tiles; ++x)
                     for (int b = 0; b < D / 64; ++b)
@@ -483,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool is_v = pos == 2 * w.n - 1 || (pos > 0 && pos % 2 == 0);
                     const int i = pos == 2 * w.n - 1 ? w.n - 1 : is_v ? pos / 2 - 1 : (pos + 1) / 2;
                     const uint32_t st = c % kStages;
-                    if (!(ok = wait_phase(&t.empty[st], (c / kStages & 1) ^ 1u, abort_flag, a.err))) break;
+                    if (!(ok = wait_phase(&t.empty[st], (c / kStages & 1) ^ 1u, stop, a.err))) break;
                     const bool looked = is_v && i < 2;
                     uint64_t* const bar = looked ? &t.v_raw[i] : &t.full[st];
                     mbar_expect_tx(bar, C::kBytes);
@@ -500,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (uint32_t pos = c > kStages ? c - kStages : 0; pos < c; ++pos)
                 if (!(raw >> (pos % kStages) & 1)) drain_phase(&t.full[pos % kStages], pos / kStages & 1);
         } else if (warp == 1 || warp == 2) {
-            issue_tiles<D>(t, sq, ring, warp - 1, lane, abort_flag, a.err);
+            issue_tiles<D>(t, sq, ring, warp - 1, lane, a.stuck && warp == 1, stop, a.err);
         } else if (warp == 3) {
             // ---- units of work, and the V tiles of each unit's first two steps ----
             // The block starts with its own unit and then claims those of blocks that have not been launched yet, in
@@ -514,9 +526,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     look |= block == 0;
                     w = unit_of<D>(a, block, lane);
                     if (w.n) break;
-                    any = claim_next(t, claims, block, lane, true, abort_flag, a.err);
+                    any = claim_next(t, claims, block, lane, true, stop, a.err);
                 }
-                if (u >= 2 && !(ok = wait_warp(&t.unit_empty[u & 1], ((u >> 1) - 1) & 1, abort_flag, a.err))) break;
+                if (u >= 2 && !(ok = wait_warp(&t.unit_empty[u & 1], ((u >> 1) - 1) & 1, stop, a.err))) break;
                 if (lane == 0) {
                     t.unit[u & 1] = w;
                     t.odd_v[u & 1] = 0;
@@ -536,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < 2 && ok; ++i) {  // NaN and infinities to zero
                     if (i < w.n) {
                         const uint32_t at = base + at_v(i, w.n), st = at % kStages;
-                        if (!(ok = wait_warp(&t.v_raw[i], looked_phase >> i & 1, abort_flag, a.err))) break;
+                        if (!(ok = wait_warp(&t.v_raw[i], looked_phase >> i & 1, stop, a.err))) break;
                         looked_phase ^= 1u << i;
                         uint4* const tile = reinterpret_cast<uint4*>(ring + st * C::kBytes);
                         bool odd = false;
@@ -563,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (lane == 0) mbar_arrive(&t.v_ok[u & 1][i]);
                 }
-                any = claim_next(t, claims, block, lane, false, abort_flag, a.err);
+                any = claim_next(t, claims, block, lane, false, stop, a.err);
                 base += 2 * w.n;
             }
         }
@@ -585,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t done = 0, mine = 0;                      // this tile's steps and units so far
     bool ok = true;
     for (uint32_t u = 0; ok; ++u) {
-    if (!(ok = wait_warp(&t.unit_full[u & 1], (u >> 1) & 1, abort_flag, a.err))) break;
+    if (!(ok = wait_warp(&t.unit_full[u & 1], (u >> 1) & 1, stop, a.err))) break;
     const typename C::Unit w = t.unit[u & 1];
     __syncwarp();
     const bool two = w.two;
@@ -593,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float ref = 0.f;
     float2 sum = make_float2(0.f, 0.f);
     for (int k = 0; k < steps; ++k, ++done) {
-        if (!(ok = wait_warp(&t.s_full[x], done & 1, abort_flag, a.err))) break;
+        if (!(ok = wait_warp(&t.s_full[x], done & 1, stop, a.err))) break;
         tc_after();
         uint32_t s[kTile];
 #pragma unroll
@@ -653,10 +665,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     // ---- output ----
-    if (ok && steps > 0) ok = wait_warp(&t.o_done[x], mine++ & 1, abort_flag, a.err);
+    if (ok && steps > 0) ok = wait_warp(&t.o_done[x], mine++ & 1, stop, a.err);
     if (ok && steps > 0) {
         tc_after();
-        for (int i = 0; i < 2 && ok; ++i) ok = wait_warp(&t.v_ok[u & 1][i], (u >> 1) & 1, abort_flag, a.err);
+        for (int i = 0; i < 2 && ok; ++i) ok = wait_warp(&t.v_ok[u & 1][i], (u >> 1) & 1, stop, a.err);
         const bool odd = *(volatile int*)&t.odd_v[u & 1] != 0;
         const int row = w.row0 + x * kTile + r;
         const float l = sum.x + sum.y, inv = 1.f / l;
@@ -748,12 +760,9 @@ cudaError_t launch(kvsel_ctx* ctx, const CUtensorMap& mq, const CUtensorMap& mk,
     return cudaGetLastError();
 }
 
-}  // namespace
-
-extern "C" int kvsel_prompt_attention(kvsel_ctx* ctx, const void* q, const void* k, const void* v, int64_t q_stride,
-                                      int64_t k_stride, int64_t v_stride, const int32_t* cu_seqlens, int S, int T, int Hq,
-                                      int Hkv, int D, float scale, void* out, float* lse, void* stream) {
-    const kvsel_trace trace_("kvsel_prompt_attention");
+int attention_call(kvsel_ctx* ctx, const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                   int64_t v_stride, const int32_t* cu_seqlens, int S, int T, int Hq, int Hkv, int D, float scale, void* out,
+                   float* lse, void* stream, uint64_t wait_ns, int stuck) {
     const kvsel_device_scope scope_;
     int rc = kvsel_enter(ctx);
     if (rc) return rc;
@@ -781,7 +790,31 @@ extern "C" int kvsel_prompt_attention(kvsel_ctx* ctx, const void* q, const void*
     if (!make_map(&mq, q, T, Hq, D, q_stride) || !make_map(&mk, k, T, Hkv, D, k_stride) || !make_map(&mv, v, T, Hkv, D, v_stride))
         return kvsel_fail(ctx, KVSEL_ERR_CUDA, "prompt_attention: tensor map encoding failed");
     const PromptArgs a{(const __nv_bfloat16*)v, v_stride, cu_seqlens, S, T, Hq, Hkv, n_virtual, unit, scale * kLog2e,
-                       (__nv_bfloat16*)out, lse, ctx->dev_err};
+                       (__nv_bfloat16*)out, lse, ctx->dev_err, wait_ns, stuck};
     const cudaError_t e = D == 64 ? launch<64>(ctx, mq, mk, mv, a, (cudaStream_t)stream) : launch<128>(ctx, mq, mk, mv, a, (cudaStream_t)stream);
     return e == cudaSuccess ? KVSEL_OK : kvsel_cuda_fail(ctx, e, "prompt_attention launch");
+}
+
+}  // namespace
+
+extern "C" int kvsel_prompt_attention(kvsel_ctx* ctx, const void* q, const void* k, const void* v, int64_t q_stride,
+                                      int64_t k_stride, int64_t v_stride, const int32_t* cu_seqlens, int S, int T, int Hq,
+                                      int Hkv, int D, float scale, void* out, float* lse, void* stream) {
+    const kvsel_trace trace_("kvsel_prompt_attention");
+    return attention_call(ctx, q, k, v, q_stride, k_stride, v_stride, cu_seqlens, S, T, Hq, Hkv, D, scale, out, lse, stream,
+                          kWaitNs, 0);
+}
+
+// Test entry (not part of the public header): kvsel_prompt_attention in which the issuer of tile 0 of every block waits on
+// a barrier that nothing completes, with every wait limited to wait_ns.  It gives up while copies and the other issuer's
+// MMAs are in flight; out and lse hold no meaningful values afterwards.
+extern "C" int kvsel_test_prompt_attention_give_up(kvsel_ctx* ctx, const void* q, const void* k, const void* v,
+                                                   int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                                   const int32_t* cu_seqlens, int S, int T, int Hq, int Hkv, int D,
+                                                   float scale, void* out, float* lse, uint64_t wait_ns, void* stream) {
+    const kvsel_trace trace_("kvsel_test_prompt_attention_give_up");
+    if (wait_ns == 0 || wait_ns > kWaitNs)
+        return kvsel_fail(ctx, KVSEL_ERR_INVALID_ARG, "test_prompt_attention_give_up: wait_ns must be in (0, 1 s]");
+    return attention_call(ctx, q, k, v, q_stride, k_stride, v_stride, cu_seqlens, S, T, Hq, Hkv, D, scale, out, lse, stream,
+                          wait_ns, 1);
 }

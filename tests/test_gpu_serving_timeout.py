@@ -64,9 +64,34 @@ def test_kv4_attention_gives_up_and_recovers(ctx, S, Tq, Hq, Hkv, D, n, kind):
         assert torch.equal(out, want)
 
 
+@pytest.mark.parametrize("lens,Hq,Hkv,D", [([600, 90, 1, 300], 8, 2, 128), ([500] * 12, 32, 8, 64), ([300, 40], 2, 2, 64)])
+def test_prompt_attention_gives_up_and_recovers(ctx, lens, Hq, Hkv, D):
+    give_up = _entry("kvsel_test_prompt_attention_give_up", "kvsel_prompt_attention")
+    g = torch.Generator(device="cuda").manual_seed(len(lens))
+    T = sum(lens)
+    q, k, v = (torch.randn((T, h, D), generator=g, device="cuda").to(BF) for h in (Hq, Hkv, Hkv))
+    cu = _i32([sum(lens[:i]) for i in range(len(lens) + 1)])
+    want, out = torch.empty_like(q), torch.empty_like(q)
+    ctx.prompt_attention(q, k, v, cu, want)
+    ctx.check_device()
+    s = torch.cuda.current_stream().cuda_stream
+    for _ in range(2):
+        rc = give_up(ctx.handle, q.data_ptr(), k.data_ptr(), v.data_ptr(), Hq * D, Hkv * D, Hkv * D, cu.data_ptr(), len(lens),
+                     T, Hq, Hkv, D, D ** -0.5, out.data_ptr(), None, LIMIT, s)
+        assert rc == kv.OK, kv.kvsel_last_error_string(ctx.handle)
+        assert kv.kvsel_check_device(ctx.handle, s) == kv.ERR_TIMEOUT, kv.kvsel_last_error_string(ctx.handle)
+        ctx.prompt_attention(q, k, v, cu, out)  # tensor memory is free again
+        ctx.check_device()
+        assert torch.equal(out, want)
+
+
 def test_give_up_entries_reject_bad_limits(ctx):
     give_up = _entry("kvsel_test_kv4_attention_give_up", "kvsel_kv4_attention")
     s = torch.cuda.current_stream().cuda_stream
     for wait in (0, 2_000_000_000):
         assert give_up(ctx.handle, None, 128, 1, 1, 1, 1, 128, None, None, None, None, 1, 16, None, None, None, 1, -1, 1.0,
                        None, None, wait, s) == kv.ERR_INVALID_ARG
+    give_up = _entry("kvsel_test_prompt_attention_give_up", "kvsel_prompt_attention")
+    for wait in (0, 2_000_000_000):
+        assert give_up(ctx.handle, None, None, None, 128, 128, 128, None, 1, 1, 1, 1, 128, 1.0, None, None, wait,
+                       s) == kv.ERR_INVALID_ARG
