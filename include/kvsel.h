@@ -464,10 +464,16 @@ int kvsel_stage_restore(kvsel_ctx* ctx, const void* host_k, const void* host_v, 
  *                     -1 behind the last token
  *   slot_map[s][p]    slot of the session's position p, -1 behind its last token
  *   counts            { new tokens, pages taken }
- * Nothing is synchronised.  A length below 0, or a session whose tokens its
- * table row, slot_map's row or new_slots cannot hold, is cut to what fits and
- * sets the device error word; so do too few free pages and page ids outside
- * [0, P): their slots (and new table entries) are -1.
+ * slot_map's rows are written whole, from the block table: tokens that
+ * kvsel_redirect_slots dropped are live in them again.  Where rows are to stay
+ * as it left them, plan without slot_map and write new_slots[i] to place
+ * new_pos[i] of the session's row.
+ * Nothing is synchronised.  A length below 0, or one that the session's table
+ * row cannot hold, sets the device error word and is cut to what fits, in every
+ * output.  Tokens that slot_map's row or new_slots cannot hold set it too and
+ * are left out there, while cu_new and counts keep the full lengths (cu_new[S]
+ * is then above T).  So do too few free pages and page ids outside [0, P):
+ * their slots (and new table entries) are -1.
  *   cached, new_len int32 [S]; free_pages int32 [n_free] (distinct, held by no
  *   session); block_table int32 [S][max_blocks] in/out; cu_new int32 [S+1];
  *   new_slots, new_pos int32 [T]; slot_map int32 [S][ld] or NULL with ld = 0;

@@ -666,7 +666,8 @@ class Context:
                    slot_map=None, stream=None):
         """Block tables, slots and positions of the step's new tokens, and slot maps, from the lengths (int32 CUDA
         tensors): cached, new_len [S]; free_pages [n_free]; block_table [S][max_blocks] (in/out); cu_new [S+1];
-        new_slots, new_pos [T] (-1 behind the last token); counts [2]; slot_map [S][ld] or None."""
+        new_slots, new_pos [T] (-1 behind the last token); counts [2]; slot_map [S][ld] or None.  slot_map's rows are
+        written whole: tokens that redirect_slots dropped are live in them again."""
         i32, dev = _torch().int32, self.device
         S, T = cached.numel(), new_slots.numel()
         if new_len.numel() != S or cu_new.numel() != S + 1 or new_pos.numel() != T or counts.numel() != 2:
