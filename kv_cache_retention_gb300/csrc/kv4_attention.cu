@@ -439,12 +439,13 @@ __global__ void __launch_bounds__(32 * W, C_blocks<D, W>()) kv4_attention_kernel
             return;
         }
         const long long first = part.before + kStart, q = part.quota;  // first: of the session's own chunks
+        const unsigned q32 = (unsigned)min(q, (long long)UINT_MAX);    // divides numbers below 2^31 alike
         const int chunks = chunks_of(length_of(a, part.session));
         if (part.end <= first) return;                 // only the place of its start is left
         int share1;
         if (first + chunks < (1ll << 31)) {
-            x.share0 = (int)((unsigned)first / (unsigned)q);
-            share1 = (int)((unsigned)(first + chunks - 1) / (unsigned)q);
+            x.share0 = (int)((unsigned)first / q32);
+            share1 = (int)((unsigned)(first + chunks - 1) / q32);
         } else {
             x.share0 = (int)(first / q);
             share1 = (int)((first + chunks - 1) / q);
