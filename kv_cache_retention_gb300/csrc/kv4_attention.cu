@@ -19,7 +19,8 @@
 // operands in registers.
 //
 // The query rows are scaled by a power of two each to a largest value in [2^14, 2^15),
-// which fp16 holds exactly but for values below 2^-38 of it.  The softmax runs over
+// which fp16 holds exactly but for values below 2^-31 of it (those are off by up to
+// 2^-39 of it).  The softmax runs over
 // the tokens once: per row a reference m within 5 (log2) of the running maximum or
 // above, weights 2^(x - m + 10), so that fp16 holds weights down to 2^-24 of the
 // largest with full precision.  Sums and outputs are fp32, moved when the reference
@@ -30,13 +31,14 @@
 // dropped tokens (most of a pruned session's slot map) cost a slot read and no more.
 // Where 32 slots are two runs of 16 rows, four pairs of bulk copies bring them instead.
 //
-// What bounds it: instructions, before memory.  For D = 128 a warp executes about 850
-// for 32 tokens of one kv head, 4.6 KB, of which 270 are the conversions and the scales'
-// multiplications and 33 the products, and issues on 60% of the cycles.  Measured: 36
-// sessions of 32 / 8 heads pruned to a quarter, 278 MB: 80 us (3.5 TB/s); 16 sessions
-// of 4 query rows, 306 MB: 98 us (3.1 TB/s); one of 92160 tokens, 106 MB: 34 us, of
-// which some 6 us go by before the first tokens arrive and 5 us with the join; one of 2048
-// tokens, 9.2 us.  More warps per SM (10 a block, 96 registers) took 104, 115 and 40 us for
+// What bounds it: the latency of dependent instructions, before memory.  For D = 128 a
+// warp executes about 850 for 32 tokens of one kv head, 4.6 KB, of which 270 are the
+// conversions and the scales' multiplications and 33 the products; a scheduler has four
+// warps to choose from (three with two row tiles) and issues on 61% (51%) of its active
+// cycles.  Measured: 36 sessions of 32 / 8 heads pruned to a quarter, 278 MB: 80 us (3.5
+// TB/s), of which the instructions would fill 43; 16 sessions of 4 query rows, 306 MB:
+// 98 us (3.1 TB/s) and 46; one of 92160 tokens, 106 MB: 35 us, of which some 6 us go by
+// before the first tokens arrive and 5 us with the join; one of 2048 tokens, 9.5 us.  More warps per SM (10 a block, 96 registers) took 104, 115 and 40 us for
 // the first three when these took 85, 117 and 36.
 //
 // One wave of two blocks per SM.  The work is the chunks of 32 positions of every
@@ -486,7 +488,7 @@ __global__ void __launch_bounds__(32 * W, C_blocks<D, W>()) kv4_attention_kernel
     const int common = len - a.Tq;          // the last token that every query row sees
 
     // ---- the warp's stream of live tokens ----
-    // Slots are read four chunks of 32 at a time, one such batch ahead of its use.
+    // Slots are read kBatch chunks of 32 at a time, one such batch ahead of its use.
     const int32_t* const map = a.map + (int64_t)s * a.ld;
     constexpr int step = kWarps * kTile;
     const int last = (int)min((long long)len, (long long)piece.chunk1 * kTile);

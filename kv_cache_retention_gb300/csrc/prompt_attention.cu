@@ -19,8 +19,8 @@
 // The softmax keeps per row a reference that only follows the running maximum when
 // that has passed it by 8 (log2): weights are then at most 2^8, which bf16 and the fp32
 // sums hold as well as 1, and O is rescaled only then.  P is rounded to bf16 since both
-// operands of the product have one type and V's range is bf16's; its relative rounding
-// of 2^-9 per weight is random and comes to about the output's own rounding.
+// operands of the product have one type and V's range is bf16's; its relative rounding,
+// 2^-8 at most per weight, is random and comes to about the output's own rounding.
 //
 // 384 threads: warp 0 loads (TMA), warps 1 and 2 issue the MMAs of one tile each, warp 3
 // hands out the units and looks over the V tiles of the diagonal (below), warps 4-7 and
@@ -35,17 +35,18 @@
 // nothing there: the V tiles that it looks over land on barriers of their own (v_raw),
 // and its arrival completes their ring stages.
 //
-// Blocks are as many as there are units, the longest first, but one per SM runs: when its
+// Blocks are as many as there are units, the last sequence's first and of a sequence the
+// longest first, but one per SM runs: when its
 // unit is done it claims the unit of a block that has not been launched yet (cluster
 // launch control), and the next unit's loads and first products run beside the end of the
-// last.  With a block per unit 4096 tokens took 118 us, 16384 tokens 1.78 ms.
+// last.  With a block per unit the 9 prompts below took 398 us, 16384 tokens 1.78 ms.
 //
 // What bounds it: the tensor cores within a unit (128 keys for both tiles take 1.5 us, 91%
 // of the rate of a large library product; both operands of S come from shared memory, at
 // its bandwidth's limit), and some 5 us a unit in which they wait: the first softmax, the
-// last product, the output.  Measured for D = 128: 16384 tokens of 40 / 8 heads 1.71 ms
-// (1.6 PFLOP/s counting what the mask leaves, 86% of that rate), 4096 of 32 / 8 heads 114
-// us (65%), 9 prompts of 14700 tokens together 313 us (64%).
+// last product, the output.  Measured for D = 128: 16384 tokens of 40 / 8 heads 1.66 to 1.74
+// ms (1.6 PFLOP/s counting what the mask leaves, 85% of that rate), 4096 of 32 / 8 heads 117
+// us (63%), 9 prompts of 14700 tokens together 328 us (61%).
 //
 // Every wait is bounded (1 s); on a timeout the block flags KVSEL_ERR_TIMEOUT in the
 // device error word, drains its own copies and MMAs, frees TMEM and returns.
