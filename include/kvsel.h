@@ -579,6 +579,87 @@ int kvsel_prompt_attention(kvsel_ctx* ctx, const void* q, const void* k, const v
                            int64_t k_stride, int64_t v_stride, const int32_t* cu_seqlens, int S, int T, int Hq,
                            int Hkv, int D, float scale, void* out, float* lse, void* stream);
 
+/*
+ * The calls over the bf16 page pools of one layer, as kvsel_rerope_scatter and
+ * kvsel_restore_blocks fill them and kvsel_rule_scores reads them: slot n's row
+ * of kv head g (slot = page id * page + offset) starts at element
+ * n*stride + g*D.  New tokens are packed: session s has the tokens
+ * [cu_new[s], cu_new[s+1]) of q, the last of its seq_lens[s] tokens (as
+ * kvsel_plan_slots gives them, when their rows have been stored), so that
+ * token i of them sits at position p = seq_lens[s] - new + i and sees the
+ * tokens j <= p whose slot is live.  Token j's slot is slot_map[s][j] or, with
+ * block_table, block_table[s][j / page] * page + j % page (exactly one of the
+ * two is given; int32 [S][ld]).  Negative slots and pages and the slot
+ * `dead_slot` (what kvsel_redirect_slots and kvsel_evict_slots write; -1 for
+ * none) are not live: their rows are never read.  Other slots or pages outside
+ * the pool are taken as not live and set the device error word.  So does a
+ * seq_lens[s] below 0 or beyond the reach of the map or table (it is cut to
+ * that), a sequence that starts below 0 or ends before it starts (it has no
+ * rows) and one that ends behind T (it is cut to T; results are undefined where
+ * sequences overlap).  Sessions may have no new tokens.
+ */
+
+/*
+ * Attention of new tokens, from one to thousands for each session, over the
+ * page pools: decode steps, chunks of prompts behind cached tokens, and batches
+ * of both:
+ *   out[i,h] = softmax_j( scale * q[i,h] . K[j,g(h)] ) V[j,g(h)]
+ *   lse[i,h] = ln sum_j exp( scale * q[i,h] . K[j,g(h)] )
+ * with g(h) = h / (Hq/Hkv).  A row that sees nothing gives zeros and -inf.
+ * Rows of tokens outside every session are not touched.
+ *   q        bf16, token i at element i*q_stride, its Hq rows back to back
+ *   k_pool, v_pool  bf16, P pages of `page` slots, k_stride and v_stride elements apart
+ *   out      bf16 [T][Hq][D]; lse fp32 [T][Hq] or NULL
+ * Requires D in {64,128}, Hq % Hkv == 0, Hq/Hkv <= 128, scale > 0, T <= 2^24,
+ * S and Hq <= 65535, P*page < 2^31; q, out, pools and strides 16-byte aligned.
+ */
+int kvsel_pool_attention(kvsel_ctx* ctx, const void* q, int64_t q_stride, const int32_t* cu_new, int S, int T, int Hq,
+                         int Hkv, int D, const void* k_pool, const void* v_pool, int64_t k_stride, int64_t v_stride,
+                         int P, int page, const int32_t* seq_lens, const int32_t* slot_map, const int32_t* block_table,
+                         int ld, int dead_slot, float scale, void* out, float* lse, void* stream);
+
+/*
+ * The softmax weight that the new tokens give to each token of their session,
+ * summed over new tokens and heads and added to a score:
+ *   score_out[s,j] = score_in[s,j] + sum_{i,h} exp( scale * q[i,h] . K[j,g(h)] - lse[i,h] )
+ * over the rows whose token sees j; tokens that no row sees keep score_in.
+ * lse is what kvsel_pool_attention gave for the same arguments; a row whose
+ * lse is -inf adds nothing.  Called after every step (and for every layer) on one
+ * score, it accumulates the attention weight that kvsel_evict_slots goes by.
+ *   score_in, score_out  fp32 [S][score_ld], score_ld at least the positions that
+ *   a row of the map or table reaches; those are written whole.  score_in NULL: zeros;
+ *   it may be score_out.
+ * Sums are fp32, in an order that the sizes alone decide.  Rules as kvsel_pool_attention.
+ */
+int kvsel_attention_mass(kvsel_ctx* ctx, const void* q, int64_t q_stride, const float* lse, const int32_t* cu_new, int S,
+                         int T, int Hq, int Hkv, int D, const void* k_pool, int64_t k_stride, int P, int page,
+                         const int32_t* seq_lens, const int32_t* slot_map, const int32_t* block_table, int ld,
+                         int dead_slot, float scale, const float* score_in, float* score_out, int64_t score_ld,
+                         void* stream);
+
+/*
+ * Eviction by score, for S sessions: session s keeps budget[s] live tokens.  Of
+ * its first seq_lens[s] tokens, those are live whose slot is not negative and not
+ * dead_slot.  When there are more than budget[s], the tokens of least score leave,
+ * of equal scores the later position first (the earlier are kept, as in
+ * kvsel_topk_retain), a NaN before any number, -0 equal to +0; never the first
+ * n_sink positions nor the last n_recent of seq_lens[s], even if more than
+ * budget[s] then stay.
+ *   slot_out[s][j]  dead_slot for a token that leaves, slot_map[s][j] for all others (rows
+ *                   are written whole; slot_out may be slot_map)
+ *   freed[s]        slots of the tokens that left, in the order of their positions, then -1; int32
+ *                   [S][ld_freed] or NULL with ld_freed = 0.  A call evicts at most ld_freed
+ *                   tokens of a session where the list is given, so that no slot is lost.
+ *   n_freed[s]      how many left; int32 [S] or NULL
+ * Kept rows never move; freed slots may be given to new tokens at once.
+ *   score  fp32 [S][score_ld], score_ld >= ld; seq_lens, budget int32 [S]; slot_map int32 [S][ld]
+ * A seq_lens[s] below 0 or above ld sets the device error word and is cut to that.
+ * Requires S <= 65535, ld < 2^31 - 2^20.  No workspace.
+ */
+int kvsel_evict_slots(kvsel_ctx* ctx, const float* score, int64_t score_ld, const int32_t* seq_lens, const int32_t* budget,
+                      int S, const int32_t* slot_map, int ld, int32_t dead_slot, int n_sink, int n_recent,
+                      int32_t* slot_out, int32_t* freed, int ld_freed, int32_t* n_freed, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -90,6 +90,11 @@ SIGNATURES = {
     "kvsel_kv4_attention": (_I, [_P, _P, _I64, _I, _I, _I, _I, _I, _P, _P, _P, _P, _I, _I, _P, _P, _P, _I, _I, _F, _P,
                                  _P, _P]),
     "kvsel_prompt_attention": (_I, [_P, _P, _P, _P, _I64, _I64, _I64, _P, _I, _I, _I, _I, _I, _F, _P, _P, _P]),
+    "kvsel_pool_attention": (_I, [_P, _P, _I64, _P, _I, _I, _I, _I, _I, _P, _P, _I64, _I64, _I, _I, _P, _P, _P, _I, _I, _F,
+                                  _P, _P, _P]),
+    "kvsel_attention_mass": (_I, [_P, _P, _I64, _P, _P, _I, _I, _I, _I, _I, _P, _I64, _I, _I, _P, _P, _P, _I, _I, _F, _P,
+                                  _P, _I64, _P]),
+    "kvsel_evict_slots": (_I, [_P, _P, _I64, _P, _P, _I, _P, _I, ctypes.c_int32, _I, _I, _P, _P, _I, _P, _P]),
 }
 
 
@@ -271,6 +276,24 @@ def kvsel_prompt_attention(ctx, q, k, v, q_stride, k_stride, v_stride, cu_seqlen
                            stream):
     return _lib.kvsel_prompt_attention(ctx, q, k, v, q_stride, k_stride, v_stride, cu_seqlens, S, T, Hq, Hkv, D, scale,
                                        out, lse, stream)
+
+
+def kvsel_pool_attention(ctx, q, q_stride, cu_new, S, T, Hq, Hkv, D, k_pool, v_pool, k_stride, v_stride, P, page, seq_lens,
+                         slot_map, block_table, ld, dead_slot, scale, out, lse, stream) -> int:
+    return _lib.kvsel_pool_attention(ctx, q, q_stride, cu_new, S, T, Hq, Hkv, D, k_pool, v_pool, k_stride, v_stride, P, page,
+                                     seq_lens, slot_map, block_table, ld, dead_slot, scale, out, lse, stream)
+
+
+def kvsel_attention_mass(ctx, q, q_stride, lse, cu_new, S, T, Hq, Hkv, D, k_pool, k_stride, P, page, seq_lens, slot_map,
+                         block_table, ld, dead_slot, scale, score_in, score_out, score_ld, stream) -> int:
+    return _lib.kvsel_attention_mass(ctx, q, q_stride, lse, cu_new, S, T, Hq, Hkv, D, k_pool, k_stride, P, page, seq_lens,
+                                     slot_map, block_table, ld, dead_slot, scale, score_in, score_out, score_ld, stream)
+
+
+def kvsel_evict_slots(ctx, score, score_ld, seq_lens, budget, S, slot_map, ld, dead_slot, n_sink, n_recent, slot_out, freed,
+                      ld_freed, n_freed, stream) -> int:
+    return _lib.kvsel_evict_slots(ctx, score, score_ld, seq_lens, budget, S, slot_map, ld, dead_slot, n_sink, n_recent,
+                                  slot_out, freed, ld_freed, n_freed, stream)
 
 
 # ---------------------------------------------------------------------------
@@ -782,5 +805,103 @@ class Context:
             self.handle, qp, kp, vp, qs, ks, vs, _at(cu_seqlens, torch.int32, dev, "cu_seqlens"), S, T, Hq, Hkv, D,
             D ** -0.5 if scale is None else scale, _at(out, bf, dev, "out"), _at(lse, torch.float32, dev, "lse"),
             self._stream(stream))
+        if rc:
+            self._check(rc)
+
+    # attention over the page pools, and eviction by it ---------------------
+
+    def _pool_call(self, who, q, cu_new, seq_lens, slot_map, block_table):
+        """q's pointer, stride and shape, S and the map of a call over the page pools."""
+        qp, qs = _rows(q, 1, _torch().bfloat16, self.device, "q")
+        S = seq_lens.numel()
+        tokens = slot_map if slot_map is not None else block_table
+        if tokens is None or (slot_map is not None and block_table is not None):
+            raise ValueError(f"{who}: one of slot_map and block_table is needed")
+        if tokens.dim() != 2 or tokens.shape[0] != S or cu_new.numel() != S + 1:
+            raise ValueError(f"{who}: slot_map or block_table must be [S][ld], seq_lens [S] and cu_new [S+1]")
+        return qp, qs, q.shape, S, tokens.shape[1]
+
+    def _pool(self, t, D, name):
+        """Pointer, elements between slots and [P][page][Hkv] of a page pool [P][page][Hkv][D] (bf16)."""
+        ptr, stride = _rows(t, 2, _torch().bfloat16, self.device, name)
+        P, page, Hkv, d = t.shape
+        if d != D:
+            raise ValueError(f"{name}: expected [P][page][Hkv][{D}], got {tuple(t.shape)}")
+        return ptr, stride, (P, page, Hkv)
+
+    def pool_attention(self, q, k_pool, v_pool, cu_new, seq_lens, out, slot_map=None, block_table=None, dead_slot=None,
+                       scale=None, lse=None, stream=None):
+        """Attention of packed new tokens q [T][Hq][D] (bf16, tokens at any even spacing; session s has the tokens
+        cu_new[s] .. cu_new[s+1], the last of its seq_lens[s]) over the page pools k_pool, v_pool [P][page][Hkv][D] (bf16,
+        slots at any even spacing, such as one layer of [L][P][page][Hkv][D]); tokens found through slot_map [S][ld] or
+        block_table [S][ld] (int32), slots < 0 and dead_slot skipped.  out [T][Hq][D] bf16; lse fp32 [T][Hq] or None;
+        scale: 1/sqrt(D) when None."""
+        torch, dev = _torch(), self.device
+        qp, qs, shape, S, ld = self._pool_call("pool_attention", q, cu_new, seq_lens, slot_map, block_table)
+        T, Hq, D = shape
+        kp, ks, sizes = self._pool(k_pool, D, "k_pool")
+        vp, vs, v_sizes = self._pool(v_pool, D, "v_pool")
+        if v_sizes != sizes:
+            raise ValueError("pool_attention: k_pool and v_pool must have the same shape")
+        if out.shape != shape or (lse is not None and lse.shape != (T, Hq)):
+            raise ValueError("pool_attention: out must be [T][Hq][D] and lse [T][Hq]")
+        i32 = torch.int32
+        P, page, Hkv = sizes
+        rc = _lib.kvsel_pool_attention(
+            self.handle, qp, qs, _at(cu_new, i32, dev, "cu_new"), S, T, Hq, Hkv, D, kp, vp, ks, vs, P, page,
+            _at(seq_lens, i32, dev, "seq_lens"), _at(slot_map, i32, dev, "slot_map"),
+            _at(block_table, i32, dev, "block_table"), ld, -1 if dead_slot is None else int(dead_slot),
+            D ** -0.5 if scale is None else scale, _at(out, torch.bfloat16, dev, "out"), _at(lse, torch.float32, dev, "lse"),
+            self._stream(stream))
+        if rc:
+            self._check(rc)
+
+    def attention_mass(self, q, lse, k_pool, cu_new, seq_lens, score, slot_map=None, block_table=None, dead_slot=None,
+                       scale=None, score_in=None, stream=None):
+        """score[s][j] = score_in[s][j] (0 when None) + the softmax weight that session s's new tokens give to its token
+        j, summed over tokens and heads: q and the other arguments as in pool_attention, lse [T][Hq] as it gave it.
+        score, score_in fp32 [S][n], n at least the positions that a row of slot_map or block_table reaches (columns behind
+        them are not touched); score_in may be score."""
+        torch, dev = _torch(), self.device
+        qp, qs, shape, S, ld = self._pool_call("attention_mass", q, cu_new, seq_lens, slot_map, block_table)
+        T, Hq, D = shape
+        kp, ks, (P, page, Hkv) = self._pool(k_pool, D, "k_pool")
+        reach = ld if slot_map is not None else ld * page
+        if score.dim() != 2 or score.shape[0] != S or score.shape[1] < reach:
+            raise ValueError("attention_mass: score must be [S][n], n at least the map's positions")
+        if lse.shape != (T, Hq) or (score_in is not None and score_in.shape != score.shape):
+            raise ValueError("attention_mass: lse must be [T][Hq] and score_in shaped like score")
+        i32, f32 = torch.int32, torch.float32
+        rc = _lib.kvsel_attention_mass(
+            self.handle, qp, qs, _at(lse, f32, dev, "lse"), _at(cu_new, i32, dev, "cu_new"), S, T, Hq, Hkv, D, kp, ks, P, page,
+            _at(seq_lens, i32, dev, "seq_lens"), _at(slot_map, i32, dev, "slot_map"),
+            _at(block_table, i32, dev, "block_table"), ld, -1 if dead_slot is None else int(dead_slot),
+            D ** -0.5 if scale is None else scale, _at(score_in, f32, dev, "score_in"), _at(score, f32, dev, "score"),
+            score.shape[1], self._stream(stream))
+        if rc:
+            self._check(rc)
+
+    def evict_slots(self, score, seq_lens, budget, slot_map, dead_slot, slot_out, n_sink=0, n_recent=0, freed=None,
+                    n_freed=None, stream=None):
+        """Sessions with more live tokens than budget[s] give up those of least score (never the first n_sink or the last
+        n_recent positions): slot_out [S][ld] is slot_map with dead_slot in their places (it may be slot_map), freed [S][f]
+        lists their slots, then -1 (at most f leave), n_freed [S] counts them.  score fp32 [S][n], n >= ld; all others int32."""
+        torch, dev = _torch(), self.device
+        i32 = torch.int32
+        S = seq_lens.numel()
+        shape = slot_map.shape
+        if len(shape) != 2 or shape[0] != S or slot_out.shape != shape:
+            raise ValueError("evict_slots: slot_map and slot_out must be [S][ld]")
+        if score.dim() != 2 or score.shape[0] != S or score.shape[1] < shape[1] or budget.numel() != S:
+            raise ValueError("evict_slots: score must be [S][n], n >= ld, and budget [S]")
+        if freed is not None and (freed.dim() != 2 or freed.shape[0] != S or freed.shape[1] == 0):
+            raise ValueError("evict_slots: freed must be [S][f], f > 0")
+        if n_freed is not None and n_freed.numel() != S:
+            raise ValueError("evict_slots: n_freed must be [S]")
+        rc = _lib.kvsel_evict_slots(
+            self.handle, _at(score, torch.float32, dev, "score"), score.shape[1], _at(seq_lens, i32, dev, "seq_lens"),
+            _at(budget, i32, dev, "budget"), S, _at(slot_map, i32, dev, "slot_map"), shape[1], int(dead_slot), int(n_sink),
+            int(n_recent), _at(slot_out, i32, dev, "slot_out"), _at(freed, i32, dev, "freed"),
+            0 if freed is None else freed.shape[1], _at(n_freed, i32, dev, "n_freed"), self._stream(stream))
         if rc:
             self._check(rc)

@@ -29,8 +29,11 @@ SOURCES = [
     "kv4_cache.cu",
     "kv4_attention.cu",
     "prompt_attention.cu",
+    "pool_attention.cu",
+    "attention_mass.cu",
+    "evict_slots.cu",
 ]
-HEADERS = ["kvsel_internal.h", "kv4_format.cuh", os.path.join("..", "..", "include", "kvsel.h")]
+HEADERS = ["kvsel_internal.h", "kv4_format.cuh", "pool_tokens.cuh", os.path.join("..", "..", "include", "kvsel.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xptxas", "-v"]

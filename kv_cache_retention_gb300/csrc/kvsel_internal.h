@@ -54,6 +54,11 @@ struct kvsel_ctx {
     char err[512] = {0};
 };
 
+// Bits of kvsel_ctx::ready of the calls over the page pools (the ones below 20 are prompt_attention's and kv4_attention's).
+enum kvsel_ready : unsigned {
+    KVSEL_READY_EVICT = 1u << 20,
+};
+
 // Device error-word bits.
 enum kvsel_devcheck : unsigned {
     KVSEL_DEV_BAD_SLOT = 1u << 0,
