@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(128) attention_mass_kernel(const MassArgs a) {
     const int G = a.Hq / a.Hkv;
     for (int64_t j = (int64_t)blockIdx.x * 128 + threadIdx.x; j < a.map.reach; j += (int64_t)gridDim.x * 128) {
         float sum = a.before ? a.before[s * a.score_ld + j] : 0.f;
-        const int slot = j < x.len && x.count > 0 ? live_slot(a.map, row, (int)j, err) : -1;
+        const int slot = j < x.len && x.count > 0 ? live_slot(a.map, raw_entry(a.map, row, (int)j), (int)j, err) : -1;
         if (slot >= 0) {
             const int i0 = max(0, (int)j - (x.len - x.count));
             float mass = 0.f;

@@ -170,9 +170,11 @@ int kvsel_ctx_create(int device, kvsel_ctx** out) {
     if (cudaDeviceGetAttribute(&ctx->num_sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess ||
         cudaMalloc(&ctx->dev_err, sizeof(unsigned)) != cudaSuccess ||
         clear_dev_err(ctx) != cudaSuccess ||
-        cudaMalloc(&ctx->kv4_partials, kv4_partials_bytes(ctx->num_sms)) != cudaSuccess) {
+        cudaMalloc(&ctx->kv4_partials, kv4_partials_bytes(ctx->num_sms)) != cudaSuccess ||
+        cudaMalloc(&ctx->pool_parts, pool_parts_bytes(ctx->num_sms)) != cudaSuccess) {
         if (ctx->dev_err) cudaFree(ctx->dev_err);
         if (ctx->kv4_partials) cudaFree(ctx->kv4_partials);
+        if (ctx->pool_parts) cudaFree(ctx->pool_parts);
         delete ctx;
         return KVSEL_ERR_CUDA;
     }
@@ -187,6 +189,7 @@ int kvsel_ctx_destroy(kvsel_ctx* ctx) {
     kvsel_stager_release(ctx);
     if (ctx->ws) cudaFree(ctx->ws);
     if (ctx->kv4_partials) cudaFree(ctx->kv4_partials);
+    if (ctx->pool_parts) cudaFree(ctx->pool_parts);
     if (ctx->dev_err) cudaFree(ctx->dev_err);
     for (int i = 0; i < ctx->n_rope; ++i) {
         cudaFree(ctx->rope[i].lo);

@@ -50,6 +50,8 @@ struct kvsel_ctx {
     // Partial results of kvsel_kv4_attention: of one size, there from the context's creation on, so
     // that captured graphs may hold its address.
     void* kv4_partials = nullptr;
+    // The same of kvsel_pool_attention.
+    void* pool_parts = nullptr;
     unsigned ready = 0;  // kernels whose attributes are set on this context's device, a bit each
     char err[512] = {0};
 };
@@ -57,6 +59,8 @@ struct kvsel_ctx {
 // Bits of kvsel_ctx::ready of the calls over the page pools (the ones below 20 are prompt_attention's and kv4_attention's).
 enum kvsel_ready : unsigned {
     KVSEL_READY_EVICT = 1u << 20,
+    KVSEL_READY_POOL64 = 1u << 21,
+    KVSEL_READY_POOL128 = 1u << 22,
 };
 
 // Device error-word bits.
@@ -126,6 +130,7 @@ int kvsel_check_rule_scores_args(kvsel_ctx* ctx, const char* who, const void* k_
                                  int64_t layer_stride, int64_t slot_stride, const float* M, int pi, int q_s, int q_e,
                                  const float* rule);
 size_t kv4_partials_bytes(int num_sms);
+size_t pool_parts_bytes(int num_sms);
 // Frees the staging buffers, events and copy stream of kvsel_stage_restore.
 void kvsel_stager_release(kvsel_ctx* ctx);
 

@@ -1,72 +1,779 @@
-// kvsel_pool_attention: attention of packed new tokens over the bf16 page pools.
+// kvsel_pool_attention: attention of packed new tokens over the bf16 page pools, on the 5th-generation tensor cores.
 //
 // Token i of a session sits at position pos = len - count + i and sees the live tokens j <= pos:
-//   out = sum_j p_j v_j / sum_j p_j,  p_j = e^(scale q . k_j - max),  lse = ln sum_j e^(scale q . k_j).
+//   out = sum_j p_j v_j / sum_j p_j,  p_j = 2^(scale log2e q . k_j - ref),  lse = ln sum_j e^(scale q . k_j).
 //
-// A warp per (token, head), its lanes on the dims; one pass over the keys with the running maximum and sum.
-#include <cuda_bf16.h>
+// Rows.  A tile has the G = Hq/Hkv heads of one kv head for as many tokens as fit 128 rows (TMEM lanes), token by token, so
+// that they share each key: a chunk of a prompt fills the tiles, a decode step has G rows.  A unit of work is two tiles of
+// one session and kv head.
+//
+// Keys go through lists of 128 live tokens that one warp makes from the map (dropped tokens cost an entry's read and no
+// more); their rows come by TMA gathers of four slots.  Per list and tile
+//   S = Q K^T   tcgen05.mma, both operands from shared memory, 128 fp32 columns
+//   P = 2^(S sc - ref) in bf16, written over S in TMEM
+//   O += P V    tcgen05.mma, P from TMEM, V from shared memory as it lies
+// Where a unit fills both tiles, they share every K and V tile and take turns: one's softmax runs beside the other's
+// products.  Where it has rows for one, TMEM's second half takes every other list for the same rows, and the two results
+// are put together at the end.
+//
+// The softmax keeps per row a reference that only follows the running maximum when that has passed it by 8 (log2): weights
+// are then at most 2^8, which bf16 and the fp32 sums hold as well as 1, and O is rescaled only then.  P is rounded to bf16
+// since both operands of the product have one type and V's range is bf16's: 2^-8 at most per weight, at random, about the
+// output's own rounding.
+//
+// 384 threads: warp 0 plans and makes the lists, warps 1 and 2 issue the MMAs of one tile each (warp 1 of both, where the
+// rows are one tile's), warp 3 loads, warps 4-7 and 8-11 are the softmax of the two tiles, a row per thread.  TMEM: S of
+// tile 0 and 1 at columns 0 and 128, O at 256 and on.
+//
+// Shares.  The units' keys, laid end to end with some for the start of each, are cut into equal shares, found from the
+// lengths on the device; neighbouring blocks take a share for one kv head each (the heads' rows of a slot lie side by side).
+// What a block has of a unit that others have a part of goes to memory of a fixed size, and a second small kernel joins
+// the parts in the order of the blocks.
+//
+// Masked places.  A weight of zero does not hide a NaN or an infinity in V.  In lists that not every row sees whole, the
+// softmax warps set such values to zero in shared memory before the product, and if there were any, each row adds those it
+// does see to its output at the end (what the sum would be: infinite or NaN).
+//
+// Every wait is bounded (1 s); on a timeout the block flags KVSEL_ERR_TIMEOUT in the device error word, drains its own copies
+// and MMAs, frees TMEM and returns.
+#include <limits.h>
 
-#include "pool_tokens.cuh"
+#include "pool_lists.cuh"
 
 namespace {
 
+constexpr int kThreads = 384;
+constexpr float kSlack = 8.f;           // how far (log2) a row's maximum may pass its reference
+// Registers per thread: at launch, then after the first warpgroup's setmaxnreg.dec and the softmax warpgroups' .inc.  An
+// .inc beyond the launch's registers would wait forever; the launcher checks the compiled count.
+constexpr int kRegsLaunch = 168, kRegsCtl = 80, kRegsSoft = 208;
+static_assert(kRegsCtl + 2 * kRegsSoft <= 3 * kRegsLaunch && kRegsLaunch * kThreads <= 65536, "register split");
+constexpr int kLists = 8;
+constexpr int kStart = 4;               // lists that the start of a unit counts as when shares are cut
+constexpr int kLeast = 4;               // lists that a share has at least, so cut
+
+// All of TMEM is allocated, so its base is column 0.
+constexpr uint32_t kTmem = 0;
+constexpr int kColS = 0, kColO = 256, kTmemCols = 512;
+
+// What a block has of a unit that others share: O as [D/4][128 rows] of four dims, then references and sums; per tile.
+constexpr int kPartTile = kTile * (128 + 2), kPart = 2 * kPartTile;
+
+// A unit that several shares have a part of, kept with the block that has its first keys; sharers 0: none.
+struct Joint {
+    int sharers, row, tokens;           // row, tokens: its first token in q, and how many
+};
+
 struct PoolArgs {
-    const __nv_bfloat16* q;
-    int64_t q_stride;
     const int32_t *cu, *lens;
-    int S, T, Hq, Hkv;
-    const __nv_bfloat16 *k, *v;
-    int64_t k_stride, v_stride;
+    int S, T, Hq, Hkv, G;
+    int tile_tokens;                    // tokens of a tile
+    const __nv_bfloat16* v;
+    int64_t v_stride;
     TokenMap map;
-    float scale;
+    float scale2;                       // scale * log2(e)
     __nv_bfloat16* out;
     float* lse;
     unsigned* err;
+    int shares;
+    float* parts;                       // [blocks][2]: of a unit that began before the share, and of one that goes on behind it
+    Joint* joints;                      // [blocks]
+    uint64_t wait_ns;                   // how long a wait goes on
+    int stuck;                          // tile 0's issuer waits for what never comes (test entry)
 };
 
 template <int D>
-__global__ void __launch_bounds__(256) pool_attention_kernel(const PoolArgs a) {
-    const int s = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int kPer = D / 32;
-    unsigned err = blockIdx.x == 0 ? session_errors(a.cu, a.lens, a.T, a.map.reach, s) : 0u;
-    const Session x = session_at(a.cu, a.lens, a.T, a.map.reach, s);
-    const int32_t* const row = a.map.map + (int64_t)s * a.map.ld;
-    for (int64_t w = (int64_t)blockIdx.x * 8 + warp; w < (int64_t)x.count * a.Hq; w += (int64_t)gridDim.x * 8) {
-        const int i = (int)(w / a.Hq), h = (int)(w % a.Hq), g = h / (a.Hq / a.Hkv), pos = x.len - x.count + i;
-        float q[kPer], o[kPer], m = -INFINITY, l = 0.f;
-        for (int e = 0; e < kPer; ++e) {
-            q[e] = __bfloat162float(a.q[(int64_t)(x.first + i) * a.q_stride + (int64_t)h * D + lane + 32 * e]);
-            o[e] = 0.f;
+struct Cfg {
+    static constexpr int kBlock = kTile * 128;             // 128 rows x 64 dims, 128-byte swizzled
+    static constexpr int kBytes = D / 64 * kBlock;         // one tile of Q, K or V
+    static constexpr int kStages = 4;                      // K and V tiles share the ring
+    static constexpr int kOut = 8 * 32 * 64;               // 32 rows of 32 dims for each softmax warp, on their way out
+    // What a block does of one unit; end: there is nothing more.
+    struct Piece {
+        int row, tokens, pos0;          // first token in q, how many, the first one's position
+        int session, stop;              // the piece's keys lie below position stop
+        int part;                       // -1: the whole unit, else which partial result it is
+        int two, end;
+    };
+    struct Tail {
+        Lists<kLists> lists;
+        uint64_t q_full, q_empty, full[kStages], empty[kStages], s_full[2], p_full[2][2], o_done[2], o_free[2][2], turn[2],
+            piece_full[2], piece_empty[2], merge[2], drained;
+        Stop stop;
+        uint64_t never;                 // nothing completes it
+        uint32_t tmem;
+        int odd[2];                     // of the two pieces: the first key of a list with NaN or infinite values, set to zero
+        Piece piece[2];
+        float2 other[2][kTile];         // tile 1's references and sums, where both tiles have the same rows
+    };
+    static constexpr size_t kSmem = (size_t)(2 + kStages) * kBytes + kOut + sizeof(Tail) + 1024;
+    static_assert(kSmem <= 232448, "shared memory per block");
+};
+
+// Place in the ring of list i's K and V tile: K0, K1, V0, K2, V1, ..., V(n-1); last: list i is the last.
+__device__ __forceinline__ int at_k(int i) { return i == 0 ? 0 : 2 * i - 1; }
+__device__ __forceinline__ int at_v(int i, bool last) { return last ? 2 * i + 1 : 2 * i + 2; }
+
+// ---- MMAs: a warp per tile -------------------------------------------------
+// Two issuers on two SM sub-partitions that take turns, so that one tile's products run beside the other's softmax.  One
+// copy of the code for both.  Each warp sees every phase of the ring's barriers, whoever's tile it is: a wait for a phase that
+// is two behind would return at once, one for a phase with another one done behind it never.  (The barriers of O are in pairs
+// for the same reason: a piece does not begin before the one two before it has been read.)
+template <int D>
+__device__ __forceinline__ void issue_tiles(typename Cfg<D>::Tail& t, const uint8_t* sq, const uint8_t* ring, int tile, int lane,
+                                            bool stuck, Stop* stop, unsigned* err) {
+    using C = Cfg<D>;
+    constexpr uint32_t kStages = C::kStages;
+    const uint32_t lead = lane == 0, X = uniform(tile);
+    uint32_t base = 0, lists = 0, turns = 0, steps0 = 0, steps1 = 0;  // ring places, lists, turns and the tiles' steps so far
+    bool was_two = false;
+    bool ok = !stuck || wait_warp(&t.never, 0, stop, err);
+    auto desc = [&](uint32_t at, uint32_t leading) { return uniform(desc_low(saddr(ring) + at % kStages * C::kBytes, leading)); };
+    auto wait_full = [&](uint32_t at) { ok = ok && wait_warp(&t.full[at % kStages], at / kStages & 1, stop, err); };
+    for (uint32_t u = 0; ok; ++u) {
+        if (!(ok = wait_warp(&t.piece_full[u & 1], (u >> 1) & 1, stop, err))) break;
+        const bool two = t.piece[u & 1].two, end = t.piece[u & 1].end;
+        __syncwarp();
+        if (lead) mbar_arrive(&t.piece_empty[u & 1]);
+        if (end) break;
+        int n = 0;                                // lists of the piece so far
+        bool ended = false;
+        auto there_is = [&](int i) {              // list i
+            while (ok && !ended && n <= i) {
+                const uint32_t l = lists % kLists;
+                if (!(ok = wait_warp(&t.lists.full[l], lists / kLists & 1, stop, err))) break;
+                n += t.lists.meta[l].n != 0;
+                ended = t.lists.meta[l].last;
+                __syncwarp();
+                if (lead) mbar_arrive(&t.lists.empty[l]);
+                ++lists;
+            }
+            return i < n;
+        };
+        // the last piece's O on tile x has been read
+        auto free_of = [&](uint32_t x) { ok = ok && wait_warp(&t.o_free[x][(u - 1) & 1], ((u - 1) >> 1) & 1, stop, err); };
+        ok = wait_warp(&t.q_full, u & 1, stop, err);
+        if (X == 1 && !two) {
+            // the other warp's lists: this one sees and releases their tiles all the same
+            if (ok && lead) mbar_arrive(&t.q_empty);
+            int seen = 0;
+            for (int i = 0; ok; ++i) {
+                const bool have = there_is(i);
+                for (const int upto = have ? 2 * i + 1 : 2 * n; ok && seen < upto; ++seen) {
+                    wait_full(base + seen);
+                    if (ok && lead) mbar_arrive(&t.empty[(base + seen) % kStages]);
+                }
+                if (!have) break;
+            }
+        } else {
+            if (two != was_two && u) {            // tiles change hands: the products on them have ended
+                free_of(0), free_of(1);
+            }
+            const int by = two ? 1 : 2;
+            const uint32_t q = uniform(desc_low(saddr(sq) + (two ? X * C::kBytes : 0u), 16));
+            // S of list i on tile x; pass: the other tile's turn comes when half of it is issued
+            auto issue_s = [&](int i, uint32_t x, bool pass) {
+                const uint32_t at = base + at_k(i);
+                wait_full(at);
+                if (!ok) return;
+                tc_after();
+                const uint32_t kd = desc(at, 16), ts = uniform(kTmem + kColS + x * kTile);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = ((k >> 2) * C::kBlock + (k & 3) * 32) >> 4;
+                    if (k == D / 32 && pass && lead) mbar_arrive(&t.turn[x ^ 1]);
+                    mma_ss(ts, q + off, kd + off, idesc(kTile, false), k > 0, lead);
+                }
+                mma_commit(saddr(&t.s_full[x]), lead);
+                mma_commit(saddr(&t.empty[at % kStages]), lead);
+            };
+            bool more = ok && there_is(0);
+            if (more) issue_s(0, two ? X : 0u, false);
+            if (more && !two && there_is(1)) issue_s(1, 1, false);
+            if (!more && ok) mma_commit(saddr(&t.q_empty), lead);
+            for (int i = 0; ok && more; ++i) {
+                const uint32_t x = two ? X : (uint32_t)i & 1;
+                more = there_is(i + by);
+                const bool last = ended && i == n - 1;
+                if (!more && (two || last || i + 2 == n)) {
+                    // no further S: Q is released with the last one (of two tiles' lists, once)
+                    if (two || last) mma_commit(saddr(&t.q_empty), lead);
+                }
+                const uint32_t at = base + at_v(i, last);
+                wait_full(at);
+                if (u && i < by) free_of(x);
+                if (two && (X == 1 || i > 0)) ok = ok && wait_warp(&t.turn[X], turns++ & 1, stop, err);
+                const uint32_t step = x ? steps1 : steps0;
+                const uint32_t vd = desc(at, C::kBlock), ts = uniform(kTmem + kColS + x * kTile), to = uniform(kTmem + kColO + x * D);
+                ok = ok && wait_warp(&t.p_full[x][0], step & 1, stop, err);
+                if (!ok) break;
+                tc_after();
+#pragma unroll
+                for (int k = 0; k < kTile / 32; ++k)
+                    mma_ts(to, ts + k * 8, vd + k * (2048 >> 4), idesc(D, true), i >= by || k > 0, lead);
+                if (!(ok = wait_warp(&t.p_full[x][1], step & 1, stop, err))) break;
+                tc_after();
+#pragma unroll
+                for (int k = kTile / 32; k < kTile / 16; ++k)
+                    mma_ts(to, ts + k * 8, vd + k * (2048 >> 4), idesc(D, true), 1, lead);
+                if (x) ++steps1; else ++steps0;
+                if (more) {
+                    issue_s(i + by, x, two);      // writes over the P read above: one thread's MMAs run in the order of issue
+                } else {
+                    if (two && X == 0 && lead) mbar_arrive(&t.turn[1]);
+                    mma_commit(saddr(&t.o_done[x]), lead);
+                }
+                mma_commit(saddr(&t.empty[at % kStages]), lead);
+                if (!two) more = more || !last;   // (the other tile's last list may still come)
+            }
         }
-        for (int j = 0; j <= pos; ++j) {
-            const int slot = live_slot(a.map, row, j, err);
-            if (slot < 0) continue;
-            float dot = 0.f;
-            for (int e = 0; e < kPer; ++e)
-                dot += q[e] * __bfloat162float(a.k[(int64_t)slot * a.k_stride + (int64_t)g * D + lane + 32 * e]);
-            for (int k = 16; k; k >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, k);
-            dot *= a.scale;
-            const float top = !(dot <= m) ? dot : m, f = m == top ? 1.f : expf(m - top), p = dot == -INFINITY ? 0.f : expf(dot - top);
-            m = top;
-            l = l * f + p;
-            for (int e = 0; e < kPer; ++e)
-                o[e] = o[e] * f + p * __bfloat162float(a.v[(int64_t)slot * a.v_stride + (int64_t)g * D + lane + 32 * e]);
-        }
-        const int64_t at = (int64_t)(x.first + i) * a.Hq + h;
-        for (int e = 0; e < kPer; ++e) a.out[at * D + lane + 32 * e] = __float2bfloat16_rn(l == 0.f ? 0.f : o[e] / l);
-        if (a.lse && lane == 0) a.lse[at] = l == 0.f ? -INFINITY : m + logf(l);
+        if (!ok) break;
+        base += 2 * n;
+        if (two && X == 0) steps1 += n;
+        if (two && X == 1) steps0 += n;
+        if (!two && X == 1) steps0 += (n + 1) / 2, steps1 += n / 2;
+        was_two = two;
     }
-    if (err) atomicOr(a.err, err);
+    mma_commit(saddr(&t.drained), lead);
+    drain_phase(&t.drained, 0);
 }
 
-}  // namespace
+// ---- shares ----------------------------------------------------------------
+// The work of one kv head, in keys: units in the order of sessions and tokens, kStart lists for the start of each and then
+// the keys that its last row sees, counted as if the last unit of a session were full (which makes a session's sum a
+// closed form).
+struct Cut {
+    int64_t lead;                       // keys of the session before its new tokens, and the start
+    int unit;                           // tokens of a unit
+    __device__ __forceinline__ int64_t before(int64_t t) const { return t * lead + unit * (t * (t + 1) / 2); }
+};
+__device__ __forceinline__ Cut cut_of(const Session& x, int unit) {
+    return Cut{(int64_t)max(0, x.len - x.count) + kStart * kTile, unit};
+}
+__device__ __forceinline__ int units_of(const Session& x, int unit) { return (int)(((int64_t)x.count + unit - 1) / unit); }
+__device__ __forceinline__ int64_t warp_sum(int64_t v) {
+#pragma unroll
+    for (int k = 16; k; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
+    return v;
+}
 
-extern "C" int kvsel_pool_attention(kvsel_ctx* ctx, const void* q, int64_t q_stride, const int32_t* cu_new, int S, int T,
-                                    int Hq, int Hkv, int D, const void* k_pool, const void* v_pool, int64_t k_stride,
-                                    int64_t v_stride, int P, int page, const int32_t* seq_lens, const int32_t* slot_map,
-                                    const int32_t* block_table, int ld, int dead_slot, float scale, void* out, float* lse,
-                                    void* stream) {
-    const kvsel_trace trace_("kvsel_pool_attention");
+// ---- the kernel ------------------------------------------------------------
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    pool_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                          const __grid_constant__ CUtensorMap map_v, const PoolArgs a) {
+    using C = Cfg<D>;
+    constexpr int kStages = C::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    uint8_t* const sq = smem;                     // [2][kBytes]
+    uint8_t* const ring = smem + 2 * C::kBytes;   // [kStages][kBytes]
+    typename C::Tail& t = *reinterpret_cast<typename C::Tail*>(smem + (2 + kStages) * C::kBytes + C::kOut);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = (int)(blockIdx.x % a.Hkv), share = (int)(blockIdx.x / a.Hkv);
+    Stop* const stop = &t.stop;
+
+    if (threadIdx.x == 0) {
+        mbar_init(&t.q_full, 1);
+        mbar_init(&t.q_empty, 2);
+        for (int i = 0; i < kStages; ++i) mbar_init(&t.full[i], 1), mbar_init(&t.empty[i], 2);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&t.s_full[i], 1);
+            mbar_init(&t.p_full[i][0], 4);
+            mbar_init(&t.p_full[i][1], 4);
+            mbar_init(&t.o_done[i], 1);
+            mbar_init(&t.o_free[i][0], 4);
+            mbar_init(&t.o_free[i][1], 4);
+            mbar_init(&t.turn[i], 1);
+            mbar_init(&t.merge[i], 4);
+            mbar_init(&t.piece_full[i], 1);
+            mbar_init(&t.piece_empty[i], 1 + 2 + 8);  // the loads, the issuers, the softmax warps
+        }
+        for (int i = 0; i < kLists; ++i) mbar_init(&t.lists.full[i], 1), mbar_init(&t.lists.empty[i], 1 + 2 + 8);
+        mbar_init(&t.drained, 2);
+        mbar_init(&t.never, 1);
+        t.stop.given_up = 0;
+        t.stop.limit_ns = a.wait_ns;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&t.tmem)), "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = t.tmem;
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
+        if (warp == 3) {
+            // ---- loads: one thread ----
+            if (lane == 0) {
+                uint32_t c = 0, l = 0, loaded_q = 0;  // ring places filled, lists, Q loads
+                bool ok = true;
+                auto load = [&](const CUtensorMap* map, const int* slots) {
+                    const uint32_t st = c % kStages;
+                    if (!(ok = wait_phase(&t.empty[st], (c / kStages & 1) ^ 1u, stop, a.err))) return;
+                    mbar_expect_tx(&t.full[st], C::kBytes);
+                    load_rows<D>(map, &t.full[st], ring + st * C::kBytes, g * D, slots);
+                    ++c;
+                };
+                for (uint32_t u = 0; ok; ++u) {
+                    if (!(ok = wait_phase(&t.piece_full[u & 1], (u >> 1) & 1, stop, a.err))) break;
+                    const typename C::Piece w = t.piece[u & 1];
+                    mbar_arrive(&t.piece_empty[u & 1]);
+                    if (w.end) break;
+                    if (u && !(ok = wait_phase(&t.q_empty, (u - 1) & 1, stop, a.err))) break;
+                    mbar_expect_tx(&t.q_full, (1 + w.two) * (D / 64) * a.tile_tokens * a.G * 128);
+                    for (int x = 0; x < 1 + w.two; ++x)
+                        for (int b = 0; b < D / 64; ++b)
+                            tma_load(&map_q, &t.q_full, sq + x * C::kBytes + b * C::kBlock, 64 * b, g * a.G,
+                                     w.row + x * a.tile_tokens);
+                    ++loaded_q;
+                    bool last = false;
+                    for (int i = 0; ok && !last; ++i, ++l) {
+                        if (!(ok = wait_phase(&t.lists.full[l % kLists], l / kLists & 1, stop, a.err))) break;
+                        last = t.lists.meta[l % kLists].last;
+                        if (t.lists.meta[l % kLists].n == 0) {
+                            mbar_arrive(&t.lists.empty[l % kLists]);
+                            continue;
+                        }
+                        load(&map_k, t.lists.slot + l % kLists * kTile);
+                        if (ok && i > 0) {
+                            load(&map_v, t.lists.slot + (l - 1) % kLists * kTile);
+                            mbar_arrive(&t.lists.empty[(l - 1) % kLists]);
+                        }
+                        if (ok && last) {
+                            load(&map_v, t.lists.slot + l % kLists * kTile);
+                            mbar_arrive(&t.lists.empty[l % kLists]);
+                        }
+                    }
+                }
+                if (loaded_q) drain_phase(&t.q_full, (loaded_q - 1) & 1);
+                for (uint32_t at = c > kStages ? c - kStages : 0; at < c; ++at) drain_phase(&t.full[at % kStages], at / kStages & 1);
+            }
+        } else if (warp == 1 || warp == 2) {
+            issue_tiles<D>(t, sq, ring, warp - 1, lane, a.stuck && warp == 1, stop, a.err);
+        } else {
+            // ---- the share's pieces, and their lists ----
+            unsigned err = 0;
+            bool ok = true;
+            uint32_t u = 0, made = 0;
+            auto publish = [&](const typename C::Piece& w) {
+                if (u >= 2 && !(ok = wait_warp(&t.piece_empty[u & 1], ((u >> 1) - 1) & 1, stop, a.err))) return;
+                if (lane == 0) {
+                    t.piece[u & 1] = w;
+                    t.odd[u & 1] = INT_MAX;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&t.piece_full[u & 1]);
+                ++u;
+            };
+            const int unit = 2 * a.tile_tokens;
+            int64_t total = 0;
+            for (int s = lane; s < a.S; s += 32) {
+                const Session x = session_at(a.cu, a.lens, a.T, a.map.reach, s);
+                total += cut_of(x, unit).before(units_of(x, unit));
+                if (blockIdx.x == 0) err |= session_errors(a.cu, a.lens, a.T, a.map.reach, s);
+            }
+            total = warp_sum(total);
+            const int64_t quota = max((total + a.shares - 1) / a.shares, (int64_t)kLeast * kTile);
+            const int64_t from = share * quota, to = from + quota;
+            int64_t at = 0;                       // where session s starts
+            if (lane == 0) a.joints[blockIdx.x].sharers = 0;
+            for (int s0 = 0; ok && s0 < a.S && at < to; s0 += 32) {
+                Session mine{0, 0, 0};
+                if (s0 + lane < a.S) mine = session_at(a.cu, a.lens, a.T, a.map.reach, s0 + lane);
+                const int64_t size = cut_of(mine, unit).before(units_of(mine, unit));
+                const int64_t all = warp_sum(size);
+                if (at + all <= from) {           // 32 sessions before the share
+                    at += all;
+                    continue;
+                }
+                for (int i = 0; ok && i < 32 && s0 + i < a.S && at < to; ++i) {
+                    Session x;
+                    x.first = __shfl_sync(0xffffffffu, mine.first, i);
+                    x.count = __shfl_sync(0xffffffffu, mine.count, i);
+                    x.len = __shfl_sync(0xffffffffu, mine.len, i);
+                    const int64_t here = __shfl_sync(0xffffffffu, size, i);
+                    if (at + here <= from) {
+                        at += here;
+                        continue;
+                    }
+                    const Cut cut = cut_of(x, unit);
+                    const int n = units_of(x, unit);
+                    int k = 0;                    // the first unit that ends behind the share's start
+                    for (int step = 1 << 24; step; step >>= 1)
+                        if (k + step <= n && at + cut.before(k + step) <= from) k += step;
+                    const int32_t* const row = a.map.map + (int64_t)(s0 + i) * a.map.ld;
+                    for (; ok && k < n; ++k) {
+                        const int64_t u0 = at + cut.before(k), u1 = at + cut.before(k + 1);
+                        if (u0 >= to) break;
+                        const int tok0 = k * unit, tokens = min(unit, x.count - tok0);
+                        const int keys = max(0, x.len - x.count + tok0 + tokens);
+                        const int lists = max(1, (int)(((int64_t)keys + kTile - 1) / kTile));
+                        auto list_at = [&](int64_t p) {   // lists of the unit that lie before place p of the work
+                            return (int)min((int64_t)lists, max((int64_t)0, (p - u0) / kTile - kStart));
+                        };
+                        const int l0 = from <= u0 ? 0 : list_at(from), l1 = to >= u1 ? lists : list_at(to);
+                        if (l0 >= l1) continue;
+                        typename C::Piece w;
+                        w.row = x.first + tok0;
+                        w.tokens = tokens;
+                        w.pos0 = x.len - x.count + tok0;
+                        w.session = s0 + i;
+                        w.stop = (int)min((int64_t)l1 * kTile, (int64_t)keys);
+                        w.part = l0 > 0 ? 0 : l1 < lists ? 1 : -1;
+                        w.two = tokens > a.tile_tokens;
+                        w.end = 0;
+                        if (w.part == 1 && lane == 0) {
+                            // the last share with some of it starts before its last list does
+                            const int64_t tail = min(u1, u0 + (int64_t)(lists + kStart) * kTile) - 1;
+                            a.joints[blockIdx.x] = Joint{(int)(tail / quota) - share + 1, w.row, tokens};
+                        }
+                        publish(w);
+                        ok = ok && make_lists(t.lists, a.map, row, l0 * kTile, w.stop, w.pos0, made, lane, stop, a.err, err);
+                    }
+                    at += here;
+                }
+            }
+            if (ok) {
+                typename C::Piece w{};
+                w.end = 1;
+                publish(w);
+            }
+            if (err) atomicOr(a.err, err);
+        }
+        __syncwarp();
+        tc_before();
+        __syncthreads();
+        tc_after();
+        if (warp == 1)
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+        return;
+    }
+
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+    // ---- softmax: one row per thread ----
+    const int x = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const int r_tok = r / a.G, r_head = g * a.G + r - r_tok * a.G;
+    const uint32_t lane_base = kTmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t ts = lane_base + kColS + x * kTile, to = lane_base + kColO + x * D;
+    const float sc = a.scale2;
+    uint32_t done = 0, mine = 0, base = 0, l = 0;  // this tile's steps and outputs, ring places and lists so far
+    bool ok = true;
+    for (uint32_t u = 0; ok; ++u) {
+        if (!(ok = wait_warp(&t.piece_full[u & 1], (u >> 1) & 1, stop, a.err))) break;
+        const typename C::Piece w = t.piece[u & 1];
+        __syncwarp();
+        if (w.end) break;
+        const int tok0 = w.two ? x * a.tile_tokens : 0, rows = min(a.tile_tokens, w.tokens - tok0) * a.G;
+        const bool active = quarter * 32 < rows;        // the warp has rows
+        const int row_pos = w.pos0 + tok0 + r_tok;
+        float ref = -3e38f;
+        float2 sum = make_float2(0.f, 0.f);
+        int n = 0, steps = 0;
+        bool last = false;
+        for (; !last; ++l) {
+            if (!(ok = wait_warp(&t.lists.full[l % kLists], l / kLists & 1, stop, a.err))) break;
+            const ListMeta meta = t.lists.meta[l % kLists];
+            last = meta.last;
+            const int i = n;
+            n += meta.n != 0;
+            if (meta.n && (w.two || (i & 1) == x)) {
+                if (!(ok = wait_warp(&t.s_full[x], done & 1, stop, a.err))) break;
+                auto clean_v = [&]() {
+                    // NaN and infinities of V to zero; both tiles look at all of it (a value may be set twice)
+                    const uint32_t at = base + at_v(i, last), st = at % kStages;
+                    if (!(ok = wait_warp(&t.full[st], at / kStages & 1, stop, a.err))) return;
+                    uint4* const tile = reinterpret_cast<uint4*>(ring + st * C::kBytes);
+#pragma unroll 4
+                    for (int e = r; e < C::kBytes / 16; e += kTile) {
+                        const uint4 v = tile[e];
+                        uint32_t y[4] = {v.x, v.y, v.z, v.w}, hit = 0;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) hit |= (y[k] & 0x7F807F80u) + 0x00800080u;
+                        if (hit & 0x80008000u) {
+                            atomicMin(&t.odd[u & 1], t.lists.pos[l % kLists * kTile]);
+                            __threadfence_block();
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                if ((y[k] & 0x7F80u) == 0x7F80u) y[k] &= 0xFFFF0000u;
+                                if ((y[k] & 0x7F800000u) == 0x7F800000u) y[k] &= 0x0000FFFFu;
+                            }
+                            tile[e] = make_uint4(y[0], y[1], y[2], y[3]);
+                        }
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                };
+                tc_after();
+                if (!active) {
+                    if (meta.masked) clean_v();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&t.p_full[x][0]), mbar_arrive(&t.p_full[x][1]);
+                } else {
+                    uint32_t s[kTile];
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) tmem_ld32(ts + 32 * b, s + 32 * b);
+                    tmem_wait_ld();
+                    if (meta.masked) {
+                        // the row sees the list's tokens up to its own position: those before place `seen`
+                        const int* const pos = t.lists.pos + l % kLists * kTile;
+                        int seen = 0;
+#pragma unroll
+                        for (int step = kTile; step; step >>= 1)
+                            if (seen + step <= meta.n && pos[seen + step - 1] <= row_pos) seen += step;
+#pragma unroll
+                        for (int c = 0; c < kTile; ++c)
+                            if (c >= seen) s[c] = 0xFF800000u;
+                    }
+                    float m[4];
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) m[b] = __uint_as_float(s[b]);
+#pragma unroll
+                    for (int c = 4; c + 8 <= kTile; c += 8)
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) m[b] = max3(m[b], __uint_as_float(s[c + b]), __uint_as_float(s[c + 4 + b]));
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) m[b] = fmaxf(m[b], __uint_as_float(s[kTile - 4 + b]));
+                    const float top = fmaxf(max3(m[0], m[1], m[2]), m[3]) * sc;
+                    if (steps == 0) {
+                        ref = fmaxf(top, -3e38f);  // of a row whose logits here are all -inf: low, and finite
+                    } else if (__any_sync(0xffffffffu, top > ref + kSlack)) {
+                        // references move up: the sums so far and O shrink with them
+                        const float next = fmaxf(ref, top), f = ex2(ref - next);
+                        ref = next;
+                        sum.x *= f, sum.y *= f;
+                        // (the commit that brought this S came after the last step's product: O is at rest)
+#pragma unroll 1
+                        for (int b = 0; b < D / 32; ++b) {
+                            uint32_t o[32];
+                            tmem_ld32(to + 32 * b, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+                            tmem_st32(to + 32 * b, o);
+                        }
+                    }
+                    if (meta.masked) clean_v();
+                    const float2 sc2 = make_float2(sc, sc), nr = make_float2(-ref, -ref);
+                    // in two halves, so that the product with V starts on the first while the second is worked out
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t p[kTile / 4];
+#pragma unroll
+                        for (int c = 0; c < kTile / 4; ++c) {
+                            const int e0 = half * (kTile / 2) + 2 * c;
+                            const float2 y = __ffma2_rn(make_float2(__uint_as_float(s[e0]), __uint_as_float(s[e0 + 1])), sc2, nr);
+                            const float2 e = make_float2(ex2(y.x), ex2(y.y));
+                            sum = __fadd2_rn(sum, e);
+                            p[c] = pack_bf16(e.x, e.y);
+                        }
+                        tmem_st32(ts + 32 * half, p);
+                        tmem_wait_st();
+                        tc_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&t.p_full[x][half]);
+                    }
+                }
+                if (!ok) break;
+                ++steps, ++done;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&t.lists.empty[l % kLists]);
+        }
+        if (!ok) break;
+        base += 2 * n;
+        // ---- output ----
+        if (steps && !(ok = wait_warp(&t.o_done[x], mine++ & 1, stop, a.err))) break;
+        tc_after();
+        float l_sum = sum.x + sum.y;
+        if (x == 1) {                                   // to the thread that has the row's other part, if that is so
+            t.other[u & 1][r] = make_float2(ref, l_sum);
+            tc_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&t.merge[u & 1]);
+        }
+        if (w.two || x == 0) {
+            uint32_t all[D];          // all at once, so that the next piece's products may start on O
+            if (steps && active) {
+#pragma unroll
+                for (int b = 0; b < D / 32; ++b) tmem_ld32(to + 32 * b, all + 32 * b);
+                tmem_wait_ld();
+            } else {
+#pragma unroll
+                for (int c = 0; c < D; ++c) all[c] = 0;
+            }
+            if (!w.two) {
+                if (!(ok = wait_warp(&t.merge[u & 1], (u >> 1) & 1, stop, a.err))) break;
+                tc_after();
+                if (n > 1 && active) {
+                    const float2 o = t.other[u & 1][r];
+                    const float next = fmaxf(ref, o.x), f0 = ex2(ref - next), f1 = ex2(o.x - next);
+                    ref = next;
+                    l_sum = l_sum * f0 + o.y * f1;
+#pragma unroll
+                    for (int b = 0; b < D / 16; ++b) {
+                        uint32_t y[16];
+                        tmem_ld16(to + D + 16 * b, y);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < 16; ++c)
+                            all[16 * b + c] = __float_as_uint(__uint_as_float(all[16 * b + c]) * f0 + __uint_as_float(y[c]) * f1);
+                    }
+                }
+                tc_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&t.o_free[1][u & 1]);
+            }
+            tc_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&t.o_free[x][u & 1]);
+            const int odd = *(volatile int*)&t.odd[u & 1];
+            const int64_t row_at = (int64_t)(w.row + tok0 + r_tok) * a.Hq + r_head;
+            float* const part = w.part < 0 ? nullptr : a.parts + ((size_t)blockIdx.x * 2 + w.part) * kPart + x * kPartTile;
+            if (active && part) {
+#pragma unroll
+                for (int c = 0; c < D / 4; ++c)
+                    reinterpret_cast<uint4*>(part)[c * kTile + r] = make_uint4(all[4 * c], all[4 * c + 1], all[4 * c + 2], all[4 * c + 3]);
+                part[kTile * 128 + r] = ref;
+                part[kTile * 129 + r] = l_sum;
+            } else if (active) {
+                // through shared memory, so that a store covers 64 bytes of each of eight rows; 16-byte pieces are swizzled by
+                // their row against bank conflicts
+                const float inv = l_sum == 0.f ? 0.f : 1.f / l_sum;
+                const int row_off = (tok0 + r_tok) * a.Hq + r_head;
+                uint8_t* const stage = smem + (2 + kStages) * C::kBytes + (warp - 4) * (32 * 64);
+#pragma unroll
+                for (int b = 0; b < D / 32; ++b) {
+                    const uint32_t* const o = all + 32 * b;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t e[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            e[k] = pack_bf16(__uint_as_float(o[8 * c + 2 * k]) * inv, __uint_as_float(o[8 * c + 2 * k + 1]) * inv);
+                        *reinterpret_cast<uint4*>(stage + lane * 64 + (c ^ ((lane >> 1) & 3)) * 16) = make_uint4(e[0], e[1], e[2], e[3]);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int rr = 8 * c + (lane >> 2), off = __shfl_sync(0xffffffffu, row_off, rr);
+                        const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 64 + ((lane & 3) ^ ((rr >> 1) & 3)) * 16);
+                        if (quarter * 32 + rr < rows)
+                            *reinterpret_cast<uint4*>(a.out + ((int64_t)w.row * a.Hq + off) * D + 32 * b + 8 * (lane & 3)) = v;
+                    }
+                    __syncwarp();
+                }
+                if (a.lse && r < rows) a.lse[row_at] = l_sum == 0.f ? -INFINITY : (ref + log2f(l_sum)) * kLn2;
+            }
+            if (odd != INT_MAX && r < rows) {
+                // what the row sees of the values that were set to zero: a sum of infinities and NaN
+                unsigned err = 0;
+                const int32_t* const map = a.map.map + (int64_t)w.session * a.map.ld;
+                const int upto = min(row_pos, w.stop - 1);
+#pragma unroll 1
+                for (int d = 0; d < D; ++d) {
+                    float add = 0.f;
+#pragma unroll 1
+                    for (int j = odd; j <= upto; ++j) {
+                        const int slot = live_slot(a.map, raw_entry(a.map, map, j), j, err);
+                        if (slot < 0) continue;
+                        const float e = __bfloat162float(a.v[(int64_t)slot * a.v_stride + (int64_t)g * D + d]);
+                        if (!(fabsf(e) < INFINITY)) add += e;
+                    }
+                    if (add == 0.f) continue;
+                    if (part)
+                        part[((d >> 2) * kTile + r) * 4 + (d & 3)] += add;
+                    else
+                        a.out[row_at * D + d] = __float2bfloat16_rn(__bfloat162float(a.out[row_at * D + d]) + add);
+                }
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&t.piece_empty[u & 1]);
+    }
+    tc_before();
+    __syncthreads();
+}
+
+// Joins the unit whose first keys block blockIdx.x has: 32 rows of a tile a block, a row per lane, four dims at a time.
+template <int D>
+__global__ void __launch_bounds__(256) pool_join_kernel(const PoolArgs a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Joint u = a.joints[blockIdx.x];
+    if (!u.sharers) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, x = blockIdx.y >> 2, r = (blockIdx.y & 3) * 32 + lane;
+    const int rows = min(a.tile_tokens, u.tokens - x * a.tile_tokens) * a.G;
+    if ((int)(blockIdx.y & 3) * 32 >= rows) return;
+    auto part = [&](int k) {
+        return a.parts + ((size_t)(blockIdx.x + k * a.Hkv) * 2 + (k == 0)) * kPart + x * kPartTile;
+    };
+    float top = -3e38f, sum = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < u.sharers; ++k) top = fmaxf(top, part(k)[kTile * 128 + r]);
+    float4 o[D / 32];
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int k = 0; k < u.sharers; ++k) {
+        const float* const p = part(k);
+        const float f = ex2(p[kTile * 128 + r] - top);
+        sum += f * p[kTile * 129 + r];
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+            const float4 y = reinterpret_cast<const float4*>(p)[(warp + 8 * c) * kTile + r];
+            o[c].x += f * y.x, o[c].y += f * y.y, o[c].z += f * y.z, o[c].w += f * y.w;
+        }
+    }
+    if (r >= rows) return;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int tok = r / a.G;
+    const int64_t at = (int64_t)(u.row + x * a.tile_tokens + tok) * a.Hq + (int)(blockIdx.x % a.Hkv) * a.G + r - tok * a.G;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c)
+        *reinterpret_cast<uint2*>(a.out + at * D + (warp + 8 * c) * 4) =
+            make_uint2(pack_bf16(o[c].x * inv, o[c].y * inv), pack_bf16(o[c].z * inv, o[c].w * inv));
+    if (a.lse && warp == 0) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+}
+
+template <int D>
+cudaError_t launch(kvsel_ctx* ctx, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const PoolArgs& a,
+                   cudaStream_t s) {
+    auto* kernel = pool_attention_kernel<D>;
+    constexpr unsigned kBit = D == 64 ? KVSEL_READY_POOL64 : KVSEL_READY_POOL128;
+    if (!(ctx->ready & kBit)) {
+        cudaFuncAttributes fa;
+        cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
+        if (e != cudaSuccess) return e;
+        if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;  // the register split counts on it
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<D>::kSmem);
+        if (e != cudaSuccess) return e;
+        ctx->ready |= kBit;
+    }
+    kernel<<<(unsigned)a.shares * a.Hkv, kThreads, Cfg<D>::kSmem, s>>>(mq, mk, mv, a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || a.shares == 1) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.shares * a.Hkv, 8);
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, pool_join_kernel<D>, a);
+}
+
+int attention_call(kvsel_ctx* ctx, const void* q, int64_t q_stride, const int32_t* cu_new, int S, int T, int Hq, int Hkv, int D,
+                   const void* k_pool, const void* v_pool, int64_t k_stride, int64_t v_stride, int P, int page,
+                   const int32_t* seq_lens, const int32_t* slot_map, const int32_t* block_table, int ld, int dead_slot,
+                   float scale, void* out, float* lse, void* stream, uint64_t wait_ns, int stuck) {
     const kvsel_device_scope scope_;
     int rc = kvsel_enter(ctx);
     if (rc) return rc;
@@ -80,13 +787,48 @@ extern "C" int kvsel_pool_attention(kvsel_ctx* ctx, const void* q, int64_t q_str
     if (!q || !cu_new || !seq_lens || !out) return kvsel_fail(ctx, KVSEL_ERR_INVALID_ARG, "pool_attention: null pointer");
     if ((reinterpret_cast<uintptr_t>(q) & 15u) || (reinterpret_cast<uintptr_t>(out) & 15u))
         return kvsel_fail(ctx, KVSEL_ERR_ALIGN, "pool_attention: q and out must be 16-byte aligned");
-    const PoolArgs a{(const __nv_bfloat16*)q, q_stride, cu_new, seq_lens, S, T, Hq, Hkv, (const __nv_bfloat16*)k_pool,
-                     (const __nv_bfloat16*)v_pool, k_stride, v_stride, map, scale, (__nv_bfloat16*)out, lse, ctx->dev_err};
-    const dim3 grid((unsigned)min((int64_t)T * Hq / 8 + 1, (int64_t)8 * ctx->num_sms), S);
-    if (D == 64)
-        pool_attention_kernel<64><<<grid, 256, 0, (cudaStream_t)stream>>>(a);
-    else
-        pool_attention_kernel<128><<<grid, 256, 0, (cudaStream_t)stream>>>(a);
-    const cudaError_t e = cudaGetLastError();
+    const int G = Hq / Hkv, tile_tokens = kTile / G;
+    CUtensorMap mq, mk, mv;
+    if (!make_query_map(&mq, q, T, Hq, D, q_stride, G, tile_tokens) ||
+        (P > 0 && (!make_pool_map(&mk, k_pool, P * page, Hkv, D, k_stride) ||
+                   !make_pool_map(&mv, v_pool, P * page, Hkv, D, v_stride))))
+        return kvsel_fail(ctx, KVSEL_ERR_CUDA, "pool_attention: tensor map encoding failed");
+    if (P == 0) mk = mv = mq;           // nothing is live
+    float* const parts = (float*)ctx->pool_parts;
+    const PoolArgs a{cu_new, seq_lens, S, T, Hq, Hkv, G, tile_tokens, (const __nv_bfloat16*)v_pool, v_stride, map, scale * kLog2e,
+                     (__nv_bfloat16*)out, lse, ctx->dev_err, Hkv < ctx->num_sms ? ctx->num_sms / Hkv : 1, parts,
+                     (Joint*)(parts + (size_t)ctx->num_sms * 2 * kPart), wait_ns, stuck};
+    const cudaError_t e = D == 64 ? launch<64>(ctx, mq, mk, mv, a, (cudaStream_t)stream) : launch<128>(ctx, mq, mk, mv, a, (cudaStream_t)stream);
     return e == cudaSuccess ? KVSEL_OK : kvsel_cuda_fail(ctx, e, "pool_attention launch");
+}
+
+}  // namespace
+
+// Partial results and joints of the blocks: as many as there are SMs, or kv heads where those are more (their blocks have
+// whole units and only clear their joints).
+size_t pool_parts_bytes(int num_sms) { return (size_t)num_sms * 2 * kPart * sizeof(float) + (size_t)65536 * sizeof(Joint); }
+
+extern "C" int kvsel_pool_attention(kvsel_ctx* ctx, const void* q, int64_t q_stride, const int32_t* cu_new, int S, int T,
+                                    int Hq, int Hkv, int D, const void* k_pool, const void* v_pool, int64_t k_stride,
+                                    int64_t v_stride, int P, int page, const int32_t* seq_lens, const int32_t* slot_map,
+                                    const int32_t* block_table, int ld, int dead_slot, float scale, void* out, float* lse,
+                                    void* stream) {
+    const kvsel_trace trace_("kvsel_pool_attention");
+    return attention_call(ctx, q, q_stride, cu_new, S, T, Hq, Hkv, D, k_pool, v_pool, k_stride, v_stride, P, page, seq_lens,
+                          slot_map, block_table, ld, dead_slot, scale, out, lse, stream, kWaitNs, 0);
+}
+
+// Test entry (not part of the public header): kvsel_pool_attention in which the issuer of tile 0 of every block waits on a
+// barrier that nothing completes, with every wait limited to wait_ns.  It gives up while copies are in flight; out and lse
+// hold no meaningful values afterwards.
+extern "C" int kvsel_test_pool_attention_give_up(kvsel_ctx* ctx, const void* q, int64_t q_stride, const int32_t* cu_new, int S,
+                                                 int T, int Hq, int Hkv, int D, const void* k_pool, const void* v_pool,
+                                                 int64_t k_stride, int64_t v_stride, int P, int page, const int32_t* seq_lens,
+                                                 const int32_t* slot_map, const int32_t* block_table, int ld, int dead_slot,
+                                                 float scale, void* out, float* lse, uint64_t wait_ns, void* stream) {
+    const kvsel_trace trace_("kvsel_test_pool_attention_give_up");
+    if (wait_ns == 0 || wait_ns > kWaitNs)
+        return kvsel_fail(ctx, KVSEL_ERR_INVALID_ARG, "test_pool_attention_give_up: wait_ns must be in (0, 1 s]");
+    return attention_call(ctx, q, q_stride, cu_new, S, T, Hq, Hkv, D, k_pool, v_pool, k_stride, v_stride, P, page, seq_lens,
+                          slot_map, block_table, ld, dead_slot, scale, out, lse, stream, wait_ns, 1);
 }

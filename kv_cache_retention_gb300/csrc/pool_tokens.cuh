@@ -22,15 +22,17 @@ struct Session {
     int first, count, len;
 };
 
-// Slot of position j of session s, below the map's reach; -1 where it is not live.
-__device__ __forceinline__ int live_slot(const TokenMap& m, const int32_t* row, int j, unsigned& err) {
-    int slot;
-    if (m.page == 0) {
-        slot = __ldg(row + j);
-    } else {
-        const int b = m.page_shift >= 0 ? j >> m.page_shift : j / m.page, pg = __ldg(row + b);
-        if (pg >= m.n_pages) err |= KVSEL_DEV_BAD_PAGE;
-        slot = pg < 0 || pg >= m.n_pages ? -1 : pg * m.page + (j - b * m.page);
+// What the map says of position j (below its reach): a slot, or the page that holds it.
+__device__ __forceinline__ int raw_entry(const TokenMap& m, const int32_t* row, int j) {
+    return __ldg(row + (m.page == 0 ? j : m.page_shift >= 0 ? j >> m.page_shift : j / m.page));
+}
+// Slot of position j, from its entry; -1 where it is not live.
+__device__ __forceinline__ int live_slot(const TokenMap& m, int entry, int j, unsigned& err) {
+    int slot = entry;
+    if (m.page != 0) {
+        if (entry >= m.n_pages) err |= KVSEL_DEV_BAD_PAGE;
+        if (entry < 0 || entry >= m.n_pages) return -1;
+        slot = entry * m.page + (m.page_shift >= 0 ? j & (m.page - 1) : j % m.page);
     }
     if (slot < 0 || slot == m.dead) return -1;
     if (slot >= m.n_slots) {
