@@ -8,7 +8,7 @@
 // one session and kv head.
 //
 // Keys go through lists of 128 live tokens that one warp makes from the map (dropped tokens cost an entry's read and no
-// more); their rows come by TMA gathers of four slots.  Per list and tile
+// more); their rows come by cp.async.  Per list and tile
 //   S = Q K^T   tcgen05.mma, both operands from shared memory, 128 fp32 columns
 //   P = 2^(S sc - ref) in bf16, written over S in TMEM
 //   O += P V    tcgen05.mma, P from TMEM, V from shared memory as it lies
@@ -21,8 +21,8 @@
 // since both operands of the product have one type and V's range is bf16's: 2^-8 at most per weight, at random, about the
 // output's own rounding.
 //
-// 384 threads: warp 0 plans and makes the lists, warps 1 and 2 issue the MMAs of one tile each (warp 1 of both, where the
-// rows are one tile's), warp 3 loads, warps 4-7 and 8-11 are the softmax of the two tiles, a row per thread.  TMEM: S of
+// 512 threads: warp 0 plans and makes the lists, warps 1 and 2 issue the MMAs of one tile each (warp 1 of both, where the
+// rows are one tile's), warps 4-7 load, warps 8-11 and 12-15 are the softmax of the two tiles, a row per thread.  TMEM: S of
 // tile 0 and 1 at columns 0 and 128, O at 256 and on.
 //
 // Shares.  The units' keys, laid end to end with some for the start of each, are cut into equal shares, found from the
@@ -42,12 +42,12 @@
 
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
 constexpr float kSlack = 8.f;           // how far (log2) a row's maximum may pass its reference
 // Registers per thread: at launch, then after the first warpgroup's setmaxnreg.dec and the softmax warpgroups' .inc.  An
 // .inc beyond the launch's registers would wait forever; the launcher checks the compiled count.
-constexpr int kRegsLaunch = 168, kRegsCtl = 80, kRegsSoft = 208;
-static_assert(kRegsCtl + 2 * kRegsSoft <= 3 * kRegsLaunch && kRegsLaunch * kThreads <= 65536, "register split");
+constexpr int kRegsLaunch = 128, kRegsCtl = 56, kRegsSoft = 200;
+static_assert(2 * kRegsCtl + 2 * kRegsSoft <= 4 * kRegsLaunch && kRegsLaunch * kThreads <= 65536, "register split");
 constexpr int kLists = 8;
 constexpr int kStart = 4;               // lists that the start of a unit counts as when shares are cut
 constexpr int kLeast = 4;               // lists that a share has at least, so cut
@@ -68,8 +68,8 @@ struct PoolArgs {
     const int32_t *cu, *lens;
     int S, T, Hq, Hkv, G;
     int tile_tokens;                    // tokens of a tile
-    const __nv_bfloat16* v;
-    int64_t v_stride;
+    const __nv_bfloat16 *k, *v;
+    uint32_t k_bytes, v_bytes;          // from a slot's rows to the next one's
     TokenMap map;
     float scale2;                       // scale * log2(e)
     __nv_bfloat16* out;
@@ -127,11 +127,9 @@ __device__ __forceinline__ void issue_tiles(typename Cfg<D>::Tail& t, const uint
     const uint32_t lead = lane == 0, X = uniform(tile);
     uint32_t base = 0, lists = 0, turns = 0, steps0 = 0, steps1 = 0;  // ring places, lists, turns and the tiles' steps so far
     bool was_two = false;
-    bool ok = !stuck || wait_warp(&t.never, 0, stop, err);
-    auto desc = [&](uint32_t at, uint32_t leading) { return uniform(desc_low(saddr(ring) + at % kStages * C::kBytes, leading)); };
-    auto wait_full = [&](uint32_t at) { ok = ok && wait_warp(&t.full[at % kStages], at / kStages & 1, stop, err); };
+    bool ok = !stuck || wait_short(&t.never, 0, stop, err);
     for (uint32_t u = 0; ok; ++u) {
-        if (!(ok = wait_warp(&t.piece_full[u & 1], (u >> 1) & 1, stop, err))) break;
+        if (!(ok = wait_short(&t.piece_full[u & 1], (u >> 1) & 1, stop, err))) break;
         const bool two = t.piece[u & 1].two, end = t.piece[u & 1].end;
         __syncwarp();
         if (lead) mbar_arrive(&t.piece_empty[u & 1]);
@@ -139,9 +137,10 @@ __device__ __forceinline__ void issue_tiles(typename Cfg<D>::Tail& t, const uint
         int n = 0;                                // lists of the piece so far
         bool ended = false;
         auto there_is = [&](int i) {              // list i
+#pragma unroll 1
             while (ok && !ended && n <= i) {
                 const uint32_t l = lists % kLists;
-                if (!(ok = wait_warp(&t.lists.full[l], lists / kLists & 1, stop, err))) break;
+                if (!(ok = wait_short(&t.lists.full[l], lists / kLists & 1, stop, err))) break;
                 n += t.lists.meta[l].n != 0;
                 ended = t.lists.meta[l].last;
                 __syncwarp();
@@ -150,88 +149,87 @@ __device__ __forceinline__ void issue_tiles(typename Cfg<D>::Tail& t, const uint
             }
             return i < n;
         };
-        // the last piece's O on tile x has been read
-        auto free_of = [&](uint32_t x) { ok = ok && wait_warp(&t.o_free[x][(u - 1) & 1], ((u - 1) >> 1) & 1, stop, err); };
-        ok = wait_warp(&t.q_full, u & 1, stop, err);
+        ok = wait_short(&t.q_full, u & 1, stop, err);
+        if (two != was_two && u) {                // tiles may change hands: the products on them have ended
+#pragma unroll 1
+            for (int x = 0; x < 2; ++x) ok = ok && wait_short(&t.o_free[x][(u - 1) & 1], ((u - 1) >> 1) & 1, stop, err);
+        }
         if (X == 1 && !two) {
             // the other warp's lists: this one sees and releases their tiles all the same
             if (ok && lead) mbar_arrive(&t.q_empty);
             int seen = 0;
+#pragma unroll 1
             for (int i = 0; ok; ++i) {
                 const bool have = there_is(i);
+#pragma unroll 1
                 for (const int upto = have ? 2 * i + 1 : 2 * n; ok && seen < upto; ++seen) {
-                    wait_full(base + seen);
-                    if (ok && lead) mbar_arrive(&t.empty[(base + seen) % kStages]);
+                    const uint32_t at = base + seen;
+                    ok = wait_short(&t.full[at % kStages], at / kStages & 1, stop, err);
+                    if (ok && lead) mbar_arrive(&t.empty[at % kStages]);
                 }
                 if (!have) break;
             }
+            steps0 += (n + 1) / 2, steps1 += n / 2;
         } else {
-            if (two != was_two && u) {            // tiles change hands: the products on them have ended
-                free_of(0), free_of(1);
-            }
             const int by = two ? 1 : 2;
             const uint32_t q = uniform(desc_low(saddr(sq) + (two ? X * C::kBytes : 0u), 16));
-            // S of list i on tile x; pass: the other tile's turn comes when half of it is issued
-            auto issue_s = [&](int i, uint32_t x, bool pass) {
-                const uint32_t at = base + at_k(i);
-                wait_full(at);
-                if (!ok) return;
-                tc_after();
-                const uint32_t kd = desc(at, 16), ts = uniform(kTmem + kColS + x * kTile);
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = ((k >> 2) * C::kBlock + (k & 3) * 32) >> 4;
-                    if (k == D / 32 && pass && lead) mbar_arrive(&t.turn[x ^ 1]);
-                    mma_ss(ts, q + off, kd + off, idesc(kTile, false), k > 0, lead);
-                }
-                mma_commit(saddr(&t.s_full[x]), lead);
-                mma_commit(saddr(&t.empty[at % kStages]), lead);
-            };
-            bool more = ok && there_is(0);
-            if (more) issue_s(0, two ? X : 0u, false);
-            if (more && !two && there_is(1)) issue_s(1, 1, false);
-            if (!more && ok) mma_commit(saddr(&t.q_empty), lead);
-            for (int i = 0; ok && more; ++i) {
+            bool released = false;
+            // Round i: O += P V of list i (from 0 on), then S of list i + by on the same tile (while there is one).
+#pragma unroll 1
+            for (int i = -by; ok; ++i) {
                 const uint32_t x = two ? X : (uint32_t)i & 1;
-                more = there_is(i + by);
-                const bool last = ended && i == n - 1;
-                if (!more && (two || last || i + 2 == n)) {
-                    // no further S: Q is released with the last one (of two tiles' lists, once)
-                    if (two || last) mma_commit(saddr(&t.q_empty), lead);
+                const uint32_t ts = uniform(kTmem + kColS + x * kTile), to = uniform(kTmem + kColO + x * D);
+                const bool more = there_is(i + by), product = i >= 0, done = ended && i + 1 >= n;
+                if (!more && !released) {         // no further S: Q is released when the ones issued have ended
+                    mma_commit(saddr(&t.q_empty), lead);
+                    released = true;
                 }
-                const uint32_t at = base + at_v(i, last);
-                wait_full(at);
-                if (u && i < by) free_of(x);
-                if (two && (X == 1 || i > 0)) ok = ok && wait_warp(&t.turn[X], turns++ & 1, stop, err);
-                const uint32_t step = x ? steps1 : steps0;
-                const uint32_t vd = desc(at, C::kBlock), ts = uniform(kTmem + kColS + x * kTile), to = uniform(kTmem + kColO + x * D);
-                ok = ok && wait_warp(&t.p_full[x][0], step & 1, stop, err);
+                const uint32_t av = base + at_v(i, ended && i == n - 1), ak = base + at_k(i + by);
+                if (product) {
+                    ok = ok && wait_short(&t.full[av % kStages], av / kStages & 1, stop, err);
+                    if (u && i < by) ok = ok && wait_short(&t.o_free[x][(u - 1) & 1], ((u - 1) >> 1) & 1, stop, err);
+                    if (two && (X == 1 || i > 0)) ok = ok && wait_short(&t.turn[X], turns++ & 1, stop, err);
+                    const uint32_t step = x ? steps1 : steps0;
+                    const uint32_t vd = uniform(desc_low(saddr(ring) + av % kStages * C::kBytes, C::kBlock));
+#pragma unroll 1
+                    for (int half = 0; half < 2; ++half) {
+                        ok = ok && wait_short(&t.p_full[x][half], step & 1, stop, err);
+                        if (!ok) break;
+                        fence_async();
+                        tc_after();
+                        const uint32_t th = uniform(ts + half * (kTile / 4)), vh = uniform(vd + half * (kTile / 32) * (2048 >> 4));
+#pragma unroll
+                        for (int k = 0; k < kTile / 32; ++k)
+                            mma_ts(to, th + k * 8, vh + k * (2048 >> 4), idesc(D, true), i >= by || half || k > 0, lead);
+                    }
+                    if (x) ++steps1; else ++steps0;
+                }
                 if (!ok) break;
-                tc_after();
+                if (more) {                       // writes over the P read above: one thread's MMAs run in the order of issue
+                    if (!(ok = wait_short(&t.full[ak % kStages], ak / kStages & 1, stop, err))) break;
+                    fence_async();
+                    tc_after();
+                    const uint32_t kd = uniform(desc_low(saddr(ring) + ak % kStages * C::kBytes, 16));
 #pragma unroll
-                for (int k = 0; k < kTile / 32; ++k)
-                    mma_ts(to, ts + k * 8, vd + k * (2048 >> 4), idesc(D, true), i >= by || k > 0, lead);
-                if (!(ok = wait_warp(&t.p_full[x][1], step & 1, stop, err))) break;
-                tc_after();
-#pragma unroll
-                for (int k = kTile / 32; k < kTile / 16; ++k)
-                    mma_ts(to, ts + k * 8, vd + k * (2048 >> 4), idesc(D, true), 1, lead);
-                if (x) ++steps1; else ++steps0;
-                if (more) {
-                    issue_s(i + by, x, two);      // writes over the P read above: one thread's MMAs run in the order of issue
-                } else {
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t off = ((k >> 2) * C::kBlock + (k & 3) * 32) >> 4;
+                        // the other tile's turn: its issuer is under way while the last of these are issued
+                        if (k == D / 32 && two && product && lead) mbar_arrive(&t.turn[x ^ 1]);
+                        mma_ss(ts, q + off, kd + off, idesc(kTile, false), k > 0, lead);
+                    }
+                    mma_commit(saddr(&t.s_full[x]), lead);
+                    mma_commit(saddr(&t.empty[ak % kStages]), lead);
+                } else if (product) {
                     if (two && X == 0 && lead) mbar_arrive(&t.turn[1]);
                     mma_commit(saddr(&t.o_done[x]), lead);
                 }
-                mma_commit(saddr(&t.empty[at % kStages]), lead);
-                if (!two) more = more || !last;   // (the other tile's last list may still come)
+                if (product) mma_commit(saddr(&t.empty[av % kStages]), lead);
+                if (done) break;
             }
+            if (two && X == 0) steps1 += n;
+            if (two && X == 1) steps0 += n;
         }
-        if (!ok) break;
         base += 2 * n;
-        if (two && X == 0) steps1 += n;
-        if (two && X == 1) steps0 += n;
-        if (!two && X == 1) steps0 += (n + 1) / 2, steps1 += n / 2;
         was_two = two;
     }
     mma_commit(saddr(&t.drained), lead);
@@ -261,8 +259,7 @@ __device__ __forceinline__ int64_t warp_sum(int64_t v) {
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    pool_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                          const __grid_constant__ CUtensorMap map_v, const PoolArgs a) {
+    pool_attention_kernel(const __grid_constant__ CUtensorMap map_q, const PoolArgs a) {
     using C = Cfg<D>;
     constexpr int kStages = C::kStages;
     extern __shared__ uint8_t smem_raw[];
@@ -277,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         mbar_init(&t.q_full, 1);
         mbar_init(&t.q_empty, 2);
-        for (int i = 0; i < kStages; ++i) mbar_init(&t.full[i], 1), mbar_init(&t.empty[i], 2);
+        for (int i = 0; i < kStages; ++i) mbar_init(&t.full[i], 128), mbar_init(&t.empty[i], 2);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&t.s_full[i], 1);
             mbar_init(&t.p_full[i][0], 4);
@@ -288,9 +285,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&t.turn[i], 1);
             mbar_init(&t.merge[i], 4);
             mbar_init(&t.piece_full[i], 1);
-            mbar_init(&t.piece_empty[i], 1 + 2 + 8);  // the loads, the issuers, the softmax warps
+            mbar_init(&t.piece_empty[i], 4 + 2 + 8);  // the loads, the issuers, the softmax warps
         }
-        for (int i = 0; i < kLists; ++i) mbar_init(&t.lists.full[i], 1), mbar_init(&t.lists.empty[i], 1 + 2 + 8);
+        for (int i = 0; i < kLists; ++i) mbar_init(&t.lists.full[i], 1), mbar_init(&t.lists.empty[i], 4 + 2 + 8);
         mbar_init(&t.drained, 2);
         mbar_init(&t.never, 1);
         t.stop.given_up = 0;
@@ -307,63 +304,68 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_after();
     const uint32_t tmem = t.tmem;
 
-    if (warp < 4) {
+    if (warp < 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
-        if (warp == 3) {
-            // ---- loads: one thread ----
-            if (lane == 0) {
-                uint32_t c = 0, l = 0, loaded_q = 0;  // ring places filled, lists, Q loads
-                bool ok = true;
-                auto load = [&](const CUtensorMap* map, const int* slots) {
-                    const uint32_t st = c % kStages;
-                    if (!(ok = wait_phase(&t.empty[st], (c / kStages & 1) ^ 1u, stop, a.err))) return;
-                    mbar_expect_tx(&t.full[st], C::kBytes);
-                    load_rows<D>(map, &t.full[st], ring + st * C::kBytes, g * D, slots);
-                    ++c;
-                };
-                for (uint32_t u = 0; ok; ++u) {
-                    if (!(ok = wait_phase(&t.piece_full[u & 1], (u >> 1) & 1, stop, a.err))) break;
-                    const typename C::Piece w = t.piece[u & 1];
-                    mbar_arrive(&t.piece_empty[u & 1]);
-                    if (w.end) break;
-                    if (u && !(ok = wait_phase(&t.q_empty, (u - 1) & 1, stop, a.err))) break;
+        if (warp >= 4) {
+            // ---- loads ----
+            uint32_t c = 0, l = 0, loaded_q = 0;  // ring places filled, lists, Q loads
+            bool ok = true;
+            auto load = [&](const __nv_bfloat16* pool, uint32_t bytes, uint32_t list) {
+                const uint32_t st = c % kStages;
+                if (!(ok = wait_short(&t.empty[st], (c / kStages & 1) ^ 1u, stop, a.err))) return;
+                load_rows<D, 4>(pool + g * D, bytes, t.lists.slot + list % kLists * kTile, ring + st * C::kBytes, &t.full[st], warp - 4, lane);
+                ++c;
+            };
+            auto release = [&](uint32_t list) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&t.lists.empty[list % kLists]);
+            };
+            for (uint32_t u = 0; ok; ++u) {
+                if (!(ok = wait_short(&t.piece_full[u & 1], (u >> 1) & 1, stop, a.err))) break;
+                const typename C::Piece w = t.piece[u & 1];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&t.piece_empty[u & 1]);
+                if (w.end) break;
+                if (u && !(ok = wait_short(&t.q_empty, (u - 1) & 1, stop, a.err))) break;
+                if (warp == 4 && lane == 0) {
                     mbar_expect_tx(&t.q_full, (1 + w.two) * (D / 64) * a.tile_tokens * a.G * 128);
                     for (int x = 0; x < 1 + w.two; ++x)
                         for (int b = 0; b < D / 64; ++b)
                             tma_load(&map_q, &t.q_full, sq + x * C::kBytes + b * C::kBlock, 64 * b, g * a.G,
                                      w.row + x * a.tile_tokens);
-                    ++loaded_q;
-                    bool last = false;
-                    for (int i = 0; ok && !last; ++i, ++l) {
-                        if (!(ok = wait_phase(&t.lists.full[l % kLists], l / kLists & 1, stop, a.err))) break;
-                        last = t.lists.meta[l % kLists].last;
-                        if (t.lists.meta[l % kLists].n == 0) {
-                            mbar_arrive(&t.lists.empty[l % kLists]);
-                            continue;
-                        }
-                        load(&map_k, t.lists.slot + l % kLists * kTile);
-                        if (ok && i > 0) {
-                            load(&map_v, t.lists.slot + (l - 1) % kLists * kTile);
-                            mbar_arrive(&t.lists.empty[(l - 1) % kLists]);
-                        }
-                        if (ok && last) {
-                            load(&map_v, t.lists.slot + l % kLists * kTile);
-                            mbar_arrive(&t.lists.empty[l % kLists]);
-                        }
+                }
+                ++loaded_q;
+                // K of a list, then V of the one before it; V of the last
+                bool last = false;
+                int n = 0;
+#pragma unroll 1
+                for (int i = 0; ok && i <= n; ++i) {
+                    if (!last) {
+                        if (!(ok = wait_short(&t.lists.full[(l + i) % kLists], (l + i) / kLists & 1, stop, a.err))) break;
+                        const ListMeta meta = t.lists.meta[(l + i) % kLists];
+                        last = meta.last;
+                        n += meta.n != 0;
+                        if (!meta.n) release(l + i);
+                    }
+#pragma unroll 1
+                    for (int v = i < n ? 0 : 1; ok && v < (i > 0 ? 2 : 1); ++v) {
+                        load(v ? a.v : a.k, v ? a.v_bytes : a.k_bytes, l + i - v);
+                        if (v) release(l + i - 1);
                     }
                 }
-                if (loaded_q) drain_phase(&t.q_full, (loaded_q - 1) & 1);
-                for (uint32_t at = c > kStages ? c - kStages : 0; at < c; ++at) drain_phase(&t.full[at % kStages], at / kStages & 1);
+                l += max(n, 1);
             }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            if (warp == 4 && loaded_q) drain_phase(&t.q_full, (loaded_q - 1) & 1);
         } else if (warp == 1 || warp == 2) {
             issue_tiles<D>(t, sq, ring, warp - 1, lane, a.stuck && warp == 1, stop, a.err);
-        } else {
+        } else if (warp == 0) {
             // ---- the share's pieces, and their lists ----
             unsigned err = 0;
             bool ok = true;
             uint32_t u = 0, made = 0;
             auto publish = [&](const typename C::Piece& w) {
-                if (u >= 2 && !(ok = wait_warp(&t.piece_empty[u & 1], ((u >> 1) - 1) & 1, stop, a.err))) return;
+                if (u >= 2 && !(ok = wait_short(&t.piece_empty[u & 1], ((u >> 1) - 1) & 1, stop, a.err))) return;
                 if (lane == 0) {
                     t.piece[u & 1] = w;
                     t.odd[u & 1] = INT_MAX;
@@ -458,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
     // ---- softmax: one row per thread ----
-    const int x = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const int x = (warp - 8) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
     const int r_tok = r / a.G, r_head = g * a.G + r - r_tok * a.G;
     const uint32_t lane_base = kTmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t ts = lane_base + kColS + x * kTile, to = lane_base + kColO + x * D;
@@ -466,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t done = 0, mine = 0, base = 0, l = 0;  // this tile's steps and outputs, ring places and lists so far
     bool ok = true;
     for (uint32_t u = 0; ok; ++u) {
-        if (!(ok = wait_warp(&t.piece_full[u & 1], (u >> 1) & 1, stop, a.err))) break;
+        if (!(ok = wait_short(&t.piece_full[u & 1], (u >> 1) & 1, stop, a.err))) break;
         const typename C::Piece w = t.piece[u & 1];
         __syncwarp();
         if (w.end) break;
@@ -478,19 +480,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         int n = 0, steps = 0;
         bool last = false;
         for (; !last; ++l) {
-            if (!(ok = wait_warp(&t.lists.full[l % kLists], l / kLists & 1, stop, a.err))) break;
+            if (!(ok = wait_short(&t.lists.full[l % kLists], l / kLists & 1, stop, a.err))) break;
             const ListMeta meta = t.lists.meta[l % kLists];
             last = meta.last;
             const int i = n;
             n += meta.n != 0;
             if (meta.n && (w.two || (i & 1) == x)) {
-                if (!(ok = wait_warp(&t.s_full[x], done & 1, stop, a.err))) break;
-                auto clean_v = [&]() {
+                if (!(ok = wait_short(&t.s_full[x], done & 1, stop, a.err))) break;
+                if (meta.masked) {
                     // NaN and infinities of V to zero; both tiles look at all of it (a value may be set twice)
                     const uint32_t at = base + at_v(i, last), st = at % kStages;
-                    if (!(ok = wait_warp(&t.full[st], at / kStages & 1, stop, a.err))) return;
+                    if (!(ok = wait_short(&t.full[st], at / kStages & 1, stop, a.err))) break;
                     uint4* const tile = reinterpret_cast<uint4*>(ring + st * C::kBytes);
-#pragma unroll 4
+#pragma unroll 1
                     for (int e = r; e < C::kBytes / 16; e += kTile) {
                         const uint4 v = tile[e];
                         uint32_t y[4] = {v.x, v.y, v.z, v.w}, hit = 0;
@@ -507,12 +509,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tile[e] = make_uint4(y[0], y[1], y[2], y[3]);
                         }
                     }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    fence_async();
                     __syncwarp();
-                };
+                }
                 tc_after();
                 if (!active) {
-                    if (meta.masked) clean_v();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&t.p_full[x][0]), mbar_arrive(&t.p_full[x][1]);
                 } else {
@@ -559,28 +560,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tmem_st32(to + 32 * b, o);
                         }
                     }
-                    if (meta.masked) clean_v();
                     const float2 sc2 = make_float2(sc, sc), nr = make_float2(-ref, -ref);
                     // in two halves, so that the product with V starts on the first while the second is worked out
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        uint32_t p[kTile / 4];
 #pragma unroll
-                        for (int c = 0; c < kTile / 4; ++c) {
-                            const int e0 = half * (kTile / 2) + 2 * c;
-                            const float2 y = __ffma2_rn(make_float2(__uint_as_float(s[e0]), __uint_as_float(s[e0 + 1])), sc2, nr);
-                            const float2 e = make_float2(ex2(y.x), ex2(y.y));
-                            sum = __fadd2_rn(sum, e);
-                            p[c] = pack_bf16(e.x, e.y);
+                        for (int part = 0; part < 2; ++part) {
+                            uint32_t p[kTile / 8];
+#pragma unroll
+                            for (int c = 0; c < kTile / 8; ++c) {
+                                const int e0 = half * (kTile / 2) + part * (kTile / 4) + 2 * c;
+                                const float2 y = __ffma2_rn(make_float2(__uint_as_float(s[e0]), __uint_as_float(s[e0 + 1])), sc2, nr);
+                                const float2 e = make_float2(ex2(y.x), ex2(y.y));
+                                sum = __fadd2_rn(sum, e);
+                                p[c] = pack_bf16(e.x, e.y);
+                            }
+                            tmem_st16(ts + 32 * half + 16 * part, p);
                         }
-                        tmem_st32(ts + 32 * half, p);
                         tmem_wait_st();
                         tc_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&t.p_full[x][half]);
                     }
                 }
-                if (!ok) break;
                 ++steps, ++done;
             }
             __syncwarp();
@@ -589,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         base += 2 * n;
         // ---- output ----
-        if (steps && !(ok = wait_warp(&t.o_done[x], mine++ & 1, stop, a.err))) break;
+        if (steps && !(ok = wait_short(&t.o_done[x], mine++ & 1, stop, a.err))) break;
         tc_after();
         float l_sum = sum.x + sum.y;
         if (x == 1) {                                   // to the thread that has the row's other part, if that is so
@@ -609,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < D; ++c) all[c] = 0;
             }
             if (!w.two) {
-                if (!(ok = wait_warp(&t.merge[u & 1], (u >> 1) & 1, stop, a.err))) break;
+                if (!(ok = wait_short(&t.merge[u & 1], (u >> 1) & 1, stop, a.err))) break;
                 tc_after();
                 if (n > 1 && active) {
                     const float2 o = t.other[u & 1][r];
@@ -647,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // their row against bank conflicts
                 const float inv = l_sum == 0.f ? 0.f : 1.f / l_sum;
                 const int row_off = (tok0 + r_tok) * a.Hq + r_head;
-                uint8_t* const stage = smem + (2 + kStages) * C::kBytes + (warp - 4) * (32 * 64);
+                uint8_t* const stage = smem + (2 + kStages) * C::kBytes + (warp - 8) * (32 * 64);
 #pragma unroll
                 for (int b = 0; b < D / 32; ++b) {
                     const uint32_t* const o = all + 32 * b;
@@ -683,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int j = odd; j <= upto; ++j) {
                         const int slot = live_slot(a.map, raw_entry(a.map, map, j), j, err);
                         if (slot < 0) continue;
-                        const float e = __bfloat162float(a.v[(int64_t)slot * a.v_stride + (int64_t)g * D + d]);
+                        const float e = __bfloat162float(a.v[(uint64_t)(uint32_t)slot * (a.v_bytes / 2) + (int64_t)g * D + d]);
                         if (!(fabsf(e) < INFINITY)) add += e;
                     }
                     if (add == 0.f) continue;
@@ -742,8 +744,7 @@ __global__ void __launch_bounds__(256) pool_join_kernel(const PoolArgs a) {
 }
 
 template <int D>
-cudaError_t launch(kvsel_ctx* ctx, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const PoolArgs& a,
-                   cudaStream_t s) {
+cudaError_t launch(kvsel_ctx* ctx, const CUtensorMap& mq, const PoolArgs& a, cudaStream_t s) {
     auto* kernel = pool_attention_kernel<D>;
     constexpr unsigned kBit = D == 64 ? KVSEL_READY_POOL64 : KVSEL_READY_POOL128;
     if (!(ctx->ready & kBit)) {
@@ -755,7 +756,7 @@ cudaError_t launch(kvsel_ctx* ctx, const CUtensorMap& mq, const CUtensorMap& mk,
         if (e != cudaSuccess) return e;
         ctx->ready |= kBit;
     }
-    kernel<<<(unsigned)a.shares * a.Hkv, kThreads, Cfg<D>::kSmem, s>>>(mq, mk, mv, a);
+    kernel<<<(unsigned)a.shares * a.Hkv, kThreads, Cfg<D>::kSmem, s>>>(mq, a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || a.shares == 1) return e;
     cudaLaunchConfig_t cfg = {};
@@ -788,17 +789,15 @@ int attention_call(kvsel_ctx* ctx, const void* q, int64_t q_stride, const int32_
     if ((reinterpret_cast<uintptr_t>(q) & 15u) || (reinterpret_cast<uintptr_t>(out) & 15u))
         return kvsel_fail(ctx, KVSEL_ERR_ALIGN, "pool_attention: q and out must be 16-byte aligned");
     const int G = Hq / Hkv, tile_tokens = kTile / G;
-    CUtensorMap mq, mk, mv;
-    if (!make_query_map(&mq, q, T, Hq, D, q_stride, G, tile_tokens) ||
-        (P > 0 && (!make_pool_map(&mk, k_pool, P * page, Hkv, D, k_stride) ||
-                   !make_pool_map(&mv, v_pool, P * page, Hkv, D, v_stride))))
+    CUtensorMap mq;
+    if (!make_query_map(&mq, q, T, Hq, D, q_stride, G, tile_tokens))
         return kvsel_fail(ctx, KVSEL_ERR_CUDA, "pool_attention: tensor map encoding failed");
-    if (P == 0) mk = mv = mq;           // nothing is live
     float* const parts = (float*)ctx->pool_parts;
-    const PoolArgs a{cu_new, seq_lens, S, T, Hq, Hkv, G, tile_tokens, (const __nv_bfloat16*)v_pool, v_stride, map, scale * kLog2e,
+    const PoolArgs a{cu_new, seq_lens, S, T, Hq, Hkv, G, tile_tokens, (const __nv_bfloat16*)k_pool,
+                     (const __nv_bfloat16*)v_pool, (uint32_t)(k_stride * 2), (uint32_t)(v_stride * 2), map, scale * kLog2e,
                      (__nv_bfloat16*)out, lse, ctx->dev_err, Hkv < ctx->num_sms ? ctx->num_sms / Hkv : 1, parts,
                      (Joint*)(parts + (size_t)ctx->num_sms * 2 * kPart), wait_ns, stuck};
-    const cudaError_t e = D == 64 ? launch<64>(ctx, mq, mk, mv, a, (cudaStream_t)stream) : launch<128>(ctx, mq, mk, mv, a, (cudaStream_t)stream);
+    const cudaError_t e = D == 64 ? launch<64>(ctx, mq, a, (cudaStream_t)stream) : launch<128>(ctx, mq, a, (cudaStream_t)stream);
     return e == cudaSuccess ? KVSEL_OK : kvsel_cuda_fail(ctx, e, "pool_attention launch");
 }
 

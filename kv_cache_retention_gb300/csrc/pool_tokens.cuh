@@ -8,12 +8,14 @@
 
 namespace {
 
-// Slot maps (page == 0) or block tables, int32 [S][ld].
+// Slot maps (page == 1) or block tables, int32 [S][ld].
 struct TokenMap {
     const int32_t* map;
     int ld, reach;           // row length, and the positions that a row holds
-    int page, page_shift;    // page_shift: log2(page), or -1
-    int n_pages, n_slots;
+    int page;
+    uint32_t mul, shift;     // j / page = umulhi(j, mul) >> shift; mul 0: j
+    int limit;               // entries lie below it: pages or slots
+    unsigned bad;            // the error of one that does not
     int dead;
 };
 
@@ -22,24 +24,19 @@ struct Session {
     int first, count, len;
 };
 
-// What the map says of position j (below its reach): a slot, or the page that holds it.
-__device__ __forceinline__ int raw_entry(const TokenMap& m, const int32_t* row, int j) {
-    return __ldg(row + (m.page == 0 ? j : m.page_shift >= 0 ? j >> m.page_shift : j / m.page));
+__device__ __forceinline__ int entry_of(const TokenMap& m, int j) {
+    return m.mul ? (int)(__umulhi((uint32_t)j, m.mul) >> m.shift) : j;
 }
-// Slot of position j, from its entry; -1 where it is not live.
+// What the map says of position j (below its reach): a slot, or the page that holds it.
+__device__ __forceinline__ int raw_entry(const TokenMap& m, const int32_t* row, int j) { return __ldg(row + entry_of(m, j)); }
+// Slot of position j, from what the map says; -1 where it is not live.
 __device__ __forceinline__ int live_slot(const TokenMap& m, int entry, int j, unsigned& err) {
-    int slot = entry;
-    if (m.page != 0) {
-        if (entry >= m.n_pages) err |= KVSEL_DEV_BAD_PAGE;
-        if (entry < 0 || entry >= m.n_pages) return -1;
-        slot = entry * m.page + (m.page_shift >= 0 ? j & (m.page - 1) : j % m.page);
-    }
-    if (slot < 0 || slot == m.dead) return -1;
-    if (slot >= m.n_slots) {
-        err |= KVSEL_DEV_BAD_SLOT;
+    if ((unsigned)entry >= (unsigned)m.limit) {
+        if (entry >= 0 && (m.page != 1 || entry != m.dead)) err |= m.bad;
         return -1;
     }
-    return slot;
+    const int slot = entry * m.page + (j - entry_of(m, j) * m.page);
+    return slot == m.dead ? -1 : slot;
 }
 
 // Session s.  Sequences that start below 0 or end before they start have no rows; they end at T, lengths at the reach.
@@ -81,13 +78,20 @@ inline int check_pool_call(kvsel_ctx* ctx, const char* who, int S, int T, int Hq
         if (P > 0 && !pools[i]) return kvsel_fail(ctx, KVSEL_ERR_INVALID_ARG, "%s: null pointer", who);
         if ((int64_t)P * page > 1 && strides[i] < (int64_t)Hkv * D)
             return kvsel_fail(ctx, KVSEL_ERR_SHAPE, "%s: slot stride < Hkv*D", who);
+        if (strides[i] > INT_MAX / 2) return kvsel_fail(ctx, KVSEL_ERR_UNSUPPORTED, "%s: slot stride too large", who);
         if ((reinterpret_cast<uintptr_t>(pools[i]) & 15u) || (strides[i] * 2) % 16)
             return kvsel_fail(ctx, KVSEL_ERR_ALIGN, "%s: pools and their strides must be 16-byte aligned", who);
     }
-    int shift = -1;
-    if ((page & (page - 1)) == 0)
-        for (shift = 0; (1 << shift) < page;) ++shift;
-    *map = TokenMap{slot_map ? slot_map : block_table, ld, (int)reach, slot_map ? 0 : page, shift, P, P * page, dead_slot};
+    *map = TokenMap{slot_map ? slot_map : block_table, ld, (int)reach, 1, 0, 0, P * page, KVSEL_DEV_BAD_SLOT, dead_slot};
+    if (!slot_map) {
+        map->page = page, map->limit = P, map->bad = KVSEL_DEV_BAD_PAGE;
+        if (page > 1) {  // with 2^(l-1) < page <= 2^l, (2^(31+l) / page + 1) j >> (31+l) is the quotient for every j < 2^31
+            int l = 1;
+            while (((int64_t)1 << l) < page) ++l;
+            map->mul = (uint32_t)(((uint64_t)1 << (31 + l)) / (uint64_t)page + 1);
+            map->shift = l - 1;
+        }
+    }
     return KVSEL_OK;
 }
 
