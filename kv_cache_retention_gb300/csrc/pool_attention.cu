@@ -8,7 +8,7 @@
 // one session and kv head.
 //
 // Keys go through lists of 128 live tokens that one warp makes from the map (dropped tokens cost an entry's read and no
-// more); their rows come by cp.async.  Per list and tile
+// more); their rows come by TMA where slots are consecutive, else by cp.async.  Per list and tile
 //   S = Q K^T   tcgen05.mma, both operands from shared memory, 128 fp32 columns
 //   P = 2^(S sc - ref) in bf16, written over S in TMEM
 //   O += P V    tcgen05.mma, P from TMEM, V from shared memory as it lies
@@ -259,7 +259,8 @@ __device__ __forceinline__ int64_t warp_sum(int64_t v) {
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    pool_attention_kernel(const __grid_constant__ CUtensorMap map_q, const PoolArgs a) {
+    pool_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                          const __grid_constant__ CUtensorMap map_v, const PoolArgs a) {
     using C = Cfg<D>;
     constexpr int kStages = C::kStages;
     extern __shared__ uint8_t smem_raw[];
@@ -310,10 +311,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ---- loads ----
             uint32_t c = 0, l = 0, loaded_q = 0;  // ring places filled, lists, Q loads
             bool ok = true;
-            auto load = [&](const __nv_bfloat16* pool, uint32_t bytes, uint32_t list) {
+            auto load = [&](const CUtensorMap* map, const __nv_bfloat16* pool, uint32_t bytes, uint32_t list) {
                 const uint32_t st = c % kStages;
                 if (!(ok = wait_short(&t.empty[st], (c / kStages & 1) ^ 1u, stop, a.err))) return;
-                load_rows<D, 4>(pool + g * D, bytes, t.lists.slot + list % kLists * kTile, ring + st * C::kBytes, &t.full[st], warp - 4, lane);
+                load_rows<D>(map, pool, bytes, g * D, t.lists.slot + list % kLists * kTile, t.lists.meta[list % kLists].runs,
+                             ring + st * C::kBytes, &t.full[st], warp - 4, lane);
                 ++c;
             };
             auto release = [&](uint32_t list) {
@@ -349,13 +351,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
 #pragma unroll 1
                     for (int v = i < n ? 0 : 1; ok && v < (i > 0 ? 2 : 1); ++v) {
-                        load(v ? a.v : a.k, v ? a.v_bytes : a.k_bytes, l + i - v);
+                        load(v ? &map_v : &map_k, v ? a.v : a.k, v ? a.v_bytes : a.k_bytes, l + i - v);
                         if (v) release(l + i - 1);
                     }
                 }
                 l += max(n, 1);
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
+            for (uint32_t at = c > kStages ? c - kStages : 0; at < c; ++at) drain_phase(&t.full[at % kStages], at / kStages & 1);
             if (warp == 4 && loaded_q) drain_phase(&t.q_full, (loaded_q - 1) & 1);
         } else if (warp == 1 || warp == 2) {
             issue_tiles<D>(t, sq, ring, warp - 1, lane, a.stuck && warp == 1, stop, a.err);
@@ -744,7 +747,8 @@ __global__ void __launch_bounds__(256) pool_join_kernel(const PoolArgs a) {
 }
 
 template <int D>
-cudaError_t launch(kvsel_ctx* ctx, const CUtensorMap& mq, const PoolArgs& a, cudaStream_t s) {
+cudaError_t launch(kvsel_ctx* ctx, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const PoolArgs& a,
+                   cudaStream_t s) {
     auto* kernel = pool_attention_kernel<D>;
     constexpr unsigned kBit = D == 64 ? KVSEL_READY_POOL64 : KVSEL_READY_POOL128;
     if (!(ctx->ready & kBit)) {
@@ -756,7 +760,7 @@ cudaError_t launch(kvsel_ctx* ctx, const CUtensorMap& mq, const PoolArgs& a, cud
         if (e != cudaSuccess) return e;
         ctx->ready |= kBit;
     }
-    kernel<<<(unsigned)a.shares * a.Hkv, kThreads, Cfg<D>::kSmem, s>>>(mq, a);
+    kernel<<<(unsigned)a.shares * a.Hkv, kThreads, Cfg<D>::kSmem, s>>>(mq, mk, mv, a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || a.shares == 1) return e;
     cudaLaunchConfig_t cfg = {};
@@ -789,15 +793,19 @@ int attention_call(kvsel_ctx* ctx, const void* q, int64_t q_stride, const int32_
     if ((reinterpret_cast<uintptr_t>(q) & 15u) || (reinterpret_cast<uintptr_t>(out) & 15u))
         return kvsel_fail(ctx, KVSEL_ERR_ALIGN, "pool_attention: q and out must be 16-byte aligned");
     const int G = Hq / Hkv, tile_tokens = kTile / G;
-    CUtensorMap mq;
-    if (!make_query_map(&mq, q, T, Hq, D, q_stride, G, tile_tokens))
+    CUtensorMap mq, mk, mv;
+    if (!make_query_map(&mq, q, T, Hq, D, q_stride, G, tile_tokens) ||
+        (P > 0 && (!make_pool_map(&mk, k_pool, P * page, Hkv, D, k_stride) ||
+                   !make_pool_map(&mv, v_pool, P * page, Hkv, D, v_stride))))
         return kvsel_fail(ctx, KVSEL_ERR_CUDA, "pool_attention: tensor map encoding failed");
+    if (P == 0) mk = mv = mq;           // nothing is live
     float* const parts = (float*)ctx->pool_parts;
     const PoolArgs a{cu_new, seq_lens, S, T, Hq, Hkv, G, tile_tokens, (const __nv_bfloat16*)k_pool,
                      (const __nv_bfloat16*)v_pool, (uint32_t)(k_stride * 2), (uint32_t)(v_stride * 2), map, scale * kLog2e,
                      (__nv_bfloat16*)out, lse, ctx->dev_err, Hkv < ctx->num_sms ? ctx->num_sms / Hkv : 1, parts,
                      (Joint*)(parts + (size_t)ctx->num_sms * 2 * kPart), wait_ns, stuck};
-    const cudaError_t e = D == 64 ? launch<64>(ctx, mq, a, (cudaStream_t)stream) : launch<128>(ctx, mq, a, (cudaStream_t)stream);
+    const cudaError_t e = D == 64 ? launch<64>(ctx, mq, mk, mv, a, (cudaStream_t)stream)
+                                   : launch<128>(ctx, mq, mk, mv, a, (cudaStream_t)stream);
     return e == cudaSuccess ? KVSEL_OK : kvsel_cuda_fail(ctx, e, "pool_attention launch");
 }
 

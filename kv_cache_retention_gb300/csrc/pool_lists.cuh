@@ -28,11 +28,13 @@ __device__ __forceinline__ bool wait_short(uint64_t* b, uint32_t parity, Stop* s
     }
     return __all_sync(0xffffffffu, ok);
 }
+constexpr int kRun = 16;            // slots that one TMA load brings where they are consecutive
 
 struct ListMeta {
     int n;          // tokens; 0 only where a piece has none
     int masked;     // not all of them are seen by every row, or there are fewer than 128
     int last;       // of its piece
+    unsigned runs;  // of each four tokens, whether they go on a run of slots that starts with their kRun; a bit each
 };
 
 // A ring of N lists.  slot, pos: the tokens in ascending positions; behind the n-th the slot of the first.
@@ -41,60 +43,85 @@ struct Lists {
     static constexpr int kAhead = 8;
     int slot[N * kTile], pos[N * kTile];
     int entry[32 * kAhead];             // the making warp's own
+    static_assert(kAhead % 4 == 0, "whole rounds");
     ListMeta meta[N];
     uint64_t full[N], empty[N];
 };
 
 // Makes the lists of positions [p0, p1) of a session, at least one; pos0: where the first row that will look at them sits.
 // A list is handed out when it is known whether another follows.  made: lists of the block so far.  The whole warp calls.
-// The loop takes 32 positions a round and is not unrolled (with 8 rounds unrolled the code passed the instruction cache, and a
-// round took 800 cycles); entries are read kAhead rounds at a time, while the ones before are gone through, and wait for
-// their round in shared memory (a queue of registers would wait for its loads whenever it moves).
+// A round takes 128 positions, four of each lane (with one of each lane and 32 a round, the chain of dependent instructions
+// took 640 cycles for those), and is not unrolled, for the instruction cache's sake.  Entries are read kAhead at a time and
+// lane, while the ones before are gone through, and wait for their round in shared memory (a queue of registers would wait
+// for its loads whenever it moves).
 template <int N>
 __device__ __forceinline__ bool make_lists(Lists<N>& t, const TokenMap& m, const int32_t* row, int p0, int p1, int pos0, uint32_t& made,
                                            int lane, Stop* stop, unsigned* err_word, unsigned& err) {
     constexpr int kAhead = Lists<N>::kAhead;
     const unsigned below = (1u << lane) - 1;
     uint32_t l = made;                  // the list that tokens go to, and how many it has
-    int n = 0, j = p0 + lane;
+    int n = 0;
     bool ok = l < N || wait_short(&t.empty[l % N], (l / N - 1) & 1, stop, err_word);
     int next[kAhead];
     auto read = [&](int p) {
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) next[k] = p + 32 * k < p1 ? raw_entry(m, row, p + 32 * k) : -1;
     };
-    read(j);
+    read(p0 + lane);
     // hands out list l of n tokens
     auto hand_out = [&](int last) {
         __syncwarp();
+        const int4 s = *reinterpret_cast<const int4*>(&t.slot[l % N * kTile + 4 * lane]);
+        const int first = t.slot[l % N * kTile + (lane & ~(kRun / 4 - 1)) * 4], off = 4 * (lane % (kRun / 4));
+        const bool run = s.x == first + off && s.y == s.x + 1 && s.z == s.x + 2 && s.w == s.x + 3;
+        const unsigned runs = __ballot_sync(0xffffffffu, run);
         if (lane == 0) {
-            t.meta[l % N] = ListMeta{n, n < kTile || t.pos[l % N * kTile + n - 1] > pos0, last};
+            t.meta[l % N] = ListMeta{n, n < kTile || t.pos[l % N * kTile + n - 1] > pos0, last, runs};
             mbar_arrive(&t.full[l % N]);
         }
         ++l;
     };
-    int round = kAhead;
 #pragma unroll 1
-    for (; ok && j - lane < p1; j += 32, ++round) {
-        if (round == kAhead) {
+    for (int p = p0, round = kAhead / 4; ok && p < p1; p += kTile, ++round) {
+        if (round == kAhead / 4) {
+            __syncwarp();
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) t.entry[32 * k + lane] = next[k];
-            if (p1 - (j - lane) > 32 * kAhead) read(j + 32 * kAhead);
+            __syncwarp();
+            if (p1 - p > 32 * kAhead) read(p + 32 * kAhead + lane);
             round = 0;
         }
-        const int slot = live_slot(m, t.entry[32 * round + lane], j, err);
-        const unsigned live = __ballot_sync(0xffffffffu, slot >= 0);
-        if (!live) continue;
-        int at = n + __popc(live & below);
-        if (slot >= 0 && at < kTile) t.slot[l % N * kTile + at] = slot, t.pos[l % N * kTile + at] = j;
-        n += __popc(live);
+        const int4 entry = *reinterpret_cast<const int4*>(&t.entry[kTile * round + 4 * lane]);
+        const int j = p + 4 * lane;
+        int slot[4], at[4];
+        slot[0] = live_slot(m, entry.x, j, err);
+        slot[1] = live_slot(m, entry.y, j + 1, err);
+        slot[2] = live_slot(m, entry.z, j + 2, err);
+        slot[3] = live_slot(m, entry.w, j + 3, err);
+        int before = n, more = 0, mine = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const unsigned live = __ballot_sync(0xffffffffu, slot[k] >= 0);
+            before += __popc(live & below);
+            more += __popc(live);
+            at[k] = mine;
+            mine += slot[k] >= 0;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            at[k] += before;
+            if (slot[k] >= 0 && at[k] < kTile) t.slot[l % N * kTile + at[k]] = slot[k], t.pos[l % N * kTile + at[k]] = j + k;
+        }
+        n += more;
         if (n > kTile) {                // the list is full, and others follow
             const int rest = n - kTile;
             n = kTile;
             hand_out(0);
-            ok = l < N || wait_short(&t.empty[l % N], (l / N - 1) & 1, stop, err_word);
-            at -= kTile;
-            if (ok && slot >= 0 && at >= 0) t.slot[l % N * kTile + at] = slot, t.pos[l % N * kTile + at] = j;
+            if (l >= N) ok = wait_short(&t.empty[l % N], (l / N - 1) & 1, stop, err_word);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (ok && slot[k] >= 0 && at[k] >= kTile)
+                    t.slot[l % N * kTile + at[k] - kTile] = slot[k], t.pos[l % N * kTile + at[k] - kTile] = j + k;
             n = rest;
         }
     }
@@ -102,6 +129,7 @@ __device__ __forceinline__ bool make_lists(Lists<N>& t, const TokenMap& m, const
     __syncwarp();
     if (n > 0) {
         const int spare = t.slot[l % N * kTile];
+        __syncwarp();
         for (int e = n + lane; e < kTile; e += 32) t.slot[l % N * kTile + e] = spare;
     }
     hand_out(1);
@@ -109,6 +137,18 @@ __device__ __forceinline__ bool make_lists(Lists<N>& t, const TokenMap& m, const
     return true;
 }
 
+// Rows of a pool as TMA sees them: 64 dims of kRun consecutive slots.
+inline bool make_pool_map(CUtensorMap* map, const void* base, int n_slots, int Hkv, int D, int64_t stride) {
+    auto fn = kvsel_tmap_encoder();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)Hkv * D, (cuuint64_t)n_slots};
+    cuuint64_t strides[1] = {(cuuint64_t)(n_slots > 1 ? stride : (int64_t)Hkv * D) * 2};
+    cuuint32_t box[2] = {64, kRun};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 // Query rows [T][Hq][D]: 64 dims of `heads` heads of `tokens` tokens a load, zeros behind the last token.
 inline bool make_query_map(CUtensorMap* map, const void* base, int T, int Hq, int D, int64_t stride, int heads, int tokens) {
     auto fn = kvsel_tmap_encoder();
@@ -121,29 +161,47 @@ inline bool make_query_map(CUtensorMap* map, const void* base, int T, int Hq, in
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-// The rows of a list's 128 slots, D dims from `base` on, to a tile of blocks of 64 dims in the layout of the 128-byte swizzle;
-// by W warps, warp w of them a share, whose lanes signal `full` (a count of 32 W) when the rows have landed.  cp.async and not TMA gathers of four
-// slots: those took 45 ns each from one thread, 6 us for a list's K and V.  The rows are written through the generic proxy:
-// who has seen `full` fences before MMAs on them.
-template <int D, int W>
-__device__ __forceinline__ void load_rows(const __nv_bfloat16* base, uint32_t stride_bytes, const int* slots, const uint8_t* tile,
-                                          uint64_t* full, int w, int lane) {
+// The rows of a list's 128 slots, D dims from dim x of a slot on, to a tile of blocks of 64 dims in the layout of the 128-byte
+// swizzle; by four warps, warp w of them 32 rows, whose lanes signal `full` (a count of 128) when the rows have landed.  Runs
+// of kRun slots come by TMA, others row by row through cp.async (TMA gathers of four slots took 45 ns each from one thread, 6
+// us for a list's K and V).  Such rows are written through the generic proxy: who has seen `full` fences before MMAs on them.
+template <int D>
+__device__ __forceinline__ void load_rows(const CUtensorMap* map, const __nv_bfloat16* pool, uint32_t stride_bytes, int x, const int* slots,
+                                          unsigned runs, const uint8_t* tile, uint64_t* full, int w, int lane) {
     constexpr int kChunks = D / 8, kRows = 32 / kChunks;  // 16-byte chunks of a row; rows of one instruction
+    constexpr int kShare = 32;
     const int chunk = lane % kChunks, low = lane / kChunks;
-    constexpr int kShare = kTile / W;
-    const char* const from = reinterpret_cast<const char*>(base) + chunk * 16;
+    const char* const from = reinterpret_cast<const char*>(pool + x) + chunk * 16;
     const uint32_t to = saddr(tile) + (chunk >> 3) * (kTile * 128) + (kShare * w + low) * 128;
     const uint32_t swizzled = ((chunk & 7) ^ low) << 4;    // of row `low`; of row i + low, i a multiple of kRows: ^ (i & 7) << 4
-    int slot[kShare / 32];
+    const int slot = slots[kShare * w + lane];
+    constexpr unsigned kAll = (1u << kRun / 4) - 1;
+#pragma unroll 1
+    for (int r = 0; r < kShare; r += kRun) {
+        if ((runs >> ((kShare * w + r) / 4) & kAll) == kAll) {
+            const int first = __shfl_sync(0xffffffffu, slot, r);
+            if (lane == 0) {
+                const uint32_t dst = saddr(tile) + (kShare * w + r) * 128;
+                asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(saddr(full)), "r"(kRun * D * 2) : "memory");
 #pragma unroll
-    for (int j = 0; j < kShare / 32; ++j) slot[j] = slots[kShare * w + 32 * j + lane];
+                for (int b = 0; b < D / 64; ++b)
+                    asm volatile(
+                        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
+                        "[%2];" ::"r"(dst + b * (kTile * 128)),
+                        "l"(reinterpret_cast<uint64_t>(map)), "r"(saddr(full)), "r"(x + 64 * b), "r"(first)
+                        : "memory");
+            }
+        } else {
 #pragma unroll
-    for (int i = 0; i < kShare; i += kRows) {
-        const uint32_t s = __shfl_sync(0xffffffffu, slot[i / 32], i % 32 + low);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * 128 + (swizzled ^ ((i & 7) << 4))),
-                     "l"(from + (uint64_t)s * stride_bytes)
-                     : "memory");
+            for (int i = 0; i < kRun; i += kRows) {
+                const uint32_t s = __shfl_sync(0xffffffffu, slot, r + i + low);
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + (r + i) * 128 + (swizzled ^ ((i & 7) << 4))),
+                             "l"(from + (uint64_t)s * stride_bytes)
+                             : "memory");
+            }
+        }
     }
+    __syncwarp();
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(saddr(full)) : "memory");
 }
 // Rows that load_rows has written, and zeros written into them, come before the MMAs that follow.

@@ -13,7 +13,7 @@ struct TokenMap {
     const int32_t* map;
     int ld, reach;           // row length, and the positions that a row holds
     int page;
-    uint32_t mul, shift;     // j / page = umulhi(j, mul) >> shift; mul 0: j
+    uint32_t mul, shift;     // j / page = j mul >> shift
     int limit;               // entries lie below it: pages or slots
     unsigned bad;            // the error of one that does not
     int dead;
@@ -25,7 +25,7 @@ struct Session {
 };
 
 __device__ __forceinline__ int entry_of(const TokenMap& m, int j) {
-    return m.mul ? (int)(__umulhi((uint32_t)j, m.mul) >> m.shift) : j;
+    return (int)(((uint64_t)(uint32_t)j * m.mul) >> m.shift);
 }
 // What the map says of position j (below its reach): a slot, or the page that holds it.
 __device__ __forceinline__ int raw_entry(const TokenMap& m, const int32_t* row, int j) { return __ldg(row + entry_of(m, j)); }
@@ -82,14 +82,14 @@ inline int check_pool_call(kvsel_ctx* ctx, const char* who, int S, int T, int Hq
         if ((reinterpret_cast<uintptr_t>(pools[i]) & 15u) || (strides[i] * 2) % 16)
             return kvsel_fail(ctx, KVSEL_ERR_ALIGN, "%s: pools and their strides must be 16-byte aligned", who);
     }
-    *map = TokenMap{slot_map ? slot_map : block_table, ld, (int)reach, 1, 0, 0, P * page, KVSEL_DEV_BAD_SLOT, dead_slot};
+    *map = TokenMap{slot_map ? slot_map : block_table, ld, (int)reach, 1, 1, 0, P * page, KVSEL_DEV_BAD_SLOT, dead_slot};
     if (!slot_map) {
         map->page = page, map->limit = P, map->bad = KVSEL_DEV_BAD_PAGE;
         if (page > 1) {  // with 2^(l-1) < page <= 2^l, (2^(31+l) / page + 1) j >> (31+l) is the quotient for every j < 2^31
             int l = 1;
             while (((int64_t)1 << l) < page) ++l;
             map->mul = (uint32_t)(((uint64_t)1 << (31 + l)) / (uint64_t)page + 1);
-            map->shift = l - 1;
+            map->shift = 31 + l;
         }
     }
     return KVSEL_OK;
