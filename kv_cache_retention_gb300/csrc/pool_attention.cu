@@ -185,31 +185,33 @@ __device__ __forceinline__ void issue_tiles(typename Cfg<D>::Tail& t, const uint
                     released = true;
                 }
                 const uint32_t av = base + at_v(i, ended && i == n - 1), ak = base + at_k(i + by);
+                const uint32_t vd = uniform(desc_low(saddr(ring) + av % kStages * C::kBytes, C::kBlock));
+                const uint32_t kd = uniform(desc_low(saddr(ring) + ak % kStages * C::kBytes, 16));
+                const uint32_t step = (x ? steps1 : steps0) & 1;
+                // all that can be waited for ahead of the turn; one answer for the lanes at the end of the round
+                if (more) ok = wait_lane(&t.full[ak % kStages], ak / kStages & 1, stop, err) && ok;
                 if (product) {
-                    ok = ok && wait_short(&t.full[av % kStages], av / kStages & 1, stop, err);
-                    if (u && i < by) ok = ok && wait_short(&t.o_free[x][(u - 1) & 1], ((u - 1) >> 1) & 1, stop, err);
-                    if (two && (X == 1 || i > 0)) ok = ok && wait_short(&t.turn[X], turns++ & 1, stop, err);
-                    const uint32_t step = x ? steps1 : steps0;
-                    const uint32_t vd = uniform(desc_low(saddr(ring) + av % kStages * C::kBytes, C::kBlock));
-#pragma unroll 1
-                    for (int half = 0; half < 2; ++half) {
-                        ok = ok && wait_short(&t.p_full[x][half], step & 1, stop, err);
-                        if (!ok) break;
-                        fence_async();
-                        tc_after();
-                        const uint32_t th = uniform(ts + half * (kTile / 4)), vh = uniform(vd + half * (kTile / 32) * (2048 >> 4));
+                    ok = wait_lane(&t.full[av % kStages], av / kStages & 1, stop, err) && ok;
+                    if (u && i < by) ok = wait_lane(&t.o_free[x][(u - 1) & 1], ((u - 1) >> 1) & 1, stop, err) && ok;
+                    fence_async();
+                    if (two && (X == 1 || i > 0)) ok = wait_lane(&t.turn[X], turns++ & 1, stop, err) && ok;
+                    const uint32_t fresh = i < by;
+                    ok = wait_lane(&t.p_full[x][0], step, stop, err) && ok;
+                    tc_after();
 #pragma unroll
-                        for (int k = 0; k < kTile / 32; ++k)
-                            mma_ts(to, th + k * 8, vh + k * (2048 >> 4), idesc(D, true), i >= by || half || k > 0, lead);
-                    }
+                    for (int k = 0; k < kTile / 32; ++k)
+                        mma_ts(to, ts + k * 8, vd + k * (2048 >> 4), idesc(D, true), k > 0 || !fresh, lead);
+                    ok = wait_lane(&t.p_full[x][1], step, stop, err) && ok;
+                    tc_after();
+#pragma unroll
+                    for (int k = kTile / 32; k < kTile / 16; ++k)
+                        mma_ts(to, ts + k * 8, vd + k * (2048 >> 4), idesc(D, true), 1, lead);
                     if (x) ++steps1; else ++steps0;
-                }
-                if (!ok) break;
-                if (more) {                       // writes over the P read above: one thread's MMAs run in the order of issue
-                    if (!(ok = wait_short(&t.full[ak % kStages], ak / kStages & 1, stop, err))) break;
+                } else {
                     fence_async();
                     tc_after();
-                    const uint32_t kd = uniform(desc_low(saddr(ring) + ak % kStages * C::kBytes, 16));
+                }
+                if (more) {                       // writes over the P read above: one thread's MMAs run in the order of issue
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
                         const uint32_t off = ((k >> 2) * C::kBlock + (k & 3) * 32) >> 4;
@@ -224,6 +226,7 @@ __device__ __forceinline__ void issue_tiles(typename Cfg<D>::Tail& t, const uint
                     mma_commit(saddr(&t.o_done[x]), lead);
                 }
                 if (product) mma_commit(saddr(&t.empty[av % kStages]), lead);
+                ok = __all_sync(0xffffffffu, ok);
                 if (done) break;
             }
             if (two && X == 0) steps1 += n;

@@ -7,27 +7,30 @@
 
 namespace {
 
-// A bounded wait in few instructions, with one answer for the warp's lanes: the kernels of these lists have some twenty, and
+// Bounded waits in few instructions, of a lane and with one answer for the warp's lanes: the kernels of these lists have some twenty, and
 // all their roles' code has to fit the instruction cache (with wait_warp in their places, 1.45 ms and not 1.15 ms for 2048
 // tokens behind 32768).
-__device__ __forceinline__ bool wait_short(uint64_t* b, uint32_t parity, Stop* stop, unsigned* err) {
+__device__ __forceinline__ bool wait_lane(uint64_t* b, uint32_t parity, Stop* stop, unsigned* err) {
     uint32_t t0 = 0;
-    bool ok;
 #pragma unroll 1
-    while (!(ok = mbar_try(b, parity))) {
+    while (!mbar_try(b, parity)) {
         uint32_t now;
         asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(now));
         now |= 1;
         if (!t0) t0 = now;
-        if (stop->given_up) break;
+        if (stop->given_up) return false;
         if (now - t0 > (uint32_t)stop->limit_ns) {
             stop->given_up = 1;
             atomicOr(err, (unsigned)KVSEL_DEV_TIMEOUT);
-            break;
+            return false;
         }
     }
-    return __all_sync(0xffffffffu, ok);
+    return true;
 }
+__device__ __forceinline__ bool wait_short(uint64_t* b, uint32_t parity, Stop* stop, unsigned* err) {
+    return __all_sync(0xffffffffu, wait_lane(b, parity, stop, err));
+}
+
 constexpr int kRun = 16;            // slots that one TMA load brings where they are consecutive
 
 struct ListMeta {
