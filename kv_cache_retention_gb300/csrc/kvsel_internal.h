@@ -61,6 +61,8 @@ enum kvsel_ready : unsigned {
     KVSEL_READY_EVICT = 1u << 20,
     KVSEL_READY_POOL64 = 1u << 21,
     KVSEL_READY_POOL128 = 1u << 22,
+    KVSEL_READY_MASS64 = 1u << 23,
+    KVSEL_READY_MASS128 = 1u << 24,
 };
 
 // Device error-word bits.

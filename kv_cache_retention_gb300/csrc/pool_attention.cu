@@ -252,11 +252,6 @@ __device__ __forceinline__ Cut cut_of(const Session& x, int unit) {
     return Cut{(int64_t)max(0, x.len - x.count) + kStart * kTile, unit};
 }
 __device__ __forceinline__ int units_of(const Session& x, int unit) { return (int)(((int64_t)x.count + unit - 1) / unit); }
-__device__ __forceinline__ int64_t warp_sum(int64_t v) {
-#pragma unroll
-    for (int k = 16; k; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
-    return v;
-}
 
 // ---- the kernel ------------------------------------------------------------
 

@@ -2,6 +2,8 @@
 // their rows.
 #pragma once
 
+#include <limits.h>
+
 #include "pool_tokens.cuh"
 #include "tc_common.cuh"
 
@@ -31,12 +33,19 @@ __device__ __forceinline__ bool wait_short(uint64_t* b, uint32_t parity, Stop* s
     return __all_sync(0xffffffffu, wait_lane(b, parity, stop, err));
 }
 
+__device__ __forceinline__ int64_t warp_sum(int64_t v) {
+#pragma unroll
+    for (int k = 16; k; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
+    return v;
+}
+
 constexpr int kRun = 16;            // slots that one TMA load brings where they are consecutive
 
 struct ListMeta {
     int n;          // tokens; 0 only where a piece has none
     int masked;     // not all of them are seen by every row, or there are fewer than 128
     int last;       // of its piece
+    int first;      // position of its first token
     unsigned runs;  // of each four tokens, whether they go on a run of slots that starts with their kRun; a bit each
 };
 
@@ -79,7 +88,7 @@ __device__ __forceinline__ bool make_lists(Lists<N>& t, const TokenMap& m, const
         const bool run = s.x == first + off && s.y == s.x + 1 && s.z == s.x + 2 && s.w == s.x + 3;
         const unsigned runs = __ballot_sync(0xffffffffu, run);
         if (lane == 0) {
-            t.meta[l % N] = ListMeta{n, n < kTile || t.pos[l % N * kTile + n - 1] > pos0, last, runs};
+            t.meta[l % N] = ListMeta{n, n < kTile || t.pos[l % N * kTile + n - 1] > pos0, last, t.pos[l % N * kTile], runs};
             mbar_arrive(&t.full[l % N]);
         }
         ++l;
