@@ -89,7 +89,7 @@ __device__ __forceinline__ bool next_item(Tail& t, uint32_t l, Item& it, Stop* s
     return true;
 }
 
-template <int D>
+template <int D, bool MAP>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_mass_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_small,
                           const __grid_constant__ CUtensorMap map_k, const MassArgs a) {
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 at += n * w;
                 if (c0 >= c1) continue;
                 publish(typename C::Piece{x.first, x.count, x.len - x.count, s0 + i, 0});
-                ok = ok && make_lists(t.lists, a.map, a.map.map + (int64_t)(s0 + i) * a.map.ld, (int)c0 * kTile,
+                ok = ok && make_lists<MAP>(t.lists, a.map, a.map.map + (int64_t)(s0 + i) * a.map.ld, (int)c0 * kTile,
                                       (int)min((int64_t)x.len, c1 * kTile), INT_MIN, l, lane, stop, a.err, err);
             }
         }
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int x = 0; ok && x < it.nl; ++x, ++c) {
                         const uint32_t st = c % C::kK, at = (l + x) % kLists;
                         if (!(ok = wait_short(&t.k_empty[st], (c / C::kK & 1) ^ 1, stop, a.err))) break;
-                        load_rows<D>(&map_k, a.k, a.k_bytes, g * D, t.lists.slot + at * kTile, t.lists.meta[at].runs,
+                        load_rows<D>(&map_k, a.k, a.k_bytes, g * D, t.lists.token + at * kTile, t.lists.meta[at].runs,
                                      sk + st * C::kBytes, &t.k_full[st], warp - 4, lane);
                     }
                 for (int x = 0; ok && x < it.nl; ++x) release(l + x);
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             do {
                 if (!next_item(t, l, it, stop, a.err, ok)) break;
                 const int t0 = first_tile(w, it), n = x == 0 ? it.n0 : it.n1;
-                const int pos = t.lists.pos[(l + (x < it.nl ? x : 0)) % kLists * kTile + r];
+                const int pos = t.lists.token[(l + (x < it.nl ? x : 0)) % kLists * kTile + r].y;
                 const int behind = r < n ? pos - w.pos0 : 0;  // the first token that sees the key
                 float2 sum = make_float2(0.f, 0.f);
 #pragma unroll 1
@@ -422,6 +422,7 @@ __global__ void __launch_bounds__(256) mass_copy_kernel(const float* before, flo
 }
 
 // score_out = score_in + the parts of the blocks that shared the kv heads, in their order, where a token is live.
+template <bool MAP>
 __global__ void __launch_bounds__(256) mass_add_kernel(const MassArgs a, const float* before, float* score, int64_t ld) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int s = blockIdx.y;
@@ -430,17 +431,17 @@ __global__ void __launch_bounds__(256) mass_add_kernel(const MassArgs a, const f
     const int32_t* const row = a.map.map + (int64_t)s * a.map.ld;
     for (int j = blockIdx.x * 256 + threadIdx.x; j < a.map.reach; j += gridDim.x * 256) {
         float sum = 0.f;
-        if (x.count > 0 && j < x.len && live_slot(a.map, raw_entry(a.map, row, j), j, err) >= 0)
+        if (x.count > 0 && j < x.len && live_slot<MAP>(a.map, raw_entry(a.map, row, j), j, err) >= 0)
             for (int k = 0; k < a.split; ++k) sum += a.score[k * a.part + s * a.score_ld + j];
         score[s * ld + j] = (before ? before[s * ld + j] : 0.f) + sum;
     }
 }
 
-template <int D>
+template <int D, bool MAP>
 cudaError_t launch(kvsel_ctx* ctx, const CUtensorMap& mq, const CUtensorMap& ms, const CUtensorMap& mk, const MassArgs& a,
                    const float* before, float* score, int64_t score_ld, cudaStream_t s) {
-    auto* kernel = attention_mass_kernel<D>;
-    constexpr unsigned kBit = D == 64 ? KVSEL_READY_MASS64 : KVSEL_READY_MASS128;
+    auto* kernel = attention_mass_kernel<D, MAP>;
+    constexpr unsigned kBit = KVSEL_READY_MASS << (D / 64 - 1 + 2 * MAP);
     if (!(ctx->ready & kBit)) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)MassCfg<D>::kSmem);
         if (e != cudaSuccess) return e;
@@ -469,7 +470,7 @@ cudaError_t launch(kvsel_ctx* ctx, const CUtensorMap& mq, const CUtensorMap& ms,
     cfg.dynamicSmemBytes = 0;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, mass_add_kernel, a, before, score, score_ld);
+    return cudaLaunchKernelEx(&cfg, mass_add_kernel<MAP>, a, before, score, score_ld);
 }
 
 int mass_call(kvsel_ctx* ctx, const void* q, int64_t q_stride, const float* lse, const int32_t* cu_new, int S, int T, int Hq, int Hkv,
@@ -512,8 +513,8 @@ int mass_call(kvsel_ctx* ctx, const void* q, int64_t q_stride, const float* lse,
         mass_copy_kernel<<<dim3((unsigned)min((map.reach + 1023) / 1024, 1024), S), 256, 0, s>>>(score_in, score_out, score_ld, map.reach);
         e = cudaGetLastError();
     } else {
-        e = D == 64 ? launch<64>(ctx, mq, ms, mk, a, score_in, score_out, score_ld, s)
-                    : launch<128>(ctx, mq, ms, mk, a, score_in, score_out, score_ld, s);
+        auto run = [&](auto call) { return call(ctx, mq, ms, mk, a, score_in, score_out, score_ld, s); };
+        e = slot_map ? D == 64 ? run(launch<64, true>) : run(launch<128, true>) : D == 64 ? run(launch<64, false>) : run(launch<128, false>);
     }
     return e == cudaSuccess ? KVSEL_OK : kvsel_cuda_fail(ctx, e, "attention_mass launch");
 }

@@ -59,10 +59,8 @@ struct kvsel_ctx {
 // Bits of kvsel_ctx::ready of the calls over the page pools (the ones below 20 are prompt_attention's and kv4_attention's).
 enum kvsel_ready : unsigned {
     KVSEL_READY_EVICT = 1u << 20,
-    KVSEL_READY_POOL64 = 1u << 21,
-    KVSEL_READY_POOL128 = 1u << 22,
-    KVSEL_READY_MASS64 = 1u << 23,
-    KVSEL_READY_MASS128 = 1u << 24,
+    KVSEL_READY_POOL = 1u << 21,  // and three more: D = 64 and 128, block tables and slot maps
+    KVSEL_READY_MASS = 1u << 25,  // likewise
 };
 
 // Device error-word bits.

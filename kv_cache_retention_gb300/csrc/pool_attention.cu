@@ -255,7 +255,7 @@ __device__ __forceinline__ int units_of(const Session& x, int unit) { return (in
 
 // ---- the kernel ------------------------------------------------------------
 
-template <int D>
+template <int D, bool MAP>
 __global__ void __launch_bounds__(kThreads, 1)
     pool_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                           const __grid_constant__ CUtensorMap map_v, const PoolArgs a) {
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto load = [&](const CUtensorMap* map, const __nv_bfloat16* pool, uint32_t bytes, uint32_t list) {
                 const uint32_t st = c % kStages;
                 if (!(ok = wait_short(&t.empty[st], (c / kStages & 1) ^ 1u, stop, a.err))) return;
-                load_rows<D>(map, pool, bytes, g * D, t.lists.slot + list % kLists * kTile, t.lists.meta[list % kLists].runs,
+                load_rows<D>(map, pool, bytes, g * D, t.lists.token + list % kLists * kTile, t.lists.meta[list % kLists].runs,
                              ring + st * C::kBytes, &t.full[st], warp - 4, lane);
                 ++c;
             };
@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             a.joints[blockIdx.x] = Joint{(int)(tail / quota) - share + 1, w.row, tokens};
                         }
                         publish(w);
-                        ok = ok && make_lists(t.lists, a.map, row, l0 * kTile, w.stop, w.pos0, made, lane, stop, a.err, err);
+                        ok = ok && make_lists<MAP>(t.lists, a.map, row, l0 * kTile, w.stop, w.pos0, made, lane, stop, a.err, err);
                     }
                     at += here;
                 }
@@ -500,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int k = 0; k < 4; ++k) hit |= (y[k] & 0x7F807F80u) + 0x00800080u;
                         if (hit & 0x80008000u) {
-                            atomicMin(&t.odd[u & 1], t.lists.pos[l % kLists * kTile]);
+                            atomicMin(&t.odd[u & 1], t.lists.token[l % kLists * kTile].y);
                             __threadfence_block();
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
@@ -524,11 +524,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_wait_ld();
                     if (meta.masked) {
                         // the row sees the list's tokens up to its own position: those before place `seen`
-                        const int* const pos = t.lists.pos + l % kLists * kTile;
+                        const int2* const list = t.lists.token + l % kLists * kTile;
                         int seen = 0;
 #pragma unroll
                         for (int step = kTile; step; step >>= 1)
-                            if (seen + step <= meta.n && pos[seen + step - 1] <= row_pos) seen += step;
+                            if (seen + step <= meta.n && list[seen + step - 1].y <= row_pos) seen += step;
 #pragma unroll
                         for (int c = 0; c < kTile; ++c)
                             if (c >= seen) s[c] = 0xFF800000u;
@@ -684,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float add = 0.f;
 #pragma unroll 1
                     for (int j = odd; j <= upto; ++j) {
-                        const int slot = live_slot(a.map, raw_entry(a.map, map, j), j, err);
+                        const int slot = live_slot<MAP>(a.map, raw_entry(a.map, map, j), j, err);
                         if (slot < 0) continue;
                         const float e = __bfloat162float(a.v[(uint64_t)(uint32_t)slot * (a.v_bytes / 2) + (int64_t)g * D + d]);
                         if (!(fabsf(e) < INFINITY)) add += e;
@@ -744,11 +744,11 @@ __global__ void __launch_bounds__(256) pool_join_kernel(const PoolArgs a) {
     if (a.lse && warp == 0) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
-template <int D>
+template <int D, bool MAP>
 cudaError_t launch(kvsel_ctx* ctx, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const PoolArgs& a,
                    cudaStream_t s) {
-    auto* kernel = pool_attention_kernel<D>;
-    constexpr unsigned kBit = D == 64 ? KVSEL_READY_POOL64 : KVSEL_READY_POOL128;
+    auto* kernel = pool_attention_kernel<D, MAP>;
+    constexpr unsigned kBit = KVSEL_READY_POOL << (D / 64 - 1 + 2 * MAP);
     if (!(ctx->ready & kBit)) {
         cudaFuncAttributes fa;
         cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
@@ -802,8 +802,9 @@ int attention_call(kvsel_ctx* ctx, const void* q, int64_t q_stride, const int32_
                      (const __nv_bfloat16*)v_pool, (uint32_t)(k_stride * 2), (uint32_t)(v_stride * 2), map, scale * kLog2e,
                      (__nv_bfloat16*)out, lse, ctx->dev_err, Hkv < ctx->num_sms ? ctx->num_sms / Hkv : 1, parts,
                      (Joint*)(parts + (size_t)ctx->num_sms * 2 * kPart), wait_ns, stuck};
-    const cudaError_t e = D == 64 ? launch<64>(ctx, mq, mk, mv, a, (cudaStream_t)stream)
-                                   : launch<128>(ctx, mq, mk, mv, a, (cudaStream_t)stream);
+    const cudaStream_t st = (cudaStream_t)stream;
+    const cudaError_t e = slot_map ? D == 64 ? launch<64, true>(ctx, mq, mk, mv, a, st) : launch<128, true>(ctx, mq, mk, mv, a, st)
+                          : D == 64 ? launch<64, false>(ctx, mq, mk, mv, a, st) : launch<128, false>(ctx, mq, mk, mv, a, st);
     return e == cudaSuccess ? KVSEL_OK : kvsel_cuda_fail(ctx, e, "pool_attention launch");
 }
 

@@ -49,24 +49,23 @@ struct ListMeta {
     unsigned runs;  // of each four tokens, whether they go on a run of slots that starts with their kRun; a bit each
 };
 
-// A ring of N lists.  slot, pos: the tokens in ascending positions; behind the n-th the slot of the first.
+// A ring of N lists.  token: slot and position, in ascending positions; behind the n-th the slot of the first.
 template <int N>
 struct Lists {
-    static constexpr int kAhead = 8;
-    int slot[N * kTile], pos[N * kTile];
-    int entry[32 * kAhead];             // the making warp's own
-    static_assert(kAhead % 4 == 0, "whole rounds");
+    static constexpr int kAhead = 4;    // rounds whose entries are on their way
+    int2 token[N * kTile];
+    int entry[kAhead * kTile];          // the making warp's own
     ListMeta meta[N];
     uint64_t full[N], empty[N];
 };
 
 // Makes the lists of positions [p0, p1) of a session, at least one; pos0: where the first row that will look at them sits.
 // A list is handed out when it is known whether another follows.  made: lists of the block so far.  The whole warp calls.
+// MAP: a slot map, not a block table.
 // A round takes 128 positions, four of each lane (with one of each lane and 32 a round, the chain of dependent instructions
-// took 640 cycles for those), and is not unrolled, for the instruction cache's sake.  Entries are read kAhead at a time and
-// lane, while the ones before are gone through, and wait for their round in shared memory (a queue of registers would wait
-// for its loads whenever it moves).
-template <int N>
+// took 640 cycles for those), and is not unrolled, for the instruction cache's sake.  Entries come through cp.async, kAhead
+// rounds ahead of their use.
+template <bool MAP, int N>
 __device__ __forceinline__ bool make_lists(Lists<N>& t, const TokenMap& m, const int32_t* row, int p0, int p1, int pos0, uint32_t& made,
                                            int lane, Stop* stop, unsigned* err_word, unsigned& err) {
     constexpr int kAhead = Lists<N>::kAhead;
@@ -74,55 +73,62 @@ __device__ __forceinline__ bool make_lists(Lists<N>& t, const TokenMap& m, const
     uint32_t l = made;                  // the list that tokens go to, and how many it has
     int n = 0;
     bool ok = l < N || wait_short(&t.empty[l % N], (l / N - 1) & 1, stop, err_word);
-    int next[kAhead];
-    auto read = [&](int p) {
+    const bool wide = MAP && (reinterpret_cast<uintptr_t>(row) & 15) == 0;
+    auto read = [&](int p, int at) {    // (nothing is read behind p1)
+        const int j = p + 4 * lane;
+        const uint32_t to = saddr(&t.entry[at * kTile + 4 * lane]);
+        if (wide) {
+            if (j < p1)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(row + j), "r"(4 * min(4, p1 - j)) : "memory");
+        } else {
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) next[k] = p + 32 * k < p1 ? raw_entry(m, row, p + 32 * k) : -1;
+            for (int k = 0; k < 4; ++k)
+                if (j + k < p1)
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + 4 * k), "l"(row + (MAP ? j + k : entry_of(m, j + k)))
+                                 : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    read(p0 + lane);
+#pragma unroll 1
+    for (int k = 0; k < kAhead - 1; ++k) read(p0 + k * kTile, k);
     // hands out list l of n tokens
     auto hand_out = [&](int last) {
         __syncwarp();
-        const int4 s = *reinterpret_cast<const int4*>(&t.slot[l % N * kTile + 4 * lane]);
-        const int first = t.slot[l % N * kTile + (lane & ~(kRun / 4 - 1)) * 4], off = 4 * (lane % (kRun / 4));
-        const bool run = s.x == first + off && s.y == s.x + 1 && s.z == s.x + 2 && s.w == s.x + 3;
+        const int2* const list = &t.token[l % N * kTile];
+        const int4 s01 = *reinterpret_cast<const int4*>(list + 4 * lane), s23 = *reinterpret_cast<const int4*>(list + 4 * lane + 2);
+        const int first = list[(lane & ~(kRun / 4 - 1)) * 4].x, off = 4 * (lane % (kRun / 4));
+        const bool run = s01.x == first + off && s01.z == s01.x + 1 && s23.x == s01.x + 2 && s23.z == s01.x + 3;
         const unsigned runs = __ballot_sync(0xffffffffu, run);
         if (lane == 0) {
-            t.meta[l % N] = ListMeta{n, n < kTile || t.pos[l % N * kTile + n - 1] > pos0, last, t.pos[l % N * kTile], runs};
+            t.meta[l % N] = ListMeta{n, n < kTile || list[n - 1].y > pos0, last, list[0].y, runs};
             mbar_arrive(&t.full[l % N]);
         }
         ++l;
     };
+    int round = 0;
 #pragma unroll 1
-    for (int p = p0, round = kAhead / 4; ok && p < p1; p += kTile, ++round) {
-        if (round == kAhead / 4) {
-            __syncwarp();
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k) t.entry[32 * k + lane] = next[k];
-            __syncwarp();
-            if (p1 - p > 32 * kAhead) read(p + 32 * kAhead + lane);
-            round = 0;
-        }
-        const int4 entry = *reinterpret_cast<const int4*>(&t.entry[kTile * round + 4 * lane]);
+    for (int p = p0; ok && p < p1; p += kTile) {
+        read(p1 - p > (kAhead - 1) * kTile ? p + (kAhead - 1) * kTile : p1, (round + kAhead - 1) % kAhead);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");  // (a lane reads what it has copied itself)
+        const int4 entry = *reinterpret_cast<const int4*>(&t.entry[round * kTile + 4 * lane]);
+        round = (round + 1) % kAhead;
         const int j = p + 4 * lane;
-        int slot[4], at[4];
-        slot[0] = live_slot(m, entry.x, j, err);
-        slot[1] = live_slot(m, entry.y, j + 1, err);
-        slot[2] = live_slot(m, entry.z, j + 2, err);
-        slot[3] = live_slot(m, entry.w, j + 3, err);
+        int slot[4] = {entry.x, entry.y, entry.z, entry.w}, at[4];
         int before = n, more = 0, mine = 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
+            slot[k] = j + k < p1 ? live_slot<MAP>(m, slot[k], j + k, err) : -1;
             const unsigned live = __ballot_sync(0xffffffffu, slot[k] >= 0);
             before += __popc(live & below);
             more += __popc(live);
             at[k] = mine;
             mine += slot[k] >= 0;
         }
+        int2* const list = &t.token[l % N * kTile];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             at[k] += before;
-            if (slot[k] >= 0 && at[k] < kTile) t.slot[l % N * kTile + at[k]] = slot[k], t.pos[l % N * kTile + at[k]] = j + k;
+            if (slot[k] >= 0 && at[k] < kTile) list[at[k]] = make_int2(slot[k], j + k);
         }
         n += more;
         if (n > kTile) {                // the list is full, and others follow
@@ -132,17 +138,17 @@ __device__ __forceinline__ bool make_lists(Lists<N>& t, const TokenMap& m, const
             if (l >= N) ok = wait_short(&t.empty[l % N], (l / N - 1) & 1, stop, err_word);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                if (ok && slot[k] >= 0 && at[k] >= kTile)
-                    t.slot[l % N * kTile + at[k] - kTile] = slot[k], t.pos[l % N * kTile + at[k] - kTile] = j + k;
+                if (ok && slot[k] >= 0 && at[k] >= kTile) t.token[l % N * kTile + at[k] - kTile] = make_int2(slot[k], j + k);
             n = rest;
         }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     if (!ok) return false;
     __syncwarp();
     if (n > 0) {
-        const int spare = t.slot[l % N * kTile];
+        const int spare = t.token[l % N * kTile].x;
         __syncwarp();
-        for (int e = n + lane; e < kTile; e += 32) t.slot[l % N * kTile + e] = spare;
+        for (int e = n + lane; e < kTile; e += 32) t.token[l % N * kTile + e].x = spare;
     }
     hand_out(1);
     made = l;
@@ -178,7 +184,7 @@ inline bool make_query_map(CUtensorMap* map, const void* base, int T, int Hq, in
 // of kRun slots come by TMA, others row by row through cp.async (TMA gathers of four slots took 45 ns each from one thread, 6
 // us for a list's K and V).  Such rows are written through the generic proxy: who has seen `full` fences before MMAs on them.
 template <int D>
-__device__ __forceinline__ void load_rows(const CUtensorMap* map, const __nv_bfloat16* pool, uint32_t stride_bytes, int x, const int* slots,
+__device__ __forceinline__ void load_rows(const CUtensorMap* map, const __nv_bfloat16* pool, uint32_t stride_bytes, int x, const int2* tokens,
                                           unsigned runs, const uint8_t* tile, uint64_t* full, int w, int lane) {
     constexpr int kChunks = D / 8, kRows = 32 / kChunks;  // 16-byte chunks of a row; rows of one instruction
     constexpr int kShare = 32;
@@ -186,7 +192,7 @@ __device__ __forceinline__ void load_rows(const CUtensorMap* map, const __nv_bfl
     const char* const from = reinterpret_cast<const char*>(pool + x) + chunk * 16;
     const uint32_t to = saddr(tile) + (chunk >> 3) * (kTile * 128) + (kShare * w + low) * 128;
     const uint32_t swizzled = ((chunk & 7) ^ low) << 4;    // of row `low`; of row i + low, i a multiple of kRows: ^ (i & 7) << 4
-    const int slot = slots[kShare * w + lane];
+    const int slot = tokens[kShare * w + lane].x;
     constexpr unsigned kAll = (1u << kRun / 4) - 1;
 #pragma unroll 1
     for (int r = 0; r < kShare; r += kRun) {

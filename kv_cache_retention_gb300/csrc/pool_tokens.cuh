@@ -8,14 +8,13 @@
 
 namespace {
 
-// Slot maps (page == 1) or block tables, int32 [S][ld].
+// Slot maps (page == 0) or block tables, int32 [S][ld].
 struct TokenMap {
     const int32_t* map;
     int ld, reach;           // row length, and the positions that a row holds
     int page;
     uint32_t mul, shift;     // j / page = j mul >> shift
     int limit;               // entries lie below it: pages or slots
-    unsigned bad;            // the error of one that does not
     int dead;
 };
 
@@ -29,13 +28,14 @@ __device__ __forceinline__ int entry_of(const TokenMap& m, int j) {
 }
 // What the map says of position j (below its reach): a slot, or the page that holds it.
 __device__ __forceinline__ int raw_entry(const TokenMap& m, const int32_t* row, int j) { return __ldg(row + entry_of(m, j)); }
-// Slot of position j, from what the map says; -1 where it is not live.
+// Slot of position j, from what the map says; -1 where it is not live.  MAP: a slot map, not a block table.
+template <bool MAP>
 __device__ __forceinline__ int live_slot(const TokenMap& m, int entry, int j, unsigned& err) {
     if ((unsigned)entry >= (unsigned)m.limit) {
-        if (entry >= 0 && (m.page != 1 || entry != m.dead)) err |= m.bad;
+        if (entry >= 0 && (!MAP || entry != m.dead)) err |= MAP ? KVSEL_DEV_BAD_SLOT : KVSEL_DEV_BAD_PAGE;
         return -1;
     }
-    const int slot = entry * m.page + (j - entry_of(m, j) * m.page);
+    const int slot = MAP ? entry : entry * m.page + (j - entry_of(m, j) * m.page);
     return slot == m.dead ? -1 : slot;
 }
 
@@ -82,9 +82,9 @@ inline int check_pool_call(kvsel_ctx* ctx, const char* who, int S, int T, int Hq
         if ((reinterpret_cast<uintptr_t>(pools[i]) & 15u) || (strides[i] * 2) % 16)
             return kvsel_fail(ctx, KVSEL_ERR_ALIGN, "%s: pools and their strides must be 16-byte aligned", who);
     }
-    *map = TokenMap{slot_map ? slot_map : block_table, ld, (int)reach, 1, 1, 0, P * page, KVSEL_DEV_BAD_SLOT, dead_slot};
+    *map = TokenMap{slot_map ? slot_map : block_table, ld, (int)reach, 0, 1, 0, P * page, dead_slot};
     if (!slot_map) {
-        map->page = page, map->limit = P, map->bad = KVSEL_DEV_BAD_PAGE;
+        map->page = page, map->limit = P;
         if (page > 1) {  // with 2^(l-1) < page <= 2^l, (2^(31+l) / page + 1) j >> (31+l) is the quotient for every j < 2^31
             int l = 1;
             while (((int64_t)1 << l) < page) ++l;
