@@ -21,9 +21,8 @@
 // since both operands of the product have one type and V's range is bf16's: 2^-8 at most per weight, at random, about the
 // output's own rounding.
 //
-// 512 threads: warp 0 plans and makes the lists, warps 1 and 2 issue the MMAs of one tile each (warp 1 of both, where the
-// rows are one tile's), warps 4-7 load, warps 8-11 and 12-15 are the softmax of the two tiles, a row per thread.  TMEM: S of
-// tile 0 and 1 at columns 0 and 128, O at 256 and on.
+// 512 threads: warp 0 plans and makes the lists, warps 1 and 2 issue the MMAs of one tile each, warps 4-7 load, warps 8-11 and
+// 12-15 are the softmax of the two tiles, a row per thread.  TMEM: S of tile 0 and 1 at columns 0 and 128, O at 256 and on.
 //
 // Shares.  The units' keys, laid end to end with some for the start of each, are cut into equal shares, found from the
 // lengths on the device; neighbouring blocks take a share for one kv head each (the heads' rows of a slot lie side by side).
@@ -46,7 +45,7 @@ constexpr int kThreads = 512;
 constexpr float kSlack = 8.f;           // how far (log2) a row's maximum may pass its reference
 // Registers per thread: at launch, then after the first warpgroup's setmaxnreg.dec and the softmax warpgroups' .inc.  An
 // .inc beyond the launch's registers would wait forever; the launcher checks the compiled count.
-constexpr int kRegsLaunch = 128, kRegsCtl = 56, kRegsSoft = 200;
+constexpr int kRegsLaunch = 128, kRegsCtl = 72, kRegsSoft = 184;
 static_assert(2 * kRegsCtl + 2 * kRegsSoft <= 4 * kRegsLaunch && kRegsLaunch * kThreads <= 65536, "register split");
 constexpr int kLists = 8;
 constexpr int kStart = 4;               // lists that the start of a unit counts as when shares are cut
@@ -86,7 +85,7 @@ template <int D>
 struct Cfg {
     static constexpr int kBlock = kTile * 128;             // 128 rows x 64 dims, 128-byte swizzled
     static constexpr int kBytes = D / 64 * kBlock;         // one tile of Q, K or V
-    static constexpr int kStages = 4;                      // K and V tiles share the ring
+    static constexpr int kStages = 4;                      // K and V tiles share the ring (at_k and at_v count on four)
     static constexpr int kOut = 8 * 32 * 64;               // 32 rows of 32 dims for each softmax warp, on their way out
     // What a block does of one unit; end: there is nothing more.
     struct Piece {
@@ -110,24 +109,29 @@ struct Cfg {
     static_assert(kSmem <= 232448, "shared memory per block");
 };
 
-// Place in the ring of list i's K and V tile: K0, K1, V0, K2, V1, ..., V(n-1); last: list i is the last.
-__device__ __forceinline__ int at_k(int i) { return i == 0 ? 0 : 2 * i - 1; }
-__device__ __forceinline__ int at_v(int i, bool last) { return last ? 2 * i + 1 : 2 * i + 2; }
+// Places in the ring of list i's K and V tile, from the piece's first one on.  Where the two tiles share the lists (two): K0,
+// K1, V0, K2, V1, ..., V(n-1) with the last list's V right behind its K.  Where they have every other list: K0, K1, V0, V1, K2,
+// K3, ..., a place for each of a last pair, so that a stage of the ring is one tile's alone.
+__device__ __forceinline__ int at_k(bool two, int i) { return !two ? (i >> 1) * 4 + (i & 1) : i == 0 ? 0 : 2 * i - 1; }
+__device__ __forceinline__ int at_v(bool two, int i, bool last) { return !two ? (i >> 1) * 4 + 2 + (i & 1) : last ? 2 * i + 1 : 2 * i + 2; }
+__device__ __forceinline__ int places(bool two, int n) { return two ? 2 * n : (n + 1) / 2 * 4; }
 
 // ---- MMAs: a warp per tile -------------------------------------------------
 // Two issuers on two SM sub-partitions that take turns, so that one tile's products run beside the other's softmax.  One
-// copy of the code for both.  Each warp sees every phase of the ring's barriers, whoever's tile it is: a wait for a phase that
-// is two behind would return at once, one for a phase with another one done behind it never.  (The barriers of O are in pairs
-// for the same reason: a piece does not begin before the one two before it has been read.)
+// copy of the code for both.  Where they share lists, both see and release every tile of the ring; where they have every
+// other list, a stage of the ring is one warp's alone for the whole piece.  A wait for a phase that is two behind would return
+// at once, one for a phase with another one done behind it never: so such a piece begins, and ends, when all the tiles of the one
+// before have been used, and the barriers of O are in pairs (a piece does not begin before the one two before it has been read).
 template <int D>
 __device__ __forceinline__ void issue_tiles(typename Cfg<D>::Tail& t, const uint8_t* sq, const uint8_t* ring, int tile, int lane,
                                             bool stuck, Stop* stop, unsigned* err) {
     using C = Cfg<D>;
     constexpr uint32_t kStages = C::kStages;
     const uint32_t lead = lane == 0, X = uniform(tile);
-    uint32_t base = 0, lists = 0, turns = 0, steps0 = 0, steps1 = 0;  // ring places, lists, turns and the tiles' steps so far
-    bool was_two = false;
+    uint32_t base = 0, lists = 0, turns = 0, steps = 0;  // ring places, lists, turns and this tile's steps so far
+    bool was_two = true;
     bool ok = !stuck || wait_short(&t.never, 0, stop, err);
+    const uint32_t ts = uniform(kTmem + kColS + X * kTile), to = uniform(kTmem + kColO + X * D);
     for (uint32_t u = 0; ok; ++u) {
         if (!(ok = wait_short(&t.piece_full[u & 1], (u >> 1) & 1, stop, err))) break;
         const bool two = t.piece[u & 1].two, end = t.piece[u & 1].end;
@@ -150,90 +154,74 @@ __device__ __forceinline__ void issue_tiles(typename Cfg<D>::Tail& t, const uint
             return i < n;
         };
         ok = wait_short(&t.q_full, u & 1, stop, err);
-        if (two != was_two && u) {                // tiles may change hands: the products on them have ended
+        if (!(two && was_two) && u) {             // the tiles of the ring that the other warp alone has seen have landed
 #pragma unroll 1
             for (int x = 0; x < 2; ++x) ok = ok && wait_short(&t.o_free[x][(u - 1) & 1], ((u - 1) >> 1) & 1, stop, err);
         }
-        if (X == 1 && !two) {
-            // the other warp's lists: this one sees and releases their tiles all the same
-            if (ok && lead) mbar_arrive(&t.q_empty);
-            int seen = 0;
-#pragma unroll 1
-            for (int i = 0; ok; ++i) {
-                const bool have = there_is(i);
-#pragma unroll 1
-                for (const int upto = have ? 2 * i + 1 : 2 * n; ok && seen < upto; ++seen) {
-                    const uint32_t at = base + seen;
-                    ok = wait_short(&t.full[at % kStages], at / kStages & 1, stop, err);
-                    if (ok && lead) mbar_arrive(&t.empty[at % kStages]);
-                }
-                if (!have) break;
-            }
-            steps0 += (n + 1) / 2, steps1 += n / 2;
-        } else {
-            const int by = two ? 1 : 2;
-            const uint32_t q = uniform(desc_low(saddr(sq) + (two ? X * C::kBytes : 0u), 16));
-            bool released = false;
-            // Round i: O += P V of list i (from 0 on), then S of list i + by on the same tile (while there is one).
-#pragma unroll 1
-            for (int i = -by; ok; ++i) {
-                const uint32_t x = two ? X : (uint32_t)i & 1;
-                const uint32_t ts = uniform(kTmem + kColS + x * kTile), to = uniform(kTmem + kColO + x * D);
-                const bool more = there_is(i + by), product = i >= 0, done = ended && i + 1 >= n;
-                if (!more && !released) {         // no further S: Q is released when the ones issued have ended
-                    mma_commit(saddr(&t.q_empty), lead);
-                    released = true;
-                }
-                const uint32_t av = base + at_v(i, ended && i == n - 1), ak = base + at_k(i + by);
-                const uint32_t vd = uniform(desc_low(saddr(ring) + av % kStages * C::kBytes, C::kBlock));
-                const uint32_t kd = uniform(desc_low(saddr(ring) + ak % kStages * C::kBytes, 16));
-                const uint32_t step = (x ? steps1 : steps0) & 1;
-                // all that can be waited for ahead of the turn; one answer for the lanes at the end of the round
-                if (more) ok = wait_lane(&t.full[ak % kStages], ak / kStages & 1, stop, err) && ok;
-                if (product) {
-                    ok = wait_lane(&t.full[av % kStages], av / kStages & 1, stop, err) && ok;
-                    if (u && i < by) ok = wait_lane(&t.o_free[x][(u - 1) & 1], ((u - 1) >> 1) & 1, stop, err) && ok;
-                    fence_async();
-                    if (two && (X == 1 || i > 0)) ok = wait_lane(&t.turn[X], turns++ & 1, stop, err) && ok;
-                    const uint32_t fresh = i < by;
-                    ok = wait_lane(&t.p_full[x][0], step, stop, err) && ok;
-                    tc_after();
-#pragma unroll
-                    for (int k = 0; k < kTile / 32; ++k)
-                        mma_ts(to, ts + k * 8, vd + k * (2048 >> 4), idesc(D, true), k > 0 || !fresh, lead);
-                    ok = wait_lane(&t.p_full[x][1], step, stop, err) && ok;
-                    tc_after();
-#pragma unroll
-                    for (int k = kTile / 32; k < kTile / 16; ++k)
-                        mma_ts(to, ts + k * 8, vd + k * (2048 >> 4), idesc(D, true), 1, lead);
-                    if (x) ++steps1; else ++steps0;
-                } else {
-                    fence_async();
-                    tc_after();
-                }
-                if (more) {                       // writes over the P read above: one thread's MMAs run in the order of issue
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t off = ((k >> 2) * C::kBlock + (k & 3) * 32) >> 4;
-                        // the other tile's turn: its issuer is under way while the last of these are issued
-                        if (k == D / 32 && two && product && lead) mbar_arrive(&t.turn[x ^ 1]);
-                        mma_ss(ts, q + off, kd + off, idesc(kTile, false), k > 0, lead);
-                    }
-                    mma_commit(saddr(&t.s_full[x]), lead);
-                    mma_commit(saddr(&t.empty[ak % kStages]), lead);
-                } else if (product) {
-                    if (two && X == 0 && lead) mbar_arrive(&t.turn[1]);
-                    mma_commit(saddr(&t.o_done[x]), lead);
-                }
-                if (product) mma_commit(saddr(&t.empty[av % kStages]), lead);
-                ok = __all_sync(0xffffffffu, ok);
-                if (done) break;
-            }
-            if (two && X == 0) steps1 += n;
-            if (two && X == 1) steps0 += n;
-        }
-        base += 2 * n;
         was_two = two;
+        const int by = two ? 1 : 2, first = two ? 0 : (int)X;
+        const uint32_t q = uniform(desc_low(saddr(sq) + (two ? X * C::kBytes : 0u), 16));
+        // Round i: O += P V of list i (not before the first), then S of list i + by (while there is one).
+#pragma unroll 1
+        for (int i = first - by; ok; i += by) {
+            const bool more = there_is(i + by), product = i >= first;
+            if (!more) mma_commit(saddr(&t.q_empty), lead);  // no further S: Q is released when the ones issued have ended
+            const uint32_t av = base + at_v(two, i, ended && i == n - 1), ak = base + at_k(two, i + by);
+            const uint32_t vd = uniform(desc_low(saddr(ring) + av % kStages * C::kBytes, C::kBlock));
+            const uint32_t kd = uniform(desc_low(saddr(ring) + ak % kStages * C::kBytes, 16));
+            // all that can be waited for ahead of the turn; one answer for the lanes at the end of the round
+            if (more) ok = wait_lane(&t.full[ak % kStages], ak / kStages & 1, stop, err) && ok;
+            if (product) {
+                ok = wait_lane(&t.full[av % kStages], av / kStages & 1, stop, err) && ok;
+                if (u && i == first) ok = wait_lane(&t.o_free[X][(u - 1) & 1], ((u - 1) >> 1) & 1, stop, err) && ok;
+                fence_async();
+                if (two && (X == 1 || i > 0)) ok = wait_lane(&t.turn[X], turns++ & 1, stop, err) && ok;
+                ok = wait_lane(&t.p_full[X][0], steps & 1, stop, err) && ok;
+                tc_after();
+#pragma unroll
+                for (int k = 0; k < kTile / 32; ++k)
+                    mma_ts(to, ts + k * 8, vd + k * (2048 >> 4), idesc(D, true), k > 0 || i != first, lead);
+                ok = wait_lane(&t.p_full[X][1], steps & 1, stop, err) && ok;
+                tc_after();
+#pragma unroll
+                for (int k = kTile / 32; k < kTile / 16; ++k)
+                    mma_ts(to, ts + k * 8, vd + k * (2048 >> 4), idesc(D, true), 1, lead);
+                ++steps;
+            } else {
+                fence_async();
+                tc_after();
+            }
+            if (more) {                           // writes over the P read above: one thread's MMAs run in the order of issue
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = ((k >> 2) * C::kBlock + (k & 3) * 32) >> 4;
+                    // the other tile's turn: its issuer is under way while the last of these are issued
+                    if (k == D / 32 && two && product && lead) mbar_arrive(&t.turn[X ^ 1]);
+                    mma_ss(ts, q + off, kd + off, idesc(kTile, false), k > 0, lead);
+                }
+                mma_commit(saddr(&t.s_full[X]), lead);
+                mma_commit(saddr(&t.empty[ak % kStages]), lead);
+                if (!two) mma_commit(saddr(&t.empty[ak % kStages]), lead);  // for the other warp too
+            } else if (product) {
+                if (two && X == 0 && lead) mbar_arrive(&t.turn[1]);
+                mma_commit(saddr(&t.o_done[X]), lead);
+            }
+            if (product) {
+                mma_commit(saddr(&t.empty[av % kStages]), lead);
+                if (!two) mma_commit(saddr(&t.empty[av % kStages]), lead);
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            if (!more) break;
+        }
+        if (!two && X == 1 && (n & 1)) {          // the places of the list that is not there
+#pragma unroll 1
+            for (int v = 0; v < 2; ++v) {
+                const uint32_t at = base + (v ? at_v(false, n, true) : at_k(false, n));
+                ok = ok && wait_short(&t.full[at % kStages], at / kStages & 1, stop, err);
+                if (ok && lead) mbar_arrive(&t.empty[at % kStages]), mbar_arrive(&t.empty[at % kStages]);
+            }
+        }
+        base += places(two, n);
     }
     mma_commit(saddr(&t.drained), lead);
     drain_phase(&t.drained, 0);
@@ -309,13 +297,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ---- loads ----
             uint32_t c = 0, l = 0, loaded_q = 0;  // ring places filled, lists, Q loads
             bool ok = true;
-            auto load = [&](const CUtensorMap* map, const __nv_bfloat16* pool, uint32_t bytes, uint32_t list) {
-                const uint32_t st = c % kStages;
-                if (!(ok = wait_short(&t.empty[st], (c / kStages & 1) ^ 1u, stop, a.err))) return;
-                load_rows<D>(map, pool, bytes, g * D, t.lists.token + list % kLists * kTile, t.lists.meta[list % kLists].runs,
-                             ring + st * C::kBytes, &t.full[st], warp - 4, lane);
-                ++c;
-            };
             auto release = [&](uint32_t list) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&t.lists.empty[list % kLists]);
@@ -335,23 +316,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                                      w.row + x * a.tile_tokens);
                 }
                 ++loaded_q;
-                // K of a list, then V of the one before it; V of the last
-                bool last = false;
-                int n = 0;
+                int n = 0;                        // lists of the piece so far
+                bool ended = false;
+                auto there_is = [&](int i) {      // list i
 #pragma unroll 1
-                for (int i = 0; ok && i <= n; ++i) {
-                    if (!last) {
-                        if (!(ok = wait_short(&t.lists.full[(l + i) % kLists], (l + i) / kLists & 1, stop, a.err))) break;
-                        const ListMeta meta = t.lists.meta[(l + i) % kLists];
-                        last = meta.last;
-                        n += meta.n != 0;
-                        if (!meta.n) release(l + i);
+                    while (ok && !ended && n <= i) {
+                        const uint32_t at = (l + n) % kLists;
+                        if (!(ok = wait_short(&t.lists.full[at], (l + n) / kLists & 1, stop, a.err))) break;
+                        ended = t.lists.meta[at].last;
+                        if (t.lists.meta[at].n)
+                            ++n;
+                        else
+                            release(l);
                     }
+                    return i < n;
+                };
+                // place after place of the ring
 #pragma unroll 1
-                    for (int v = i < n ? 0 : 1; ok && v < (i > 0 ? 2 : 1); ++v) {
-                        load(v ? &map_v : &map_k, v ? a.v : a.k, v ? a.v_bytes : a.k_bytes, l + i - v);
-                        if (v) release(l + i - 1);
+                for (int p = 0; ok; ++p) {
+                    int i = w.two ? (p + 1) / 2 : p / 4 * 2 + (p & 1);
+                    bool v = w.two ? p > 0 && !(p & 1) : (p & 2) != 0, last = false;
+                    if (w.two && v) i -= 1;
+                    const bool real = there_is(i);
+                    if (!real && !(p & 1)) break;
+                    if (!real && w.two) i -= 1, v = last = true;
+                    const uint32_t st = c % kStages, list = (l + i) % kLists;
+                    if (!(ok = ok && wait_short(&t.empty[st], (c / kStages & 1) ^ 1u, stop, a.err))) break;
+                    if (real || w.two) {
+                        load_rows<D>(v ? &map_v : &map_k, v ? a.v : a.k, v ? a.v_bytes : a.k_bytes, g * D, t.lists.token + list * kTile,
+                                     t.lists.meta[list].runs, ring + st * C::kBytes, &t.full[st], warp - 4, lane);
+                        if (v) release(l + i);
+                    } else {
+                        mbar_arrive(&t.full[st]);
                     }
+                    ++c;
+                    if (last) break;
                 }
                 l += max(n, 1);
             }
@@ -490,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!(ok = wait_short(&t.s_full[x], done & 1, stop, a.err))) break;
                 if (meta.masked) {
                     // NaN and infinities of V to zero; both tiles look at all of it (a value may be set twice)
-                    const uint32_t at = base + at_v(i, last), st = at % kStages;
+                    const uint32_t at = base + at_v(w.two, i, last), st = at % kStages;
                     if (!(ok = wait_short(&t.full[st], at / kStages & 1, stop, a.err))) break;
                     uint4* const tile = reinterpret_cast<uint4*>(ring + st * C::kBytes);
 #pragma unroll 1
@@ -542,7 +541,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int b = 0; b < 4; ++b) m[b] = max3(m[b], __uint_as_float(s[c + b]), __uint_as_float(s[c + 4 + b]));
 #pragma unroll
                     for (int b = 0; b < 4; ++b) m[b] = fmaxf(m[b], __uint_as_float(s[kTile - 4 + b]));
-                    const float top = fmaxf(max3(m[0], m[1], m[2]), m[3]) * sc;
+                    // (rows of no token hold anything, and have no say in when references move)
+                    const float top = r < rows ? fmaxf(max3(m[0], m[1], m[2]), m[3]) * sc : -INFINITY;
                     if (steps == 0) {
                         ref = fmaxf(top, -3e38f);  // of a row whose logits here are all -inf: low, and finite
                     } else if (__any_sync(0xffffffffu, top > ref + kSlack)) {
@@ -590,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&t.lists.empty[l % kLists]);
         }
         if (!ok) break;
-        base += 2 * n;
+        base += places(w.two, n);
         // ---- output ----
         if (steps && !(ok = wait_short(&t.o_done[x], mine++ & 1, stop, a.err))) break;
         tc_after();
