@@ -128,29 +128,34 @@ __device__ __forceinline__ void issue_tiles(typename Cfg<D>::Tail& t, const uint
     using C = Cfg<D>;
     constexpr uint32_t kStages = C::kStages;
     const uint32_t lead = lane == 0, X = uniform(tile);
-    uint32_t base = 0, lists = 0, turns = 0, steps = 0;  // ring places, lists, turns and this tile's steps so far
+    uint32_t base = 0, turns = 0, steps = 0;  // ring places, turns and this tile's steps so far
     bool was_two = true;
     bool ok = !stuck || wait_short(&t.never, 0, stop, err);
     const uint32_t ts = uniform(kTmem + kColS + X * kTile), to = uniform(kTmem + kColO + X * D);
     for (uint32_t u = 0; ok; ++u) {
         if (!(ok = wait_short(&t.piece_full[u & 1], (u >> 1) & 1, stop, err))) break;
-        const bool two = t.piece[u & 1].two, end = t.piece[u & 1].end;
-        __syncwarp();
-        if (lead) mbar_arrive(&t.piece_empty[u & 1]);
-        if (end) break;
-        int n = 0;                                // lists of the piece so far
+        const bool two = t.piece[u & 1].two;
+        if (t.piece[u & 1].end) break;
+        int n = 0;                                // lists of the piece that are known of
         bool ended = false;
-        auto there_is = [&](int i) {              // list i
+        auto there_is = [&](int i) {              // list i; looks no more often than it has to
+            uint32_t t0 = 0;
 #pragma unroll 1
             while (ok && !ended && n <= i) {
-                const uint32_t l = lists % kLists;
-                if (!(ok = wait_short(&t.lists.full[l], lists / kLists & 1, stop, err))) break;
-                n += t.lists.meta[l].n != 0;
-                ended = t.lists.meta[l].last;
-                __syncwarp();
-                if (lead) mbar_arrive(&t.lists.empty[l]);
-                ++lists;
+                const int p = t.lists.progress[u & 1];
+                n = p >> 1;
+                ended = p & 1;
+                if (ended || n > i) break;
+                uint32_t now;
+                asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(now));
+                now |= 1;
+                if (!t0) t0 = now;
+                // (whoever makes the lists gives up at the same limit, and says so)
+                if (stop->given_up || now - t0 > (uint32_t)stop->limit_ns) stop->given_up = 1, atomicOr(err, (unsigned)KVSEL_DEV_TIMEOUT), ok = false;
             }
+            ok = __all_sync(0xffffffffu, ok);
+            n = __shfl_sync(0xffffffffu, n, 0);
+            ended = __shfl_sync(0xffffffffu, ended, 0);
             return i < n;
         };
         ok = wait_short(&t.q_full, u & 1, stop, err);
@@ -169,14 +174,19 @@ __device__ __forceinline__ void issue_tiles(typename Cfg<D>::Tail& t, const uint
             const uint32_t av = base + at_v(two, i, ended && i == n - 1), ak = base + at_k(two, i + by);
             const uint32_t vd = uniform(desc_low(saddr(ring) + av % kStages * C::kBytes, C::kBlock));
             const uint32_t kd = uniform(desc_low(saddr(ring) + ak % kStages * C::kBytes, 16));
-            // all that can be waited for ahead of the turn; one answer for the lanes at the end of the round
-            if (more) ok = wait_lane(&t.full[ak % kStages], ak / kStages & 1, stop, err) && ok;
+            // one answer for the lanes at the end of the round
+            uint64_t* const k_full = &t.full[ak % kStages];
+            const uint32_t k_par = ak / kStages & 1;
             if (product) {
-                ok = wait_lane(&t.full[av % kStages], av / kStages & 1, stop, err) && ok;
+                // K, V, this tile's turn and the first half of P
+                uint64_t* const v_full = &t.full[av % kStages];
+                const uint32_t v_par = av / kStages & 1;
+                const bool turn = two && (X == 1 || i > 0);
                 if (u && i == first) ok = wait_lane(&t.o_free[X][(u - 1) & 1], ((u - 1) >> 1) & 1, stop, err) && ok;
+                ok = wait_lane4(v_full, v_par, more ? k_full : v_full, more ? k_par : v_par, turn ? &t.turn[X] : v_full,
+                                turn ? turns & 1 : v_par, &t.p_full[X][0], steps & 1, stop, err) && ok;
+                turns += turn;
                 fence_async();
-                if (two && (X == 1 || i > 0)) ok = wait_lane(&t.turn[X], turns++ & 1, stop, err) && ok;
-                ok = wait_lane(&t.p_full[X][0], steps & 1, stop, err) && ok;
                 tc_after();
 #pragma unroll
                 for (int k = 0; k < kTile / 32; ++k)
@@ -188,6 +198,7 @@ __device__ __forceinline__ void issue_tiles(typename Cfg<D>::Tail& t, const uint
                     mma_ts(to, ts + k * 8, vd + k * (2048 >> 4), idesc(D, true), 1, lead);
                 ++steps;
             } else {
+                if (more) ok = wait_lane(k_full, k_par, stop, err) && ok;
                 fence_async();
                 tc_after();
             }
@@ -222,6 +233,8 @@ __device__ __forceinline__ void issue_tiles(typename Cfg<D>::Tail& t, const uint
             }
         }
         base += places(two, n);
+        __syncwarp();
+        if (lead) mbar_arrive(&t.piece_empty[u & 1]);
     }
     mma_commit(saddr(&t.drained), lead);
     drain_phase(&t.drained, 0);
@@ -261,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         mbar_init(&t.q_full, 1);
         mbar_init(&t.q_empty, 2);
-        for (int i = 0; i < kStages; ++i) mbar_init(&t.full[i], 128), mbar_init(&t.empty[i], 2);
+        for (int i = 0; i < kStages; ++i) mbar_init(&t.full[i], 32), mbar_init(&t.empty[i], 2);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&t.s_full[i], 1);
             mbar_init(&t.p_full[i][0], 4);
@@ -274,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&t.piece_full[i], 1);
             mbar_init(&t.piece_empty[i], 4 + 2 + 8);  // the loads, the issuers, the softmax warps
         }
-        for (int i = 0; i < kLists; ++i) mbar_init(&t.lists.full[i], 1), mbar_init(&t.lists.empty[i], 4 + 2 + 8);
+        for (int i = 0; i < kLists; ++i) mbar_init(&t.lists.full[i], 1), mbar_init(&t.lists.empty[i], 2 + 8);  // the loads of K and of V, the softmax warps
         mbar_init(&t.drained, 2);
         mbar_init(&t.never, 1);
         t.stop.given_up = 0;
@@ -295,7 +308,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
         if (warp >= 4) {
             // ---- loads ----
-            uint32_t c = 0, l = 0, loaded_q = 0;  // ring places filled, lists, Q loads
+            const uint32_t mine = warp - 4;
+            uint32_t c = 0, l = 0, loaded_q = 0;  // ring places and lists so far, Q loads
+            uint32_t loaded = 0;                  // one behind the last place that this warp has filled
             bool ok = true;
             auto release = [&](uint32_t list) {
                 __syncwarp();
@@ -326,36 +341,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ended = t.lists.meta[at].last;
                         if (t.lists.meta[at].n)
                             ++n;
-                        else
+                        else if (mine < 2)        // (as the two loads of a list would)
                             release(l);
                     }
                     return i < n;
                 };
-                // place after place of the ring
+                // every kStages-th place of the ring: a stage of it is this warp's
 #pragma unroll 1
-                for (int p = 0; ok; ++p) {
+                for (int p = (mine - c) % kStages; ok; p += kStages) {
                     int i = w.two ? (p + 1) / 2 : p / 4 * 2 + (p & 1);
                     bool v = w.two ? p > 0 && !(p & 1) : (p & 2) != 0, last = false;
                     if (w.two && v) i -= 1;
-                    const bool real = there_is(i);
-                    if (!real && !(p & 1)) break;
-                    if (!real && w.two) i -= 1, v = last = true;
-                    const uint32_t st = c % kStages, list = (l + i) % kLists;
-                    if (!(ok = ok && wait_short(&t.empty[st], (c / kStages & 1) ^ 1u, stop, a.err))) break;
-                    if (real || w.two) {
-                        load_rows<D>(v ? &map_v : &map_k, v ? a.v : a.k, v ? a.v_bytes : a.k_bytes, g * D, t.lists.token + list * kTile,
-                                     t.lists.meta[list].runs, ring + st * C::kBytes, &t.full[st], warp - 4, lane);
-                        if (v) release(l + i);
-                    } else {
-                        mbar_arrive(&t.full[st]);
+                    bool real = there_is(i);
+                    if (w.two && v && !there_is(i + 1)) break;  // V of the last list is elsewhere
+                    if (!real) {
+                        if (!(p & 1) || !(w.two ? i == n : i - 1 < n)) break;
+                        last = true;              // V of the last list, right behind its K; or a place without a list
+                        if (w.two) i -= 1, v = real = true;
                     }
-                    ++c;
+                    const uint32_t at = c + p, list = (l + i) % kLists;
+                    if (!(ok = ok && wait_short(&t.empty[mine], (at / kStages & 1) ^ 1u, stop, a.err))) break;
+                    if (real) {
+                        load_rows<D>(v ? &map_v : &map_k, v ? a.v : a.k, v ? a.v_bytes : a.k_bytes, g * D, t.lists.token + list * kTile,
+                                     t.lists.meta[list].runs, ring + mine * C::kBytes, &t.full[mine], lane);
+                        release(l + i);
+                    } else {
+                        mbar_arrive(&t.full[mine]);
+                    }
+                    loaded = at + 1;
                     if (last) break;
                 }
+                there_is(INT_MAX);                // (warps see every list)
+                c += places(w.two, n);
                 l += max(n, 1);
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
-            for (uint32_t at = c > kStages ? c - kStages : 0; at < c; ++at) drain_phase(&t.full[at % kStages], at / kStages & 1);
+            if (loaded) drain_phase(&t.full[mine], (loaded - 1) / kStages & 1);
             if (warp == 4 && loaded_q) drain_phase(&t.q_full, (loaded_q - 1) & 1);
         } else if (warp == 1 || warp == 2) {
             issue_tiles<D>(t, sq, ring, warp - 1, lane, a.stuck && warp == 1, stop, a.err);
@@ -369,6 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) {
                     t.piece[u & 1] = w;
                     t.odd[u & 1] = INT_MAX;
+                    t.lists.progress[u & 1] = 0;
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&t.piece_full[u & 1]);
@@ -437,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             a.joints[blockIdx.x] = Joint{(int)(tail / quota) - share + 1, w.row, tokens};
                         }
                         publish(w);
-                        ok = ok && make_lists<MAP>(t.lists, a.map, row, l0 * kTile, w.stop, w.pos0, made, lane, stop, a.err, err);
+                        ok = ok && make_lists<MAP>(t.lists, a.map, row, l0 * kTile, w.stop, w.pos0, made, &t.lists.progress[(u - 1) & 1], lane, stop, a.err, err);
                     }
                     at += here;
                 }

@@ -33,6 +33,37 @@ __device__ __forceinline__ bool wait_short(uint64_t* b, uint32_t parity, Stop* s
     return __all_sync(0xffffffffu, wait_lane(b, parity, stop, err));
 }
 
+// wait_lane for four phases at once, whose answers come in the time of one: next to MMAs, which take all of shared memory's
+// bandwidth, an answer takes some hundred cycles.
+__device__ __forceinline__ bool wait_lane4(uint64_t* b0, uint32_t p0, uint64_t* b1, uint32_t p1, uint64_t* b2, uint32_t p2, uint64_t* b3,
+                                           uint32_t p3, Stop* stop, unsigned* err) {
+    uint32_t t0 = 0;
+#pragma unroll 1
+    for (;;) {
+        uint32_t done, now;
+        asm volatile(
+            "{\n .reg .pred p, q, r, s;\n"
+            " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n"
+            " mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4, 20000;\n"
+            " mbarrier.try_wait.parity.shared::cta.b64 r, [%5], %6, 20000;\n"
+            " mbarrier.try_wait.parity.shared::cta.b64 s, [%7], %8, 20000;\n"
+            " and.pred p, p, q;\n and.pred r, r, s;\n and.pred p, p, r;\n selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(done)
+            : "r"(saddr(b0)), "r"(p0), "r"(saddr(b1)), "r"(p1), "r"(saddr(b2)), "r"(p2), "r"(saddr(b3)), "r"(p3)
+            : "memory");
+        if (done) return true;
+        asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(now));
+        now |= 1;
+        if (!t0) t0 = now;
+        if (stop->given_up) return false;
+        if (now - t0 > (uint32_t)stop->limit_ns) {
+            stop->given_up = 1;
+            atomicOr(err, (unsigned)KVSEL_DEV_TIMEOUT);
+            return false;
+        }
+    }
+}
+
 __device__ __forceinline__ int64_t warp_sum(int64_t v) {
 #pragma unroll
     for (int k = 16; k; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
@@ -51,12 +82,13 @@ struct ListMeta {
 
 // A ring of N lists.  token: slot and position, in ascending positions; behind the n-th the slot of the first.
 template <int N>
-struct Lists {
+struct alignas(16) Lists {
     static constexpr int kAhead = 4;    // rounds whose entries are on their way
     int2 token[N * kTile];
     int entry[kAhead * kTile];          // the making warp's own
     ListMeta meta[N];
     uint64_t full[N], empty[N];
+    volatile int progress[2];           // of the piece whose lists are made (by its number's parity): 2 * lists handed out + whether those are all
 };
 
 // Makes the lists of positions [p0, p1) of a session, at least one; pos0: where the first row that will look at them sits.
@@ -67,7 +99,7 @@ struct Lists {
 // rounds ahead of their use.
 template <bool MAP, int N>
 __device__ __forceinline__ bool make_lists(Lists<N>& t, const TokenMap& m, const int32_t* row, int p0, int p1, int pos0, uint32_t& made,
-                                           int lane, Stop* stop, unsigned* err_word, unsigned& err) {
+                                           volatile int* progress, int lane, Stop* stop, unsigned* err_word, unsigned& err) {
     constexpr int kAhead = Lists<N>::kAhead;
     const unsigned below = (1u << lane) - 1;
     uint32_t l = made;                  // the list that tokens go to, and how many it has
@@ -102,6 +134,7 @@ __device__ __forceinline__ bool make_lists(Lists<N>& t, const TokenMap& m, const
         if (lane == 0) {
             t.meta[l % N] = ListMeta{n, n < kTile || list[n - 1].y > pos0, last, list[0].y, runs};
             mbar_arrive(&t.full[l % N]);
+            *progress = 2 * (int)(l - made + (n > 0)) + last;
         }
         ++l;
     };
@@ -180,46 +213,47 @@ inline bool make_query_map(CUtensorMap* map, const void* base, int T, int Hq, in
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 // The rows of a list's 128 slots, D dims from dim x of a slot on, to a tile of blocks of 64 dims in the layout of the 128-byte
-// swizzle; by four warps, warp w of them 32 rows, whose lanes signal `full` (a count of 128) when the rows have landed.  Runs
-// of kRun slots come by TMA, others row by row through cp.async (TMA gathers of four slots took 45 ns each from one thread, 6
-// us for a list's K and V).  Such rows are written through the generic proxy: who has seen `full` fences before MMAs on them.
+// swizzle; by one warp, whose lanes signal `full` (a count of 32) when the rows have landed.  Runs of kRun slots come by TMA,
+// others row by row through cp.async (TMA gathers of four slots took 45 ns each from one thread, 6 us for a list's K and V).
+// Such rows are written through the generic proxy: who has seen `full` fences before MMAs on them.
 template <int D>
 __device__ __forceinline__ void load_rows(const CUtensorMap* map, const __nv_bfloat16* pool, uint32_t stride_bytes, int x, const int2* tokens,
-                                          unsigned runs, const uint8_t* tile, uint64_t* full, int w, int lane) {
+                                          unsigned runs, const uint8_t* tile, uint64_t* full, int lane) {
     constexpr int kChunks = D / 8, kRows = 32 / kChunks;  // 16-byte chunks of a row; rows of one instruction
-    constexpr int kShare = 32;
     const int chunk = lane % kChunks, low = lane / kChunks;
     const char* const from = reinterpret_cast<const char*>(pool + x) + chunk * 16;
-    const uint32_t to = saddr(tile) + (chunk >> 3) * (kTile * 128) + (kShare * w + low) * 128;
+    const uint32_t to = saddr(tile) + (chunk >> 3) * (kTile * 128) + low * 128;
     const uint32_t swizzled = ((chunk & 7) ^ low) << 4;    // of row `low`; of row i + low, i a multiple of kRows: ^ (i & 7) << 4
-    const int slot = tokens[kShare * w + lane].x;
     constexpr unsigned kAll = (1u << kRun / 4) - 1;
+    // the runs, a lane each
+    const bool run = lane < kTile / kRun && (runs >> (lane * (kRun / 4)) & kAll) == kAll;
+    const unsigned by_tma = __ballot_sync(0xffffffffu, run);
+    if (run) {
+        const int first = tokens[lane * kRun].x;
+        const uint32_t dst = saddr(tile) + lane * (kRun * 128);
+        asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(saddr(full)), "r"(kRun * D * 2) : "memory");
+#pragma unroll
+        for (int b = 0; b < D / 64; ++b)
+            asm volatile(
+                "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+                    dst + b * (kTile * 128)),
+                "l"(reinterpret_cast<uint64_t>(map)), "r"(saddr(full)), "r"(x + 64 * b), "r"(first)
+                : "memory");
+    }
+    if (by_tma != (1u << kTile / kRun) - 1) {
 #pragma unroll 1
-    for (int r = 0; r < kShare; r += kRun) {
-        if ((runs >> ((kShare * w + r) / 4) & kAll) == kAll) {
-            const int first = __shfl_sync(0xffffffffu, slot, r);
-            if (lane == 0) {
-                const uint32_t dst = saddr(tile) + (kShare * w + r) * 128;
-                asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(saddr(full)), "r"(kRun * D * 2) : "memory");
+        for (int r = 0; r < kTile; r += 32) {
+            const int slot = tokens[r + lane].x;
 #pragma unroll
-                for (int b = 0; b < D / 64; ++b)
-                    asm volatile(
-                        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
-                        "[%2];" ::"r"(dst + b * (kTile * 128)),
-                        "l"(reinterpret_cast<uint64_t>(map)), "r"(saddr(full)), "r"(x + 64 * b), "r"(first)
-                        : "memory");
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < kRun; i += kRows) {
-                const uint32_t s = __shfl_sync(0xffffffffu, slot, r + i + low);
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + (r + i) * 128 + (swizzled ^ ((i & 7) << 4))),
-                             "l"(from + (uint64_t)s * stride_bytes)
-                             : "memory");
+            for (int i = 0; i < 32; i += kRows) {
+                const uint32_t s = __shfl_sync(0xffffffffu, slot, i + low);
+                if (!(by_tma >> ((r + i) / kRun) & 1))
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + (r + i) * 128 + (swizzled ^ ((i & 7) << 4))),
+                                 "l"(from + (uint64_t)s * stride_bytes)
+                                 : "memory");
             }
         }
     }
-    __syncwarp();
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(saddr(full)) : "memory");
 }
 // Rows that load_rows has written, and zeros written into them, come before the MMAs that follow.
