@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Stop* const stop = &t.stop;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::kK; ++i) mbar_init(&t.k_full[i], 32), mbar_init(&t.k_empty[i], 1);
+        for (int i = 0; i < C::kK; ++i) mbar_init(&t.k_full[i], 128), mbar_init(&t.k_empty[i], 1);
         for (int i = 0; i < C::kQ; ++i) mbar_init(&t.q_full[i], 1), mbar_init(&t.q_empty[i], 1);
         for (int i = 0; i < C::kL; ++i) mbar_init(&t.l_full[i], 1), mbar_init(&t.l_empty[i], 8);
         for (int i = 0; i < 4; ++i) mbar_init(&t.s_full[i >> 1][i & 1], 1), mbar_init(&t.s_empty[i >> 1][i & 1], 4);
@@ -308,9 +308,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (uint32_t at = c > C::kQ ? c - C::kQ : 0; at < c; ++at) drain_phase(&t.q_full[at % C::kQ], at / C::kQ & 1);
     } else if (warp < 8) {
-        // ---- K tiles: a stage of the ring for each of three warps (a warp sees every phase of its barriers) ----
-        static_assert(C::kK <= 4, "a warp for each");
-        uint32_t c = 0, mine = warp - 4, loaded = 0;  // tiles so far; one behind the last that this warp has loaded
+        // ---- K tiles, a quarter of each ----
+        uint32_t c = 0;
         typename C::Piece w;
         for (uint32_t u = 0; ok && next_piece(u, w, false); ++u) {
             Item it;
@@ -321,18 +320,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                     for (int x = 0; ok && x < it.nl; ++x, ++c) {
                         const uint32_t st = c % C::kK, at = (l + x) % kLists;
-                        if (st != mine) continue;
                         if (!(ok = wait_short(&t.k_empty[st], (c / C::kK & 1) ^ 1, stop, a.err))) break;
-                        load_rows<D>(&map_k, a.k, a.k_bytes, g * D, t.lists.token + at * kTile, t.lists.meta[at].runs,
-                                     sk + st * C::kBytes, &t.k_full[st], lane);
-                        loaded = c + 1;
+                        load_rows<D, 4>(&map_k, a.k, a.k_bytes, g * D, t.lists.token + at * kTile, t.lists.meta[at].runs,
+                                        sk + st * C::kBytes, &t.k_full[st], warp - 4, lane);
                     }
                 for (int x = 0; ok && x < it.nl; ++x) release(l + x);
                 l += it.nl;
             } while (ok && !it.last);
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
-        if (loaded) drain_phase(&t.k_full[(loaded - 1) % C::kK], (loaded - 1) / C::kK & 1);
+        for (uint32_t at = c > C::kK ? c - C::kK : 0; at < c; ++at) drain_phase(&t.k_full[at % C::kK], at / C::kK & 1);
     } else {
         // ---- sums: a key per thread ----
         asm volatile("griddepcontrol.wait;" ::: "memory");  // the score has been copied

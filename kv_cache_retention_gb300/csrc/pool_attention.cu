@@ -139,19 +139,19 @@ __device__ __forceinline__ void issue_tiles(typename Cfg<D>::Tail& t, const uint
         int n = 0;                                // lists of the piece that are known of
         bool ended = false;
         auto there_is = [&](int i) {              // list i; looks no more often than it has to
-            uint32_t t0 = 0;
+            if (ended || n > i) return i < n;
+            uint32_t t0 = 0, tries = 0;
 #pragma unroll 1
-            while (ok && !ended && n <= i) {
+            for (;;) {
                 const int p = t.lists.progress[u & 1];
                 n = p >> 1;
                 ended = p & 1;
                 if (ended || n > i) break;
-                uint32_t now;
-                asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(now));
-                now |= 1;
-                if (!t0) t0 = now;
-                // (whoever makes the lists gives up at the same limit, and says so)
-                if (stop->given_up || now - t0 > (uint32_t)stop->limit_ns) stop->given_up = 1, atomicOr(err, (unsigned)KVSEL_DEV_TIMEOUT), ok = false;
+                __nanosleep(100);
+                if (gives_up(tries, t0, stop, err)) {
+                    ok = false;
+                    break;
+                }
             }
             ok = __all_sync(0xffffffffu, ok);
             n = __shfl_sync(0xffffffffu, n, 0);
@@ -362,8 +362,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t at = c + p, list = (l + i) % kLists;
                     if (!(ok = ok && wait_short(&t.empty[mine], (at / kStages & 1) ^ 1u, stop, a.err))) break;
                     if (real) {
-                        load_rows<D>(v ? &map_v : &map_k, v ? a.v : a.k, v ? a.v_bytes : a.k_bytes, g * D, t.lists.token + list * kTile,
-                                     t.lists.meta[list].runs, ring + mine * C::kBytes, &t.full[mine], lane);
+                        load_rows<D, 1>(v ? &map_v : &map_k, v ? a.v : a.k, v ? a.v_bytes : a.k_bytes, g * D, t.lists.token + list * kTile,
+                                     t.lists.meta[list].runs, ring + mine * C::kBytes, &t.full[mine], 0, lane);
                         release(l + i);
                     } else {
                         mbar_arrive(&t.full[mine]);

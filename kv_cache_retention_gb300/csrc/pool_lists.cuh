@@ -9,24 +9,27 @@
 
 namespace {
 
-// Bounded waits in few instructions, of a lane and with one answer for the warp's lanes: the kernels of these lists have some twenty, and
-// all their roles' code has to fit the instruction cache (with wait_warp in their places, 1.45 ms and not 1.15 ms for 2048
-// tokens behind 32768).
+// Bounded waits in few instructions, of a lane and with one answer for the warp's lanes: the kernels of these lists have some
+// twenty, and all their roles' code has to fit the instruction cache (with wait_warp in their places, 1.45 ms and not 1.15 ms for
+// 2048 tokens behind 32768).  The clock and the other roles' giving up are looked at once in 64 tries: looked at each time, by
+// all who wait, they took a fifth of the kernel's instructions.
+__device__ __forceinline__ bool gives_up(uint32_t& tries, uint32_t& t0, Stop* stop, unsigned* err) {
+    if (++tries & 63) return false;
+    uint32_t now;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(now));
+    now |= 1;
+    if (!t0) t0 = now;
+    if (stop->given_up) return true;
+    if (now - t0 <= (uint32_t)stop->limit_ns) return false;
+    stop->given_up = 1;
+    atomicOr(err, (unsigned)KVSEL_DEV_TIMEOUT);
+    return true;
+}
 __device__ __forceinline__ bool wait_lane(uint64_t* b, uint32_t parity, Stop* stop, unsigned* err) {
-    uint32_t t0 = 0;
+    uint32_t t0 = 0, tries = 0;
 #pragma unroll 1
-    while (!mbar_try(b, parity)) {
-        uint32_t now;
-        asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(now));
-        now |= 1;
-        if (!t0) t0 = now;
-        if (stop->given_up) return false;
-        if (now - t0 > (uint32_t)stop->limit_ns) {
-            stop->given_up = 1;
-            atomicOr(err, (unsigned)KVSEL_DEV_TIMEOUT);
-            return false;
-        }
-    }
+    while (!mbar_try(b, parity))
+        if (gives_up(tries, t0, stop, err)) return false;
     return true;
 }
 __device__ __forceinline__ bool wait_short(uint64_t* b, uint32_t parity, Stop* stop, unsigned* err) {
@@ -37,10 +40,10 @@ __device__ __forceinline__ bool wait_short(uint64_t* b, uint32_t parity, Stop* s
 // bandwidth, an answer takes some hundred cycles.
 __device__ __forceinline__ bool wait_lane4(uint64_t* b0, uint32_t p0, uint64_t* b1, uint32_t p1, uint64_t* b2, uint32_t p2, uint64_t* b3,
                                            uint32_t p3, Stop* stop, unsigned* err) {
-    uint32_t t0 = 0;
+    uint32_t t0 = 0, tries = 0;
 #pragma unroll 1
     for (;;) {
-        uint32_t done, now;
+        uint32_t done;
         asm volatile(
             "{\n .reg .pred p, q, r, s;\n"
             " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n"
@@ -52,15 +55,7 @@ __device__ __forceinline__ bool wait_lane4(uint64_t* b0, uint32_t p0, uint64_t* 
             : "r"(saddr(b0)), "r"(p0), "r"(saddr(b1)), "r"(p1), "r"(saddr(b2)), "r"(p2), "r"(saddr(b3)), "r"(p3)
             : "memory");
         if (done) return true;
-        asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(now));
-        now |= 1;
-        if (!t0) t0 = now;
-        if (stop->given_up) return false;
-        if (now - t0 > (uint32_t)stop->limit_ns) {
-            stop->given_up = 1;
-            atomicOr(err, (unsigned)KVSEL_DEV_TIMEOUT);
-            return false;
-        }
+        if (gives_up(tries, t0, stop, err)) return false;
     }
 }
 
@@ -213,12 +208,12 @@ inline bool make_query_map(CUtensorMap* map, const void* base, int T, int Hq, in
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 // The rows of a list's 128 slots, D dims from dim x of a slot on, to a tile of blocks of 64 dims in the layout of the 128-byte
-// swizzle; by one warp, whose lanes signal `full` (a count of 32) when the rows have landed.  Runs of kRun slots come by TMA,
-// others row by row through cp.async (TMA gathers of four slots took 45 ns each from one thread, 6 us for a list's K and V).
+// swizzle; by W warps, warp w of them a share, whose lanes signal `full` (a count of 32 W) when the rows have landed.  Runs of
+// kRun slots come by TMA, others row by row through cp.async (TMA gathers of four slots took 45 ns each from one thread, 6 us for a list's K and V).
 // Such rows are written through the generic proxy: who has seen `full` fences before MMAs on them.
-template <int D>
+template <int D, int W>
 __device__ __forceinline__ void load_rows(const CUtensorMap* map, const __nv_bfloat16* pool, uint32_t stride_bytes, int x, const int2* tokens,
-                                          unsigned runs, const uint8_t* tile, uint64_t* full, int lane) {
+                                          unsigned runs, const uint8_t* tile, uint64_t* full, int w, int lane) {
     constexpr int kChunks = D / 8, kRows = 32 / kChunks;  // 16-byte chunks of a row; rows of one instruction
     const int chunk = lane % kChunks, low = lane / kChunks;
     const char* const from = reinterpret_cast<const char*>(pool + x) + chunk * 16;
@@ -228,7 +223,7 @@ __device__ __forceinline__ void load_rows(const CUtensorMap* map, const __nv_bfl
     // the runs, a lane each
     const bool run = lane < kTile / kRun && (runs >> (lane * (kRun / 4)) & kAll) == kAll;
     const unsigned by_tma = __ballot_sync(0xffffffffu, run);
-    if (run) {
+    if (run && (W == 1 || lane / (kTile / kRun / W) == w)) {
         const int first = tokens[lane * kRun].x;
         const uint32_t dst = saddr(tile) + lane * (kRun * 128);
         asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(saddr(full)), "r"(kRun * D * 2) : "memory");
@@ -242,7 +237,7 @@ __device__ __forceinline__ void load_rows(const CUtensorMap* map, const __nv_bfl
     }
     if (by_tma != (1u << kTile / kRun) - 1) {
 #pragma unroll 1
-        for (int r = 0; r < kTile; r += 32) {
+        for (int r = w * (kTile / W); r < (w + 1) * (kTile / W); r += 32) {
             const int slot = tokens[r + lane].x;
 #pragma unroll
             for (int i = 0; i < 32; i += kRows) {
