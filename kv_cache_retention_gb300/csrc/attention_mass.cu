@@ -79,12 +79,12 @@ struct Item {
 template <class Tail>
 __device__ __forceinline__ bool next_item(Tail& t, uint32_t l, Item& it, Stop* stop, unsigned* err, bool& ok) {
     it.n1 = 0;
-    if (!(ok = wait_short(&t.lists.full[l % kLists], l / kLists & 1, stop, err))) return false;
+    if (!(ok = wait_idle(&t.lists.full[l % kLists], l / kLists & 1, stop, err))) return false;
     const ListMeta m = t.lists.meta[l % kLists];
     it.nl = 1, it.n0 = m.n, it.first = m.first, it.last = m.last;
     if (!m.last) {
         ++l;
-        if (!(ok = wait_short(&t.lists.full[l % kLists], l / kLists & 1, stop, err))) return false;
+        if (!(ok = wait_idle(&t.lists.full[l % kLists], l / kLists & 1, stop, err))) return false;
         it.nl = 2, it.n1 = t.lists.meta[l % kLists].n, it.last = t.lists.meta[l % kLists].last;
     }
     return true;
@@ -96,7 +96,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                           const __grid_constant__ CUtensorMap map_k, const MassArgs a) {
     using C = MassCfg<D>;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    // (an offset and not a cast, so that the compiler knows it for shared memory)
+    uint8_t* const smem = smem_raw + (-saddr(smem_raw) & 1023u);
     uint8_t* const sk = smem;                       // [kK][kBytes]
     uint8_t* const sq = smem + C::kK * C::kBytes;   // [kQ][kBytes]
     typename C::Tail& t = *reinterpret_cast<typename C::Tail*>(smem + (C::kK + C::kQ) * C::kBytes);
@@ -138,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&t.lists.empty[list % kLists]);
     };
     auto next_piece = [&](uint32_t u, typename C::Piece& w, bool keep) {
-        if (!(ok = wait_short(&t.piece_full[u & 1], (u >> 1) & 1, stop, a.err))) return false;
+        if (!(ok = wait_idle(&t.piece_full[u & 1], (u >> 1) & 1, stop, a.err))) return false;
         w = t.piece[u & 1];
         __syncwarp();
         if (lane == 0 && !keep) mbar_arrive(&t.piece_empty[u & 1]);
@@ -152,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         unsigned err = 0;
         uint32_t u = 0;
         auto publish = [&](const typename C::Piece& w) {
-            if (u >= 2 && !(ok = wait_short(&t.piece_empty[u & 1], ((u >> 1) - 1) & 1, stop, a.err))) return;
+            if (u >= 2 && !(ok = wait_idle(&t.piece_empty[u & 1], ((u >> 1) - 1) & 1, stop, a.err))) return;
             if (lane == 0) t.piece[u & 1] = w;
             __syncwarp();
             if (lane == 0) mbar_arrive(&t.piece_full[u & 1]);
@@ -269,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const float x = real ? __ldg(a.lse + (int64_t)(w.row + tok) * a.Hq + g * a.G + col % a.G) : -INFINITY;
                             v[k] = x == -INFINITY ? -INFINITY : x * -kLog2e;
                         }
-                        if (!(ok = wait_short(&t.l_empty[c % C::kL], (c / C::kL & 1) ^ 1, stop, a.err))) break;
+                        if (!(ok = wait_idle(&t.l_empty[c % C::kL], (c / C::kL & 1) ^ 1, stop, a.err))) break;
 #pragma unroll
                         for (int k = 0; k < kTile / 32; ++k) t.lse[c % C::kL][lane + 32 * k] = v[k];
                         __syncwarp();
@@ -296,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                     for (int i = t0; ok && i < nt; ++i, ++c) {
                         const uint32_t st = c % C::kQ;
-                        if (!(ok = wait_short(&t.q_empty[st], (c / C::kQ & 1) ^ 1, stop, a.err))) break;
+                        if (!(ok = wait_idle(&t.q_empty[st], (c / C::kQ & 1) ^ 1, stop, a.err))) break;
                         if (lane == 0) {
                             mbar_expect_tx(&t.q_full[st], bytes);
                             for (int b = 0; b < D / 64; ++b)
@@ -320,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                     for (int x = 0; ok && x < it.nl; ++x, ++c) {
                         const uint32_t st = c % C::kK, at = (l + x) % kLists;
-                        if (!(ok = wait_short(&t.k_empty[st], (c / C::kK & 1) ^ 1, stop, a.err))) break;
+                        if (!(ok = wait_idle(&t.k_empty[st], (c / C::kK & 1) ^ 1, stop, a.err))) break;
                         load_rows<D, 4>(&map_k, a.k, a.k_bytes, g * D, t.lists.token + at * kTile, t.lists.meta[at].runs,
                                         sk + st * C::kBytes, &t.k_full[st], warp - 4, lane);
                     }

@@ -133,7 +133,7 @@ __device__ __forceinline__ void issue_tiles(typename Cfg<D>::Tail& t, const uint
     bool ok = !stuck || wait_short(&t.never, 0, stop, err);
     const uint32_t ts = uniform(kTmem + kColS + X * kTile), to = uniform(kTmem + kColO + X * D);
     for (uint32_t u = 0; ok; ++u) {
-        if (!(ok = wait_short(&t.piece_full[u & 1], (u >> 1) & 1, stop, err))) break;
+        if (!(ok = wait_idle(&t.piece_full[u & 1], (u >> 1) & 1, stop, err))) break;
         const bool two = t.piece[u & 1].two;
         if (t.piece[u & 1].end) break;
         int n = 0;                                // lists of the piece that are known of
@@ -263,7 +263,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     using C = Cfg<D>;
     constexpr int kStages = C::kStages;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    // (an offset and not a cast, so that the compiler knows it for shared memory)
+    uint8_t* const smem = smem_raw + (-saddr(smem_raw) & 1023u);
     uint8_t* const sq = smem;                     // [2][kBytes]
     uint8_t* const ring = smem + 2 * C::kBytes;   // [kStages][kBytes]
     typename C::Tail& t = *reinterpret_cast<typename C::Tail*>(smem + (2 + kStages) * C::kBytes + C::kOut);
@@ -317,12 +318,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(&t.lists.empty[list % kLists]);
             };
             for (uint32_t u = 0; ok; ++u) {
-                if (!(ok = wait_short(&t.piece_full[u & 1], (u >> 1) & 1, stop, a.err))) break;
+                if (!(ok = wait_idle(&t.piece_full[u & 1], (u >> 1) & 1, stop, a.err))) break;
                 const typename C::Piece w = t.piece[u & 1];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&t.piece_empty[u & 1]);
                 if (w.end) break;
-                if (u && !(ok = wait_short(&t.q_empty, (u - 1) & 1, stop, a.err))) break;
+                if (u && !(ok = wait_idle(&t.q_empty, (u - 1) & 1, stop, a.err))) break;
                 if (warp == 4 && lane == 0) {
                     mbar_expect_tx(&t.q_full, (1 + w.two) * (D / 64) * a.tile_tokens * a.G * 128);
                     for (int x = 0; x < 1 + w.two; ++x)
@@ -337,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                     while (ok && !ended && n <= i) {
                         const uint32_t at = (l + n) % kLists;
-                        if (!(ok = wait_short(&t.lists.full[at], (l + n) / kLists & 1, stop, a.err))) break;
+                        if (!(ok = wait_idle(&t.lists.full[at], (l + n) / kLists & 1, stop, a.err))) break;
                         ended = t.lists.meta[at].last;
                         if (t.lists.meta[at].n)
                             ++n;
@@ -360,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (w.two) i -= 1, v = real = true;
                     }
                     const uint32_t at = c + p, list = (l + i) % kLists;
-                    if (!(ok = ok && wait_short(&t.empty[mine], (at / kStages & 1) ^ 1u, stop, a.err))) break;
+                    if (!(ok = ok && wait_idle(&t.empty[mine], (at / kStages & 1) ^ 1u, stop, a.err))) break;
                     if (real) {
                         load_rows<D, 1>(v ? &map_v : &map_k, v ? a.v : a.k, v ? a.v_bytes : a.k_bytes, g * D, t.lists.token + list * kTile,
                                      t.lists.meta[list].runs, ring + mine * C::kBytes, &t.full[mine], 0, lane);
@@ -386,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             uint32_t u = 0, made = 0;
             auto publish = [&](const typename C::Piece& w) {
-                if (u >= 2 && !(ok = wait_short(&t.piece_empty[u & 1], ((u >> 1) - 1) & 1, stop, a.err))) return;
+                if (u >= 2 && !(ok = wait_idle(&t.piece_empty[u & 1], ((u >> 1) - 1) & 1, stop, a.err))) return;
                 if (lane == 0) {
                     t.piece[u & 1] = w;
                     t.odd[u & 1] = INT_MAX;
@@ -490,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t done = 0, mine = 0, base = 0, l = 0;  // this tile's steps and outputs, ring places and lists so far
     bool ok = true;
     for (uint32_t u = 0; ok; ++u) {
-        if (!(ok = wait_short(&t.piece_full[u & 1], (u >> 1) & 1, stop, a.err))) break;
+        if (!(ok = wait_idle(&t.piece_full[u & 1], (u >> 1) & 1, stop, a.err))) break;
         const typename C::Piece w = t.piece[u & 1];
         __syncwarp();
         if (w.end) break;
@@ -502,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int n = 0, steps = 0;
         bool last = false;
         for (; !last; ++l) {
-            if (!(ok = wait_short(&t.lists.full[l % kLists], l / kLists & 1, stop, a.err))) break;
+            if (!(ok = wait_idle(&t.lists.full[l % kLists], l / kLists & 1, stop, a.err))) break;
             const ListMeta meta = t.lists.meta[l % kLists];
             last = meta.last;
             const int i = n;

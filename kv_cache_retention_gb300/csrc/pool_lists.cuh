@@ -9,6 +9,8 @@
 
 namespace {
 
+constexpr unsigned kIdleNs = 100;
+
 // Bounded waits in few instructions, of a lane and with one answer for the warp's lanes: the kernels of these lists have some
 // twenty, and all their roles' code has to fit the instruction cache (with wait_warp in their places, 1.45 ms and not 1.15 ms for
 // 2048 tokens behind 32768).  The clock and the other roles' giving up are looked at once in 64 tries: looked at each time, by
@@ -31,6 +33,20 @@ __device__ __forceinline__ bool wait_lane(uint64_t* b, uint32_t parity, Stop* st
     while (!mbar_try(b, parity))
         if (gives_up(tries, t0, stop, err)) return false;
     return true;
+}
+// For those that nothing waits for at once: they ask less often, since each try takes its turn at shared memory.
+__device__ __forceinline__ bool wait_idle(uint64_t* b, uint32_t parity, Stop* stop, unsigned* err) {
+    uint32_t t0 = 0, tries = 0;
+    bool ok = true;
+#pragma unroll 1
+    while (!mbar_try(b, parity)) {
+        __nanosleep(kIdleNs);
+        if (gives_up(tries, t0, stop, err)) {
+            ok = false;
+            break;
+        }
+    }
+    return __all_sync(0xffffffffu, ok);
 }
 __device__ __forceinline__ bool wait_short(uint64_t* b, uint32_t parity, Stop* stop, unsigned* err) {
     return __all_sync(0xffffffffu, wait_lane(b, parity, stop, err));
@@ -99,7 +115,7 @@ __device__ __forceinline__ bool make_lists(Lists<N>& t, const TokenMap& m, const
     const unsigned below = (1u << lane) - 1;
     uint32_t l = made;                  // the list that tokens go to, and how many it has
     int n = 0;
-    bool ok = l < N || wait_short(&t.empty[l % N], (l / N - 1) & 1, stop, err_word);
+    bool ok = l < N || wait_idle(&t.empty[l % N], (l / N - 1) & 1, stop, err_word);
     const bool wide = MAP && (reinterpret_cast<uintptr_t>(row) & 15) == 0;
     auto read = [&](int p, int at) {    // (nothing is read behind p1)
         const int j = p + 4 * lane;
@@ -163,7 +179,7 @@ __device__ __forceinline__ bool make_lists(Lists<N>& t, const TokenMap& m, const
             const int rest = n - kTile;
             n = kTile;
             hand_out(0);
-            if (l >= N) ok = wait_short(&t.empty[l % N], (l / N - 1) & 1, stop, err_word);
+            if (l >= N) ok = wait_idle(&t.empty[l % N], (l / N - 1) & 1, stop, err_word);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 if (ok && slot[k] >= 0 && at[k] >= kTile) t.token[l % N * kTile + at[k] - kTile] = make_int2(slot[k], j + k);
