@@ -229,16 +229,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                             ok = wait_lane(&t.s_empty[x][b], (used & 1) ^ 1, stop, a.err) && ok;
                             tc_after();
+                            if (elect_one()) {
 #pragma unroll
-                            for (int j = 0; j < D / 16; ++j) {
-                                const uint32_t off = ((j >> 2) * C::kBlock + (j & 3) * 32) >> 4;
-                                mma_ss(d, k + off, q + off, id, j > 0, lead);
+                                for (int j = 0; j < D / 16; ++j) {
+                                    const uint32_t off = ((j >> 2) * C::kBlock + (j & 3) * 32) >> 4;
+                                    mma_ss_one(d, k + off, q + off, id, j > 0);
+                                }
+                                mma_commit_one(saddr(&t.s_full[x][b]));
+                                if (i == nt - 1) mma_commit_one(saddr(&t.k_empty[st]));
+                                if (x == it.nl - 1) mma_commit_one(saddr(&t.q_empty[cq % C::kQ]));
                             }
-                            mma_commit(saddr(&t.s_full[x][b]), lead);
-                            if (i == nt - 1) mma_commit(saddr(&t.k_empty[st]), lead);
+                            __syncwarp();
                             if (x) ++cs1; else ++cs0;
                         }
-                        mma_commit(saddr(&t.q_empty[cq % C::kQ]), lead);
                         ok = __all_sync(0xffffffffu, ok);
                     }
                 }

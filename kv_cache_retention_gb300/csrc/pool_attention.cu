@@ -188,39 +188,48 @@ __device__ __forceinline__ void issue_tiles(typename Cfg<D>::Tail& t, const uint
                 turns += turn;
                 fence_async();
                 tc_after();
+                if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < kTile / 32; ++k)
-                    mma_ts(to, ts + k * 8, vd + k * (2048 >> 4), idesc(D, true), k > 0 || i != first, lead);
+                    for (int k = 0; k < kTile / 32; ++k)
+                        mma_ts_one(to, ts + k * 8, vd + k * (2048 >> 4), idesc(D, true), k > 0 || i != first);
+                }
+                __syncwarp();
                 ok = wait_lane(&t.p_full[X][1], steps & 1, stop, err) && ok;
                 tc_after();
+                if (elect_one()) {
 #pragma unroll
-                for (int k = kTile / 32; k < kTile / 16; ++k)
-                    mma_ts(to, ts + k * 8, vd + k * (2048 >> 4), idesc(D, true), 1, lead);
+                    for (int k = kTile / 32; k < kTile / 16; ++k)
+                        mma_ts_one(to, ts + k * 8, vd + k * (2048 >> 4), idesc(D, true), 1);
+                }
+                __syncwarp();
                 ++steps;
             } else {
                 if (more) ok = wait_lane(k_full, k_par, stop, err) && ok;
                 fence_async();
                 tc_after();
             }
-            if (more) {                           // writes over the P read above: one thread's MMAs run in the order of issue
+            if (elect_one()) {
+                if (more) {                       // writes over the P read above: one thread's MMAs run in the order of issue
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = ((k >> 2) * C::kBlock + (k & 3) * 32) >> 4;
-                    // the other tile's turn: its issuer is under way while the last of these are issued
-                    if (k == D / 32 && two && product && lead) mbar_arrive(&t.turn[X ^ 1]);
-                    mma_ss(ts, q + off, kd + off, idesc(kTile, false), k > 0, lead);
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t off = ((k >> 2) * C::kBlock + (k & 3) * 32) >> 4;
+                        // the other tile's turn: its issuer is under way while the last of these are issued
+                        if (k == D / 32 && two && product) mbar_arrive(&t.turn[X ^ 1]);
+                        mma_ss_one(ts, q + off, kd + off, idesc(kTile, false), k > 0);
+                    }
+                    mma_commit_one(saddr(&t.s_full[X]));
+                    mma_commit_one(saddr(&t.empty[ak % kStages]));
+                    if (!two) mma_commit_one(saddr(&t.empty[ak % kStages]));  // for the other warp too
+                } else if (product) {
+                    if (two && X == 0) mbar_arrive(&t.turn[1]);
+                    mma_commit_one(saddr(&t.o_done[X]));
                 }
-                mma_commit(saddr(&t.s_full[X]), lead);
-                mma_commit(saddr(&t.empty[ak % kStages]), lead);
-                if (!two) mma_commit(saddr(&t.empty[ak % kStages]), lead);  // for the other warp too
-            } else if (product) {
-                if (two && X == 0 && lead) mbar_arrive(&t.turn[1]);
-                mma_commit(saddr(&t.o_done[X]), lead);
+                if (product) {
+                    mma_commit_one(saddr(&t.empty[av % kStages]));
+                    if (!two) mma_commit_one(saddr(&t.empty[av % kStages]));
+                }
             }
-            if (product) {
-                mma_commit(saddr(&t.empty[av % kStages]), lead);
-                if (!two) mma_commit(saddr(&t.empty[av % kStages]), lead);
-            }
+            __syncwarp();
             ok = __all_sync(0xffffffffu, ok);
             if (!more) break;
         }
