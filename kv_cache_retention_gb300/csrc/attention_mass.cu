@@ -11,8 +11,8 @@
 // as many tokens as fit 128 rows at a time, which both K tiles share: per tile two products of 128 x 128 x D, then 2^x of
 // each element.  Tiles whose tokens lie before the item's keys are left out.
 //
-// 512 threads: warp 0 plans and makes the lists, warp 1 issues the MMAs, warp 2 reads the rows' lse, warp 3 loads Q tiles,
-// warps 4-7 load K tiles, warps 8-11 and 12-15 sum the two lists' weights.  TMEM: two buffers of 128 columns for each list.
+// 512 threads: warp 0 plans and makes the lists, warps 1 and 3 issue the MMAs of the two lists, warp 2 loads Q tiles and reads
+// the rows' lse, warps 4-7 load K tiles, warps 8-11 and 12-15 sum the two lists' weights.  TMEM: two buffers of 128 columns for each list.
 //
 // Shares.  All sessions' chunks of 128 positions, each counted as the row tiles it meets and some for its own loads, are cut
 // into equal contiguous shares, a block each, found from the lengths on the device.  Where there are few chunks, several
@@ -51,7 +51,7 @@ template <int D>
 struct MassCfg {
     static constexpr int kBlock = kTile * 128;             // 128 rows x 64 dims, 128-byte swizzled
     static constexpr int kBytes = D / 64 * kBlock;         // one tile of K or Q
-    static constexpr int kK = 3, kQ = 3, kL = 4;           // tiles of K, of Q; lse rows
+    static constexpr int kK = 4, kQ = 2, kL = 4;           // tiles of K (two for each list of an item), of Q; lse rows
     struct Piece {
         int row, count, pos0, session, end;
     };
@@ -106,13 +106,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     Stop* const stop = &t.stop;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::kK; ++i) mbar_init(&t.k_full[i], 128), mbar_init(&t.k_empty[i], 1);
-        for (int i = 0; i < C::kQ; ++i) mbar_init(&t.q_full[i], 1), mbar_init(&t.q_empty[i], 1);
+        for (int i = 0; i < C::kK; ++i) mbar_init(&t.k_full[i], 64), mbar_init(&t.k_empty[i], 1);
+        for (int i = 0; i < C::kQ; ++i) mbar_init(&t.q_full[i], 1), mbar_init(&t.q_empty[i], 2);
         for (int i = 0; i < C::kL; ++i) mbar_init(&t.l_full[i], 1), mbar_init(&t.l_empty[i], 8);
         for (int i = 0; i < 4; ++i) mbar_init(&t.s_full[i >> 1][i & 1], 1), mbar_init(&t.s_empty[i >> 1][i & 1], 4);
         for (int i = 0; i < 2; ++i) mbar_init(&t.piece_full[i], 1), mbar_init(&t.piece_empty[i], 3 + 4 + 8);
         for (int i = 0; i < kLists; ++i) mbar_init(&t.lists.full[i], 1), mbar_init(&t.lists.empty[i], 3 + 4 + 8);
-        mbar_init(&t.drained, 1);
+        mbar_init(&t.drained, 2);
         mbar_init(&t.never, 1);
         t.stop.given_up = 0;
         t.stop.limit_ns = a.wait_ns;
@@ -196,10 +196,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (ok) publish(typename C::Piece{0, 0, 0, 0, 1});
         if (err) atomicOr(a.err, err);
-    } else if (warp == 1) {
-        // ---- MMAs ----
-        const uint32_t lead = lane == 0;
-        uint32_t ck = 0, cq = 0, cs0 = 0, cs1 = 0;  // K tiles, Q tiles, and the lists' buffers used so far
+    } else if (warp == 1 || warp == 3) {
+        // ---- MMAs: a warp for each list of an item (one warp for both took 638 us for the mass of 2048 tokens) ----
+        const uint32_t x = warp >> 1;
+        uint32_t ck = 0, cq = 0, cs = 0;  // K tiles, Q tiles, and this list's buffers used so far
         ok = !a.stuck || wait_short(&t.never, 0, stop, a.err);
         typename C::Piece w;
         for (uint32_t u = 0; ok && next_piece(u, w, false); ++u) {
@@ -209,52 +209,54 @@ __global__ void __launch_bounds__(kThreads, 1)
             Item it;
             do {
                 if (!next_item(t, l, it, stop, a.err, ok)) break;
-                for (int x = 0; x < it.nl; ++x) release(l + x);
+                for (int y = 0; y < it.nl; ++y) release(l + y);
                 l += it.nl;
                 const int t0 = first_tile(w, it);
+                const bool mine = (int)x < it.nl;
 #pragma unroll 1
-                for (int g = head0; ok && it.n0 && g < a.Hkv; g += a.split, ck += it.nl) {
+                for (int g = head0; ok && it.n0 && g < a.Hkv; g += a.split, ck += 2) {
+                    const uint32_t st = (ck + x) % C::kK;
+                    const uint32_t k = uniform(desc_low(saddr(sk) + st * C::kBytes, 16));
+                    ok = wait_lane(&t.k_full[st], (ck + x) / C::kK & 1, stop, a.err) && ok;
+                    fence_async();
 #pragma unroll 1
                     for (int i = t0; ok && i < nt; ++i, ++cq) {
-                        const uint32_t q = uniform(desc_low(saddr(sq) + cq % C::kQ * C::kBytes, 16));
-                        ok = wait_lane(&t.q_full[cq % C::kQ], cq / C::kQ & 1, stop, a.err) && ok;
-#pragma unroll 1
-                        for (int x = 0; x < it.nl; ++x) {
-                            const uint32_t st = (ck + x) % C::kK, b = (x ? cs1 : cs0) & 1, used = (x ? cs1 : cs0) >> 1;
-                            const uint32_t k = uniform(desc_low(saddr(sk) + st * C::kBytes, 16));
-                            const uint32_t d = uniform(kTmem + x * 256 + b * 128);
-                            if (i == t0) {
-                                ok = wait_lane(&t.k_full[st], (ck + x) / C::kK & 1, stop, a.err) && ok;
-                                fence_async();
-                            }
-                            ok = wait_lane(&t.s_empty[x][b], (used & 1) ^ 1, stop, a.err) && ok;
-                            tc_after();
-                            if (elect_one()) {
+                        const uint32_t b = cs & 1, d = uniform(kTmem + x * 256 + b * 128), sq_at = cq % C::kQ;
+                        const uint32_t q = uniform(desc_low(saddr(sq) + sq_at * C::kBytes, 16));
+                        uint64_t* const qf = &t.q_full[sq_at];
+                        const uint32_t qp = cq / C::kQ & 1;
+                        ok = wait_lane4(qf, qp, mine ? &t.s_empty[x][b] : qf, mine ? ((cs >> 1) & 1) ^ 1 : qp, qf, qp, qf, qp, stop, a.err) && ok;
+                        tc_after();
+                        if (elect_one()) {
+                            if (mine) {
 #pragma unroll
                                 for (int j = 0; j < D / 16; ++j) {
                                     const uint32_t off = ((j >> 2) * C::kBlock + (j & 3) * 32) >> 4;
                                     mma_ss_one(d, k + off, q + off, id, j > 0);
                                 }
                                 mma_commit_one(saddr(&t.s_full[x][b]));
-                                if (i == nt - 1) mma_commit_one(saddr(&t.k_empty[st]));
-                                if (x == it.nl - 1) mma_commit_one(saddr(&t.q_empty[cq % C::kQ]));
                             }
-                            __syncwarp();
-                            if (x) ++cs1; else ++cs0;
+                            mma_commit_one(saddr(&t.q_empty[sq_at]));
+                            if (i == nt - 1) mma_commit_one(saddr(&t.k_empty[st]));
                         }
+                        __syncwarp();
+                        cs += mine;
                         ok = __all_sync(0xffffffffu, ok);
                     }
                 }
             } while (ok && !it.last);
         }
-        mma_commit(saddr(&t.drained), lead);
+        if (elect_one()) mma_commit_one(saddr(&t.drained));
+        __syncwarp();
         drain_phase(&t.drained, 0);
     } else if (warp == 2) {
-        // ---- the rows' lse ----
-        uint32_t c = 0;
+        // ---- Q tiles, and the rows' lse ----
+        uint32_t c = 0, loaded = 0;
         typename C::Piece w;
         for (uint32_t u = 0; ok && next_piece(u, w, false); ++u) {
             const int nt = row_tiles(w);
+            const bool small = w.count <= a.small_tokens;
+            const int bytes = D / 64 * (small ? a.small_tokens : a.tile_tokens) * a.G * 128;
             Item it;
             do {
                 if (!next_item(t, l, it, stop, a.err, ok)) break;
@@ -273,6 +275,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const float x = real ? __ldg(a.lse + (int64_t)(w.row + tok) * a.Hq + g * a.G + col % a.G) : -INFINITY;
                             v[k] = x == -INFINITY ? -INFINITY : x * -kLog2e;
                         }
+                        const uint32_t st = c % C::kQ;
+                        if (!(ok = wait_short(&t.q_empty[st], (c / C::kQ & 1) ^ 1, stop, a.err))) break;
+                        if (lane == 0) {
+                            mbar_expect_tx(&t.q_full[st], bytes);
+                            for (int b = 0; b < D / 64; ++b)
+                                tma_load(small ? &map_small : &map_q, &t.q_full[st], sq + st * C::kBytes + b * C::kBlock, 64 * b, g * a.G,
+                                         w.row + i * a.tile_tokens);
+                        }
+                        loaded = c + 1;
                         if (!(ok = wait_idle(&t.l_empty[c % C::kL], (c / C::kL & 1) ^ 1, stop, a.err))) break;
 #pragma unroll
                         for (int k = 0; k < kTile / 32; ++k) t.lse[c % C::kL][lane + 32 * k] = v[k];
@@ -281,59 +292,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
             } while (ok && !it.last);
         }
-    } else if (warp == 3) {
-        // ---- Q tiles ----
-        uint32_t c = 0;
-        typename C::Piece w;
-        for (uint32_t u = 0; ok && next_piece(u, w, false); ++u) {
-            const int nt = row_tiles(w);
-            const bool small = w.count <= a.small_tokens;
-            const int bytes = D / 64 * (small ? a.small_tokens : a.tile_tokens) * a.G * 128;
-            Item it;
-            do {
-                if (!next_item(t, l, it, stop, a.err, ok)) break;
-                for (int x = 0; x < it.nl; ++x) release(l + x);
-                l += it.nl;
-                const int t0 = first_tile(w, it);
-#pragma unroll 1
-                for (int g = head0; ok && it.n0 && g < a.Hkv; g += a.split)
-#pragma unroll 1
-                    for (int i = t0; ok && i < nt; ++i, ++c) {
-                        const uint32_t st = c % C::kQ;
-                        if (!(ok = wait_idle(&t.q_empty[st], (c / C::kQ & 1) ^ 1, stop, a.err))) break;
-                        if (lane == 0) {
-                            mbar_expect_tx(&t.q_full[st], bytes);
-                            for (int b = 0; b < D / 64; ++b)
-                                tma_load(small ? &map_small : &map_q, &t.q_full[st], sq + st * C::kBytes + b * C::kBlock, 64 * b, g * a.G,
-                                         w.row + i * a.tile_tokens);
-                        }
-                    }
-            } while (ok && !it.last);
-        }
-        for (uint32_t at = c > C::kQ ? c - C::kQ : 0; at < c; ++at) drain_phase(&t.q_full[at % C::kQ], at / C::kQ & 1);
+        for (uint32_t at = loaded > C::kQ ? loaded - C::kQ : 0; at < loaded; ++at) drain_phase(&t.q_full[at % C::kQ], at / C::kQ & 1);
     } else if (warp < 8) {
-        // ---- K tiles, a quarter of each ----
-        uint32_t c = 0;
+        // ---- K tiles: two warps for each list of an item, half a tile each ----
+        static_assert(C::kK == 4, "a stage of the ring is one list's");
+        const int x = (warp - 4) >> 1;
+        uint32_t c = 0, loaded = 0;     // places of the ring so far; one behind the last that this warp has filled
         typename C::Piece w;
         for (uint32_t u = 0; ok && next_piece(u, w, false); ++u) {
             Item it;
             do {
                 if (!next_item(t, l, it, stop, a.err, ok)) break;
+                const uint32_t at = (l + (x < it.nl ? x : 0)) % kLists;
 #pragma unroll 1
-                for (int g = head0; ok && it.n0 && g < a.Hkv; g += a.split)
-#pragma unroll 1
-                    for (int x = 0; ok && x < it.nl; ++x, ++c) {
-                        const uint32_t st = c % C::kK, at = (l + x) % kLists;
-                        if (!(ok = wait_idle(&t.k_empty[st], (c / C::kK & 1) ^ 1, stop, a.err))) break;
-                        load_rows<D, 4>(&map_k, a.k, a.k_bytes, g * D, t.lists.token + at * kTile, t.lists.meta[at].runs,
-                                        sk + st * C::kBytes, &t.k_full[st], warp - 4, lane);
-                    }
-                for (int x = 0; ok && x < it.nl; ++x) release(l + x);
+                for (int g = head0; ok && it.n0 && g < a.Hkv; g += a.split, c += 2) {
+                    const uint32_t st = (c + x) % C::kK;
+                    if (!(ok = wait_short(&t.k_empty[st], ((c + x) / C::kK & 1) ^ 1, stop, a.err))) break;
+                    if (x < it.nl)
+                        load_rows<D, 2>(&map_k, a.k, a.k_bytes, g * D, t.lists.token + at * kTile, t.lists.meta[at].runs,
+                                        sk + st * C::kBytes, &t.k_full[st], warp & 1, lane);
+                    else
+                        mbar_arrive(&t.k_full[st]);  // (there is no second list)
+                    loaded = c + x + 1;
+                }
+                for (int y = 0; ok && y < it.nl; ++y) release(l + y);
                 l += it.nl;
             } while (ok && !it.last);
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
-        for (uint32_t at = c > C::kK ? c - C::kK : 0; at < c; ++at) drain_phase(&t.k_full[at % C::kK], at / C::kK & 1);
+        for (uint32_t at = loaded > 2 ? loaded - 3 : loaded - 1; loaded && at < loaded; at += 2)
+            drain_phase(&t.k_full[at % C::kK], at / C::kK & 1);
     } else {
         // ---- sums: a key per thread ----
         asm volatile("griddepcontrol.wait;" ::: "memory");  // the score has been copied
@@ -350,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int t0 = first_tile(w, it), n = x == 0 ? it.n0 : it.n1;
                 const int pos = t.lists.token[(l + (x < it.nl ? x : 0)) % kLists * kTile + r].y;
                 const int behind = r < n ? pos - w.pos0 : 0;  // the first token that sees the key
-                float2 sum = make_float2(0.f, 0.f);
+                float2 sum = make_float2(0.f, 0.f), sum2 = sum;  // (two, which depend on themselves half as often)
 #pragma unroll 1
                 for (int g = head0; ok && it.n0 && g < a.Hkv; g += a.split)
 #pragma unroll 1
@@ -365,34 +353,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const int lo = min(max(behind - i * a.tile_tokens, 0), a.tile_tokens) * a.G;
                             const int hi = min(a.tile_tokens, w.count - i * a.tile_tokens) * a.G;
                             const bool part = __any_sync(0xffffffffu, lo > 0) || hi < a.tile_tokens * a.G;
-#pragma unroll 1
-                            for (int h = 0; h < hi; h += 64) {
-                                uint32_t s[64];
-                                tmem_ld32(ts + b * 128 + h, s);
-                                tmem_ld32(ts + b * 128 + h + 32, s + 32);
-                                tmem_wait_ld();
-                                if (h + 64 >= hi) {
-                                    tc_before();
-                                    __syncwarp();
-                                    if (lane == 0) mbar_arrive(&t.s_empty[x][b]);
-                                }
-                                const float4* const nl = reinterpret_cast<const float4*>(t.lse[c % C::kL] + h);
-                                if (!part) {
+                            const float* const nl = t.lse[c % C::kL];
+                            uint32_t s0[32], s1[32];
+                            auto taken = [&]() {    // the buffer's columns are all in registers
+                                tc_before();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(&t.s_empty[x][b]);
+                            };
+                            tmem_ld32(ts + b * 128, s0);
+                            tmem_wait_ld();
+                            if (!part) {
+                                // 32 columns at a time, the next ones on their way meanwhile
+                                auto add = [&](const uint32_t* s, int h) {
 #pragma unroll
-                                    for (int k = 0; k < 16; ++k) {
-                                        const float4 m = nl[k];
+                                    for (int k = 0; k < 8; ++k) {
+                                        const float4 m = *reinterpret_cast<const float4*>(nl + h + 4 * k);
                                         const float2 y0 = __ffma2_rn(make_float2(__uint_as_float(s[4 * k]), __uint_as_float(s[4 * k + 1])),
                                                                      sc2, make_float2(m.x, m.y));
                                         const float2 y1 = __ffma2_rn(make_float2(__uint_as_float(s[4 * k + 2]), __uint_as_float(s[4 * k + 3])),
                                                                      sc2, make_float2(m.z, m.w));
                                         sum = __fadd2_rn(sum, make_float2(ex2(y0.x), ex2(y0.y)));
-                                        sum = __fadd2_rn(sum, make_float2(ex2(y1.x), ex2(y1.y)));
+                                        sum2 = __fadd2_rn(sum2, make_float2(ex2(y1.x), ex2(y1.y)));
                                     }
-                                } else {
-                                    const unsigned wide = (unsigned)max(hi - lo, 0);
+                                };
+                                tmem_ld32(ts + b * 128 + 32, s1);
+                                add(s0, 0);
+                                tmem_wait_ld();
+                                tmem_ld32(ts + b * 128 + 64, s0);
+                                add(s1, 32);
+                                tmem_wait_ld();
+                                tmem_ld32(ts + b * 128 + 96, s1);
+                                add(s0, 64);
+                                tmem_wait_ld();
+                                taken();
+                                add(s1, 96);
+                            } else {
+                                const unsigned wide = (unsigned)max(hi - lo, 0);
+#pragma unroll 1
+                                for (int h = 0; h < hi; h += 32) {
+                                    if (h) {
+                                        tmem_ld32(ts + b * 128 + h, s0);
+                                        tmem_wait_ld();
+                                    }
+                                    if (h + 32 >= hi) taken();
 #pragma unroll
-                                    for (int k = 0; k < 64; ++k) {
-                                        const float e = ex2(__uint_as_float(s[k]) * a.scale2 + t.lse[c % C::kL][h + k]);
+                                    for (int k = 0; k < 32; ++k) {
+                                        const float e = ex2(fmaf(__uint_as_float(s0[k]), a.scale2, nl[h + k]));
                                         if ((unsigned)(h + k - lo) < wide) sum.x += e;
                                     }
                                 }
@@ -403,7 +409,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 if (ok && r < n) {
                     float* const to = a.score + (a.part ? head0 * a.part : 0) + w.session * a.score_ld + pos;
-                    *to = a.part ? sum.x + sum.y : *to + (sum.x + sum.y);
+                    const float mass = (sum.x + sum2.x) + (sum.y + sum2.y);
+                    *to = a.part ? mass : *to + mass;
                 }
                 for (int y = 0; ok && y < it.nl; ++y) release(l + y);
                 l += it.nl;
