@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t q = uniform(desc_low(saddr(sq) + sq_at * C::kBytes, 16));
                         uint64_t* const qf = &t.q_full[sq_at];
                         const uint32_t qp = cq / C::kQ & 1;
-                        ok = wait_lane4(qf, qp, mine ? &t.s_empty[x][b] : qf, mine ? ((cs >> 1) & 1) ^ 1 : qp, qf, qp, qf, qp, stop, a.err) && ok;
+                        ok = wait_lane2(qf, qp, mine ? &t.s_empty[x][b] : qf, mine ? ((cs >> 1) & 1) ^ 1 : qp, stop, a.err) && ok;
                         tc_after();
                         if (elect_one()) {
                             if (mine) {
@@ -343,10 +343,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int g = head0; ok && it.n0 && g < a.Hkv; g += a.split)
 #pragma unroll 1
                     for (int i = t0; ok && i < nt; ++i, ++c) {
-                        ok = wait_lane(&t.l_full[c % C::kL], c / C::kL & 1, stop, a.err);
+                        const uint32_t b = cs & 1;
+                        uint64_t* const lf = &t.l_full[c % C::kL];
+                        const uint32_t lp = c / C::kL & 1;
+                        ok = wait_lane2(lf, lp, x < it.nl ? &t.s_full[x][b] : lf, x < it.nl ? (cs >> 1) & 1 : lp, stop, a.err);
                         if (x < it.nl) {
-                            const uint32_t b = cs & 1;
-                            ok = wait_lane(&t.s_full[x][b], (cs >> 1) & 1, stop, a.err) && ok;
                             ++cs;
                             tc_after();
                             // columns that count: of tokens that see the key, and of the session's tokens

@@ -52,8 +52,25 @@ __device__ __forceinline__ bool wait_short(uint64_t* b, uint32_t parity, Stop* s
     return __all_sync(0xffffffffu, wait_lane(b, parity, stop, err));
 }
 
-// wait_lane for four phases at once, whose answers come in the time of one: next to MMAs, which take all of shared memory's
+// wait_lane for two or four phases at once, whose answers come in the time of one: next to MMAs, which take all of shared memory's
 // bandwidth, an answer takes some hundred cycles.
+__device__ __forceinline__ bool wait_lane2(uint64_t* b0, uint32_t p0, uint64_t* b1, uint32_t p1, Stop* stop, unsigned* err) {
+    uint32_t t0 = 0, tries = 0;
+#pragma unroll 1
+    for (;;) {
+        uint32_t done;
+        asm volatile(
+            "{\n .reg .pred p, q;\n"
+            " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n"
+            " mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4, 20000;\n"
+            " and.pred p, p, q;\n selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(done)
+            : "r"(saddr(b0)), "r"(p0), "r"(saddr(b1)), "r"(p1)
+            : "memory");
+        if (done) return true;
+        if (gives_up(tries, t0, stop, err)) return false;
+    }
+}
 __device__ __forceinline__ bool wait_lane4(uint64_t* b0, uint32_t p0, uint64_t* b1, uint32_t p1, uint64_t* b2, uint32_t p2, uint64_t* b3,
                                            uint32_t p3, Stop* stop, unsigned* err) {
     uint32_t t0 = 0, tries = 0;
