@@ -18,7 +18,9 @@ namespace cg = cooperative_groups;
 
 namespace {
 
-constexpr int kThreads = 1024, kWarps = kThreads / 32, kBins = 2048;
+constexpr int kThreads = 512, kWarps = kThreads / 32, kBins = 2048;
+static_assert(kBins == 4 * kThreads && kWarps <= 32, "four bins a thread, a warp for the warps' sums");
+constexpr int kBatch = 8;     // positions of a lane whose loads are in flight at once
 constexpr int kHeld = 32768;  // keys of a block that shared memory holds
 constexpr uint32_t kStays = 0xFFFFFFFFu;  // key of a token that may not leave; no score has it
 
@@ -29,7 +31,6 @@ struct EvictArgs {
     int ld, dead, n_sink, n_recent;
     int32_t *out, *freed, *n_freed;
     int room;              // row length of freed
-    int held;              // keys stay in shared memory
     unsigned* err;
 };
 
@@ -41,7 +42,7 @@ __device__ __forceinline__ uint32_t key_of(float f) {
 }
 
 struct Shared {
-    unsigned hist[2][kBins];   // two, so that a pass clears one while others still read the last
+    alignas(16) unsigned hist[2][kBins];   // two, so that a pass clears one while others still read the last
     unsigned live, may;        // this block's counts
     unsigned less, equal;      // of its keys below the threshold, and at it
     unsigned warp_less[kWarps], warp_equal[kWarps];
@@ -49,7 +50,9 @@ struct Shared {
     unsigned digit, before;    // the digit that holds the wanted rank, and the keys of lower digits
 };
 
-__global__ void __launch_bounds__(kThreads, 2) evict_slots_kernel(const EvictArgs a) {
+// HELD: the block's keys stay in shared memory; else scores and slots are read again for each pass.
+template <bool HELD>
+__global__ void __launch_bounds__(kThreads, 3) evict_slots_kernel(const EvictArgs a) {
     extern __shared__ uint32_t keys[];
     __shared__ Shared sh;
     cg::cluster_group cluster = cg::this_cluster();
@@ -65,29 +68,35 @@ __global__ void __launch_bounds__(kThreads, 2) evict_slots_kernel(const EvictArg
     const int32_t* const in = a.map + (int64_t)s * a.ld;
     int32_t* const out = a.out + (int64_t)s * a.ld;
 
-    auto load_key = [&](int p, bool& live) {
-        live = false;
-        if (p >= n) return kStays;
-        const int slot = in[p];
-        live = slot >= 0 && slot != a.dead;
-        return live && p >= a.n_sink && p < n - a.n_recent ? key_of(score[p]) : kStays;
+    auto key_from = [&](int p, int slot, float value) {  // of a position below n
+        return slot >= 0 && slot != a.dead && p >= a.n_sink && p < n - a.n_recent ? key_of(value) : kStays;
     };
     auto key_at = [&](int p) {
-        bool live;
-        return a.held ? keys[p - (int)base] : load_key(p, live);
+        return HELD ? keys[p - (int)base] : p < n ? key_from(p, in[p], score[p]) : kStays;
     };
     for (int i = tid; i < 2 * kBins; i += kThreads) sh.hist[0][i] = 0;
     if (tid == 0) sh.live = sh.may = 0;
     __syncthreads();
     unsigned n_live = 0, n_may = 0;
-#pragma unroll 4
-    for (int p = w0 + lane; p < w1; p += 32) {
-        bool live;
-        const uint32_t key = load_key(p, live);
-        if (a.held) keys[p - (int)base] = key;
-        n_live += live;
-        n_may += key != kStays;
-        if (key != kStays) atomicAdd(&sh.hist[0][key >> 21], 1u);
+    for (int q = w0 + lane; q < w1; q += 32 * kBatch) {
+        int slot[kBatch];
+        float value[kBatch];            // (of dead tokens too: its load does not wait for the slot's)
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int p = q + 32 * k;
+            slot[k] = p < min(n, w1) ? in[p] : -1;
+            value[k] = p < min(n, w1) ? score[p] : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int p = q + 32 * k;
+            if (p >= w1) break;
+            const uint32_t key = key_from(p, slot[k], value[k]);
+            if (HELD) keys[p - (int)base] = key;
+            n_live += slot[k] >= 0 && slot[k] != a.dead;
+            n_may += key != kStays;
+            if (key != kStays) atomicAdd(&sh.hist[0][key >> 21], 1u);
+        }
     }
     n_live = __reduce_add_sync(0xffffffffu, n_live);
     n_may = __reduce_add_sync(0xffffffffu, n_may);
@@ -111,20 +120,24 @@ __global__ void __launch_bounds__(kThreads, 2) evict_slots_kernel(const EvictArg
             unsigned* const hist = sh.hist[pass & 1];
             if (pass) {
                 const uint32_t above = pass == 1 ? 21 : 10;
+#pragma unroll 4
                 for (int p = w0 + lane; p < w1; p += 32) {
                     const uint32_t key = key_at(p);
                     if (key != kStays && key >> above == threshold >> above) atomicAdd(&hist[(key >> shift) & (bins - 1)], 1u);
                 }
                 cluster.sync();
             }
-            // two bins a thread, summed over the blocks; then the digit that holds the rank
-            unsigned x0 = 0, x1 = 0;
-            if (2 * tid < bins)
+            // four bins a thread, summed over the blocks; then the digit that holds the rank
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (4 * tid < bins) {
+#pragma unroll 4
                 for (int b = 0; b < c; ++b) {
-                    const uint2 v = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(hist, b) + 2 * tid);
-                    x0 += v.x, x1 += v.y;
+                    const uint4 v = *reinterpret_cast<const uint4*>(cluster.map_shared_rank(hist, b) + 4 * tid);
+                    x.x += v.x, x.y += v.y, x.z += v.z, x.w += v.w;
                 }
-            unsigned upto = x0 + x1;
+            }
+            const unsigned all = x.x + x.y + x.z + x.w;
+            unsigned upto = all;
 #pragma unroll
             for (int k = 1; k < 32; k *= 2) {
                 const unsigned y = __shfl_up_sync(0xffffffffu, upto, k);
@@ -132,19 +145,14 @@ __global__ void __launch_bounds__(kThreads, 2) evict_slots_kernel(const EvictArg
             }
             if (lane == 31) sh.scan[warp] = upto;
             __syncthreads();
-            if (warp == 0) {
-                unsigned y = sh.scan[lane];
+            // (every warp adds up the warps before it)
+            unsigned before = __reduce_add_sync(0xffffffffu, lane < warp ? sh.scan[lane] : 0u) + upto - all;
+            const unsigned bin[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                for (int k = 1; k < 32; k *= 2) {
-                    const unsigned z = __shfl_up_sync(0xffffffffu, y, k);
-                    if (lane >= k) y += z;
-                }
-                sh.scan[lane] = y;
+            for (int k = 0; k < 4; ++k) {
+                if (before < rank && rank <= before + bin[k]) sh.digit = 4 * tid + k, sh.before = before;
+                before += bin[k];
             }
-            __syncthreads();
-            const unsigned before = upto - x0 - x1 + (warp ? sh.scan[warp - 1] : 0u);
-            if (before < rank && rank <= before + x0) sh.digit = 2 * tid, sh.before = before;
-            if (before + x0 < rank && rank <= before + x0 + x1) sh.digit = 2 * tid + 1, sh.before = before + x0;
             if (pass == 1)        // (the blocks have read this one: a sync of the cluster lies between)
                 for (int i = tid; i < kBins; i += kThreads) sh.hist[0][i] = 0;
             __syncthreads();
@@ -155,6 +163,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_slots_kernel(const EvictArg
     // ---- who leaves, and where it stands in the list ----
     unsigned w_less = 0, w_equal = 0;
     if (leave)
+#pragma unroll 4
         for (int p = w0 + lane; p < w1; p += 32) {
             const uint32_t key = key_at(p);
             w_less += key < threshold;
@@ -166,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_slots_kernel(const EvictArg
     __syncthreads();
     unsigned less = 0, equal = 0, b_equal = 0;   // before this warp's positions; b_equal: of the whole session
     {
-        const unsigned l = sh.warp_less[lane], e = sh.warp_equal[lane];
+        const unsigned l = lane < kWarps ? sh.warp_less[lane] : 0u, e = lane < kWarps ? sh.warp_equal[lane] : 0u;
         less = __reduce_add_sync(0xffffffffu, lane < warp ? l : 0u);
         equal = __reduce_add_sync(0xffffffffu, lane < warp ? e : 0u);
         const unsigned all_l = __reduce_add_sync(0xffffffffu, l), all_e = __reduce_add_sync(0xffffffffu, e);
@@ -182,21 +191,25 @@ __global__ void __launch_bounds__(kThreads, 2) evict_slots_kernel(const EvictArg
     const unsigned spared = leave ? b_equal - rank : 0u;  // the first `spared` of the keys at the threshold stay
     const unsigned below = (1u << lane) - 1;
     int32_t* const freed = a.freed ? a.freed + (int64_t)s * a.room : nullptr;
-    for (int q = w0; q < w1; q += 32) {
-        const int p = q + lane;
-        const bool in_row = p < w1;
-        const uint32_t key = leave && in_row ? key_at(p) : kStays;
-        const unsigned lm = __ballot_sync(0xffffffffu, leave && key < threshold);
-        const unsigned em = __ballot_sync(0xffffffffu, leave && key == threshold && key != kStays);
-        if (in_row) {
-            const unsigned eq = equal + __popc(em & below);
-            const bool gone = (lm >> lane & 1) || ((em >> lane & 1) && eq >= spared);
-            const int slot = in[p];
-            if (gone && freed) freed[less + __popc(lm & below) + (eq > spared ? eq - spared : 0u)] = slot;
-            out[p] = gone ? a.dead : slot;
+    for (int q = w0; q < w1; q += 32 * kBatch) {
+        int slot[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) slot[k] = q + 32 * k + lane < w1 ? in[q + 32 * k + lane] : 0;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int p = q + 32 * k + lane;
+            const uint32_t key = leave && p < w1 ? key_at(p) : kStays;
+            const unsigned lm = __ballot_sync(0xffffffffu, leave && key < threshold);
+            const unsigned em = __ballot_sync(0xffffffffu, leave && key == threshold && key != kStays);
+            if (p < w1) {
+                const unsigned eq = equal + __popc(em & below);
+                const bool gone = (lm >> lane & 1) || ((em >> lane & 1) && eq >= spared);
+                if (gone && freed) freed[less + __popc(lm & below) + (eq > spared ? eq - spared : 0u)] = slot[k];
+                out[p] = gone ? a.dead : slot[k];
+            }
+            less += __popc(lm);
+            equal += __popc(em);
         }
-        less += __popc(lm);
-        equal += __popc(em);
     }
     if (freed)
         for (int64_t i = (int64_t)leave + (int64_t)r * kThreads + tid; i < a.room; i += (int64_t)c * kThreads) freed[i] = -1;
@@ -221,17 +234,17 @@ extern "C" int kvsel_evict_slots(kvsel_ctx* ctx, const float* score, int64_t sco
     if (!seq_lens || !budget || (ld > 0 && (!score || !slot_map || !slot_out)))
         return kvsel_fail(ctx, KVSEL_ERR_INVALID_ARG, "evict_slots: null pointer");
     if (!(ctx->ready & KVSEL_READY_EVICT)) {
-        const cudaError_t e = cudaFuncSetAttribute(evict_slots_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeld * 4);
+        const cudaError_t e = cudaFuncSetAttribute(evict_slots_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeld * 4);
         if (e != cudaSuccess) return kvsel_cuda_fail(ctx, e, "evict_slots set-up");
         ctx->ready |= KVSEL_READY_EVICT;
     }
-    // A cluster as large as keeps all sessions' blocks on the GPU at once (two an SM) and leaves a thread a position.
+    // A cluster as large as keeps all sessions' blocks on the GPU at once (three an SM) and leaves a thread four positions.
     int c = 1;
-    while (c < 8 && (int64_t)S * c <= ctx->num_sms && ld > c * kThreads) c *= 2;
+    while (c < 8 && 2 * (int64_t)S * c <= 3 * ctx->num_sms && ld > c * 4 * kThreads) c *= 2;
     const int64_t per = (((int64_t)ld + c * kWarps - 1) / (c * kWarps) + 31) & ~31;
-    const int held = per * kWarps <= kHeld;
+    const bool held = per * kWarps <= kHeld;
     const EvictArgs a{score, score_ld, seq_lens, budget, slot_map, ld, dead_slot, n_sink, n_recent, slot_out, freed, n_freed,
-                      freed ? ld_freed : INT_MAX, held, ctx->dev_err};
+                      freed ? ld_freed : INT_MAX, ctx->dev_err};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)S * c);
     cfg.blockDim = dim3(kThreads);
@@ -243,6 +256,6 @@ extern "C" int kvsel_evict_slots(kvsel_ctx* ctx, const float* score, int64_t sco
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, evict_slots_kernel, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, held ? evict_slots_kernel<true> : evict_slots_kernel<false>, a);
     return e == cudaSuccess ? KVSEL_OK : kvsel_cuda_fail(ctx, e, "evict_slots launch");
 }
