@@ -33,7 +33,7 @@ SOURCES = [
     "attention_mass.cu",
     "evict_slots.cu",
 ]
-HEADERS = ["kvsel_internal.h", "kv4_format.cuh", "pool_tokens.cuh", "pool_lists.cuh", "tc_common.cuh", os.path.join("..", "..", "include", "kvsel.h")]
+HEADERS = ["kvsel_internal.h", "kv4_format.cuh", "pool_tokens.cuh", "pool_lists.cuh", "pool_attention.cuh", "pool_decode.cuh", "tc_common.cuh", os.path.join("..", "..", "include", "kvsel.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xptxas", "-v"]

@@ -309,7 +309,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t st = (c + x) % C::kK;
                     if (!(ok = wait_short(&t.k_empty[st], ((c + x) / C::kK & 1) ^ 1, stop, a.err))) break;
                     if (x < it.nl)
-                        load_rows<D, 2>(&map_k, a.k, a.k_bytes, g * D, t.lists.token + at * kTile, t.lists.meta[at].runs,
+                        load_rows<D, 2>(&map_k, a.k, a.k_bytes, g * D, t.lists.token + at * kTile, t.lists.meta[at].n,
+                                        t.lists.meta[at].runs,
                                         sk + st * C::kBytes, &t.k_full[st], warp & 1, lane);
                     else
                         mbar_arrive(&t.k_full[st]);  // (there is no second list)
@@ -454,7 +455,7 @@ template <int D, bool MAP>
 cudaError_t launch(kvsel_ctx* ctx, const CUtensorMap& mq, const CUtensorMap& ms, const CUtensorMap& mk, const MassArgs& a,
                    const float* before, float* score, int64_t score_ld, cudaStream_t s) {
     auto* kernel = attention_mass_kernel<D, MAP>;
-    constexpr unsigned kBit = KVSEL_READY_MASS << (D / 64 - 1 + 2 * MAP);
+    constexpr uint64_t kBit = (uint64_t)KVSEL_READY_MASS << (D / 64 - 1 + 2 * MAP);
     if (!(ctx->ready & kBit)) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)MassCfg<D>::kSmem);
         if (e != cudaSuccess) return e;

@@ -52,15 +52,16 @@ struct kvsel_ctx {
     void* kv4_partials = nullptr;
     // The same of kvsel_pool_attention.
     void* pool_parts = nullptr;
-    unsigned ready = 0;  // kernels whose attributes are set on this context's device, a bit each
+    uint64_t ready = 0;  // kernels whose attributes are set on this context's device, a bit each
     char err[512] = {0};
 };
 
 // Bits of kvsel_ctx::ready of the calls over the page pools (the ones below 20 are prompt_attention's and kv4_attention's).
-enum kvsel_ready : unsigned {
+enum kvsel_ready : uint64_t {
     KVSEL_READY_EVICT = 1u << 20,
     KVSEL_READY_POOL = 1u << 21,  // and three more: D = 64 and 128, block tables and slot maps
     KVSEL_READY_MASS = 1u << 25,  // likewise
+    KVSEL_READY_DECODE = 1ull << 32,  // likewise, of the kernel for few new tokens
 };
 
 // Device error-word bits.

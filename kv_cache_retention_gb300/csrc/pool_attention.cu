@@ -37,12 +37,11 @@
 // and MMAs, frees TMEM and returns.
 #include <limits.h>
 
-#include "pool_lists.cuh"
+#include "pool_decode.cuh"
 
 namespace {
 
 constexpr int kThreads = 512;
-constexpr float kSlack = 8.f;           // how far (log2) a row's maximum may pass its reference
 // Registers per thread: at launch, then after the first warpgroup's setmaxnreg.dec and the softmax warpgroups' .inc.  An
 // .inc beyond the launch's registers would wait forever; the launcher checks the compiled count.
 constexpr int kRegsLaunch = 128, kRegsCtl = 72, kRegsSoft = 184;
@@ -50,36 +49,6 @@ static_assert(2 * kRegsCtl + 2 * kRegsSoft <= 4 * kRegsLaunch && kRegsLaunch * k
 constexpr int kLists = 8;
 constexpr int kStart = 4;               // lists that the start of a unit counts as when shares are cut
 constexpr int kLeast = 4;               // lists that a share has at least, so cut
-
-// All of TMEM is allocated, so its base is column 0.
-constexpr uint32_t kTmem = 0;
-constexpr int kColS = 0, kColO = 256, kTmemCols = 512;
-
-// What a block has of a unit that others share: O as [D/4][128 rows] of four dims, then references and sums; per tile.
-constexpr int kPartTile = kTile * (128 + 2), kPart = 2 * kPartTile;
-
-// A unit that several shares have a part of, kept with the block that has its first keys; sharers 0: none.
-struct Joint {
-    int sharers, row, tokens;           // row, tokens: its first token in q, and how many
-};
-
-struct PoolArgs {
-    const int32_t *cu, *lens;
-    int S, T, Hq, Hkv, G;
-    int tile_tokens;                    // tokens of a tile
-    const __nv_bfloat16 *k, *v;
-    uint32_t k_bytes, v_bytes;          // from a slot's rows to the next one's
-    TokenMap map;
-    float scale2;                       // scale * log2(e)
-    __nv_bfloat16* out;
-    float* lse;
-    unsigned* err;
-    int shares;
-    float* parts;                       // [blocks][2]: of a unit that began before the share, and of one that goes on behind it
-    Joint* joints;                      // [blocks]
-    uint64_t wait_ns;                   // how long a wait goes on
-    int stuck;                          // tile 0's issuer waits for what never comes (test entry)
-};
 
 template <int D>
 struct Cfg {
@@ -373,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!(ok = ok && wait_idle(&t.empty[mine], (at / kStages & 1) ^ 1u, stop, a.err))) break;
                     if (real) {
                         load_rows<D, 1>(v ? &map_v : &map_k, v ? a.v : a.k, v ? a.v_bytes : a.k_bytes, g * D, t.lists.token + list * kTile,
-                                     t.lists.meta[list].runs, ring + mine * C::kBytes, &t.full[mine], 0, lane);
+                                     t.lists.meta[list].n, t.lists.meta[list].runs, ring + mine * C::kBytes, &t.full[mine], 0, lane);
                         release(l + i);
                     } else {
                         mbar_arrive(&t.full[mine]);
@@ -409,7 +378,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int unit = 2 * a.tile_tokens;
             int64_t total = 0;
             for (int s = lane; s < a.S; s += 32) {
-                const Session x = session_at(a.cu, a.lens, a.T, a.map.reach, s);
+                Session x = session_at(a.cu, a.lens, a.T, a.map.reach, s);
+                if (x.count <= a.few) x.count = 0;  // (another kernel's)
                 total += cut_of(x, unit).before(units_of(x, unit));
                 if (blockIdx.x == 0) err |= session_errors(a.cu, a.lens, a.T, a.map.reach, s);
             }
@@ -421,6 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int s0 = 0; ok && s0 < a.S && at < to; s0 += 32) {
                 Session mine{0, 0, 0};
                 if (s0 + lane < a.S) mine = session_at(a.cu, a.lens, a.T, a.map.reach, s0 + lane);
+                if (mine.count <= a.few) mine.count = 0;
                 const int64_t size = cut_of(mine, unit).before(units_of(mine, unit));
                 const int64_t all = warp_sum(size);
                 if (at + all <= from) {           // 32 sessions before the share
@@ -519,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             n += meta.n != 0;
             if (meta.n && (w.two || (i & 1) == x)) {
                 if (!(ok = wait_short(&t.s_full[x], done & 1, stop, a.err))) break;
-                if (meta.masked) {
+                if (meta.causal) {
                     // NaN and infinities of V to zero; both tiles look at all of it (a value may be set twice)
                     const uint32_t at = base + at_v(w.two, i, last), st = at % kStages;
                     if (!(ok = wait_short(&t.full[st], at / kStages & 1, stop, a.err))) break;
@@ -553,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int b = 0; b < 4; ++b) tmem_ld32(ts + 32 * b, s + 32 * b);
                     tmem_wait_ld();
-                    if (meta.masked) {
+                    if (meta.causal || meta.n < kTile) {
                         // the row sees the list's tokens up to its own position: those before place `seen`
                         const int2* const list = t.lists.token + l % kLists * kTile;
                         int seen = 0;
@@ -780,7 +751,7 @@ template <int D, bool MAP>
 cudaError_t launch(kvsel_ctx* ctx, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const PoolArgs& a,
                    cudaStream_t s) {
     auto* kernel = pool_attention_kernel<D, MAP>;
-    constexpr unsigned kBit = KVSEL_READY_POOL << (D / 64 - 1 + 2 * MAP);
+    constexpr uint64_t kBit = (uint64_t)KVSEL_READY_POOL << (D / 64 - 1 + 2 * MAP);
     if (!(ctx->ready & kBit)) {
         cudaFuncAttributes fa;
         cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
@@ -823,28 +794,47 @@ int attention_call(kvsel_ctx* ctx, const void* q, int64_t q_stride, const int32_
     if ((reinterpret_cast<uintptr_t>(q) & 15u) || (reinterpret_cast<uintptr_t>(out) & 15u))
         return kvsel_fail(ctx, KVSEL_ERR_ALIGN, "pool_attention: q and out must be 16-byte aligned");
     const int G = Hq / Hkv, tile_tokens = kTile / G;
-    CUtensorMap mq, mk, mv;
+    const int most = decode::kRows / G;  // tokens that the rows of few hold
+    // Sessions of few tokens go to the kernel for them where they may be most of the batch's; its launch is not worth it for
+    // chunks, whose own kernel takes them too.  Where all tokens together are few, that one is not needed.
+    const bool few = most > 0 && (int64_t)T * G <= 2 * (int64_t)decode::kRows * S, all_few = T <= most;
+    CUtensorMap mq, ms, mk, mv;
     if (!make_query_map(&mq, q, T, Hq, D, q_stride, G, tile_tokens) ||
+        (few && !make_query_map(&ms, q, T, Hq, D, q_stride, G, most)) ||
         (P > 0 && (!make_pool_map(&mk, k_pool, P * page, Hkv, D, k_stride) ||
                    !make_pool_map(&mv, v_pool, P * page, Hkv, D, v_stride))))
         return kvsel_fail(ctx, KVSEL_ERR_CUDA, "pool_attention: tensor map encoding failed");
     if (P == 0) mk = mv = mq;           // nothing is live
+    const int pairs = (Hkv + decode::kHeads - 1) / decode::kHeads;
     float* const parts = (float*)ctx->pool_parts;
-    const PoolArgs a{cu_new, seq_lens, S, T, Hq, Hkv, G, tile_tokens, (const __nv_bfloat16*)k_pool,
-                     (const __nv_bfloat16*)v_pool, (uint32_t)(k_stride * 2), (uint32_t)(v_stride * 2), map, scale * kLog2e,
-                     (__nv_bfloat16*)out, lse, ctx->dev_err, Hkv < ctx->num_sms ? ctx->num_sms / Hkv : 1, parts,
-                     (Joint*)(parts + (size_t)ctx->num_sms * 2 * kPart), wait_ns, stuck};
+    float* const few_parts = parts + (size_t)ctx->num_sms * 2 * kPart;
+    Joint* const joints = (Joint*)(few_parts + (size_t)ctx->num_sms * 2 * decode::kPart);
+    PoolArgs a{cu_new, seq_lens, S, T, Hq, Hkv, G, tile_tokens, few ? most : 0, (const __nv_bfloat16*)k_pool,
+               (const __nv_bfloat16*)v_pool, (uint32_t)(k_stride * 2), (uint32_t)(v_stride * 2), map, scale * kLog2e,
+               (__nv_bfloat16*)out, lse, ctx->dev_err, pairs < ctx->num_sms ? ctx->num_sms / pairs : 1, few_parts, joints,
+               wait_ns, stuck};
     const cudaStream_t st = (cudaStream_t)stream;
-    const cudaError_t e = slot_map ? D == 64 ? launch<64, true>(ctx, mq, mk, mv, a, st) : launch<128, true>(ctx, mq, mk, mv, a, st)
-                          : D == 64 ? launch<64, false>(ctx, mq, mk, mv, a, st) : launch<128, false>(ctx, mq, mk, mv, a, st);
+    cudaError_t e = cudaSuccess;
+    auto run = [&](auto call, const CUtensorMap& m) { e = call(ctx, m, mk, mv, a, st); };
+    if (few)
+        slot_map ? D == 64 ? run(decode::launch<64, true>, ms) : run(decode::launch<128, true>, ms)
+        : D == 64 ? run(decode::launch<64, false>, ms) : run(decode::launch<128, false>, ms);
+    if (e == cudaSuccess && !(few && all_few)) {
+        a.shares = Hkv < ctx->num_sms ? ctx->num_sms / Hkv : 1;
+        a.parts = parts, a.joints = joints + 65536;
+        slot_map ? D == 64 ? run(launch<64, true>, mq) : run(launch<128, true>, mq)
+        : D == 64 ? run(launch<64, false>, mq) : run(launch<128, false>, mq);
+    }
     return e == cudaSuccess ? KVSEL_OK : kvsel_cuda_fail(ctx, e, "pool_attention launch");
 }
 
 }  // namespace
 
 // Partial results and joints of the blocks: as many as there are SMs, or kv heads where those are more (their blocks have
-// whole units and only clear their joints).
-size_t pool_parts_bytes(int num_sms) { return (size_t)num_sms * 2 * kPart * sizeof(float) + (size_t)65536 * sizeof(Joint); }
+// whole units and only clear their joints); of this kernel and of the one for few tokens.
+size_t pool_parts_bytes(int num_sms) {
+    return (size_t)num_sms * 2 * (kPart + decode::kPart) * sizeof(float) + (size_t)2 * 65536 * sizeof(Joint);
+}
 
 extern "C" int kvsel_pool_attention(kvsel_ctx* ctx, const void* q, int64_t q_stride, const int32_t* cu_new, int S, int T,
                                     int Hq, int Hkv, int D, const void* k_pool, const void* v_pool, int64_t k_stride,

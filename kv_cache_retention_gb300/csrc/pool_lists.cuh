@@ -102,7 +102,7 @@ constexpr int kRun = 16;            // slots that one TMA load brings where they
 
 struct ListMeta {
     int n;          // tokens; 0 only where a piece has none
-    int masked;     // not all of them are seen by every row, or there are fewer than 128
+    int causal;     // not all of them are seen by every row
     int last;       // of its piece
     int first;      // position of its first token
     unsigned runs;  // of each four tokens, whether they go on a run of slots that starts with their kRun; a bit each
@@ -160,7 +160,7 @@ __device__ __forceinline__ bool make_lists(Lists<N>& t, const TokenMap& m, const
         const bool run = s01.x == first + off && s01.z == s01.x + 1 && s23.x == s01.x + 2 && s23.z == s01.x + 3;
         const unsigned runs = __ballot_sync(0xffffffffu, run);
         if (lane == 0) {
-            t.meta[l % N] = ListMeta{n, n < kTile || list[n - 1].y > pos0, last, list[0].y, runs};
+            t.meta[l % N] = ListMeta{n, n > 0 && list[n - 1].y > pos0, last, list[0].y, runs};
             mbar_arrive(&t.full[l % N]);
             *progress = 2 * (int)(l - made + (n > 0)) + last;
         }
@@ -243,10 +243,11 @@ inline bool make_query_map(CUtensorMap* map, const void* base, int T, int Hq, in
 // The rows of a list's 128 slots, D dims from dim x of a slot on, to a tile of blocks of 64 dims in the layout of the 128-byte
 // swizzle; by W warps, warp w of them a share, whose lanes signal `full` (a count of 32 W) when the rows have landed.  Runs of
 // kRun slots come by TMA, others row by row through cp.async (TMA gathers of four slots took 45 ns each from one thread, 6 us for a list's K and V).
-// Such rows are written through the generic proxy: who has seen `full` fences before MMAs on them.
+// Such rows are written through the generic proxy: who has seen `full` fences before MMAs on them.  Rows behind the n-th token
+// are zeros.
 template <int D, int W>
 __device__ __forceinline__ void load_rows(const CUtensorMap* map, const __nv_bfloat16* pool, uint32_t stride_bytes, int x, const int2* tokens,
-                                          unsigned runs, const uint8_t* tile, uint64_t* full, int w, int lane) {
+                                          int n, unsigned runs, const uint8_t* tile, uint64_t* full, int w, int lane) {
     constexpr int kChunks = D / 8, kRows = 32 / kChunks;  // 16-byte chunks of a row; rows of one instruction
     const int chunk = lane % kChunks, low = lane / kChunks;
     const char* const from = reinterpret_cast<const char*>(pool + x) + chunk * 16;
@@ -276,8 +277,8 @@ __device__ __forceinline__ void load_rows(const CUtensorMap* map, const __nv_bfl
             for (int i = 0; i < 32; i += kRows) {
                 const uint32_t s = __shfl_sync(0xffffffffu, slot, i + low);
                 if (!(by_tma >> ((r + i) / kRun) & 1))
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + (r + i) * 128 + (swizzled ^ ((i & 7) << 4))),
-                                 "l"(from + (uint64_t)s * stride_bytes)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + (r + i) * 128 + (swizzled ^ ((i & 7) << 4))),
+                                 "l"(from + (uint64_t)s * stride_bytes), "r"(r + i + low < n ? 16 : 0)
                                  : "memory");
             }
         }
