@@ -23,8 +23,8 @@ constexpr int kRegsLaunch = 168, kRegsCtl = 120, kRegsSoft = 240;
 static_assert(2 * kRegsCtl + kRegsSoft <= 3 * kRegsLaunch && kRegsLaunch * kThreads <= 65536, "register split");
 constexpr int kRows = 32, kHeads = 2;
 constexpr int kLists = 8;
-constexpr int kStart = 4;               // lists that the start of a session counts as when shares are cut
-constexpr int kLeast = 2;               // lists that a share has at least, so cut
+constexpr int kStart = 2;               // lists that the start of a session counts as when shares are cut
+constexpr int kLeast = 1;               // lists that a share has at least, so cut
 
 // What a block has of a session that others share: O as [D/4][32 rows] of four dims, then references and sums; per head.
 constexpr int kPartHead = kRows * (128 + 2), kPart = kHeads * kPartHead;
@@ -105,8 +105,7 @@ __device__ __forceinline__ void issue_tiles(typename Cfg<D>::Tail& t, const uint
                 const uint32_t kd = uniform(desc_low(saddr(ring) + (X * C::kStages + sk) * C::kBytes, 16));
                 if (product) {
                     if (u && i == 0) ok = wait_lane(&t.o_free[X][(u - 1) & 1], ((u - 1) >> 1) & 1, stop, err) && ok;
-                    ok = wait_lane4(&t.full[X][sv], phase_of(pv), &t.p_full[X][0], steps & 1, &t.p_full[X][0], steps & 1,
-                                    &t.p_full[X][0], steps & 1, stop, err) && ok;
+                    ok = wait_lane2(&t.full[X][sv], phase_of(pv), &t.p_full[X][0], steps & 1, stop, err) && ok;
                     fence_async();
                     tc_after();
                     if (elect_one()) {
@@ -115,24 +114,25 @@ __device__ __forceinline__ void issue_tiles(typename Cfg<D>::Tail& t, const uint
                             mma_ts_one(to, ts + k * 8, vd + k * (2048 >> 4), idesc(D, true), k > 0 || i > 0);
                     }
                     __syncwarp();
-                    ok = wait_lane2(&t.p_full[X][1], steps & 1, more ? &t.full[X][sk] : &t.p_full[X][1], more ? phase_of(pk) : steps & 1,
-                                    stop, err) && ok;
-                    fence_async();
+                    ok = wait_lane(&t.p_full[X][1], steps & 1, stop, err) && ok;
                     tc_after();
                     if (elect_one()) {
 #pragma unroll
                         for (int k = kTile / 32; k < kTile / 16; ++k)
                             mma_ts_one(to, ts + k * 8, vd + k * (2048 >> 4), idesc(D, true), 1);
+                        // (V's stage takes the K tile after next: it is not to wait for the next one's arrival)
+                        mma_commit_one(saddr(&t.empty[X][sv]));
                     }
                     __syncwarp();
                     ++steps;
-                } else {
-                    if (more) ok = wait_lane(&t.full[X][sk], phase_of(pk), stop, err) && ok;
+                }
+                if (more) {             // S writes over the P read above: one thread's MMAs run in the order of issue
+                    ok = wait_lane(&t.full[X][sk], phase_of(pk), stop, err) && ok;
                     fence_async();
                     tc_after();
                 }
                 if (elect_one()) {
-                    if (more) {         // writes over the P read above: one thread's MMAs run in the order of issue
+                    if (more) {
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k) {
                             const uint32_t in = (k & 3) * 32;
@@ -145,7 +145,6 @@ __device__ __forceinline__ void issue_tiles(typename Cfg<D>::Tail& t, const uint
                         if (product) mma_commit_one(saddr(&t.o_done[X]));
                         mma_commit_one(saddr(&t.q_empty));
                     }
-                    if (product) mma_commit_one(saddr(&t.empty[X][sv]));
                 }
                 __syncwarp();
                 ok = __all_sync(0xffffffffu, ok);
@@ -552,41 +551,60 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
 }
 
-// Joins the session whose first keys block blockIdx.x has, for head blockIdx.y of its two: a row per lane, four dims at a time.
+// Joins the session whose first keys block blockIdx.x has: one head's 32 dims a block, a row per lane, every eighth part a
+// warp, so that the parts' loads are on their way together.
 template <int D>
 __global__ void __launch_bounds__(256) pool_decode_join_kernel(const PoolArgs a) {
+    __shared__ float tops[8][kRows], sums[8][kRows];
+    __shared__ float4 os[8][8][kRows];  // [warp][dims][row]
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const Joint u = a.joints[blockIdx.x];
-    const int pairs = (a.Hkv + kHeads - 1) / kHeads, g = (int)(blockIdx.x % pairs) * kHeads + blockIdx.y;
+    const int pairs = (a.Hkv + kHeads - 1) / kHeads, x = blockIdx.y / (D / 32), d0 = blockIdx.y % (D / 32) * 8;
+    const int g = (int)(blockIdx.x % pairs) * kHeads + x;
     if (!u.sharers || g >= a.Hkv) return;
-    const int warp = threadIdx.x >> 5, r = threadIdx.x & 31;
-    auto part = [&](int k) { return a.parts + ((size_t)(blockIdx.x + k * pairs) * 2 + (k == 0)) * kPart + blockIdx.y * kPartHead; };
+    const int warp = threadIdx.x >> 5, r = threadIdx.x & 31, rows = u.tokens * a.G;
+    auto part = [&](int k) { return a.parts + ((size_t)(blockIdx.x + k * pairs) * 2 + (k == 0)) * kPart + x * kPartHead; };
     float top = -3e38f, sum = 0.f;
-#pragma unroll 8
-    for (int k = 0; k < u.sharers; ++k) top = fmaxf(top, part(k)[kRows * 128 + r]);
-    float4 o[D / 32];
+    float4 o[8];
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = 0; k < u.sharers; ++k) {
-        const float* const p = part(k);
-        const float f = ex2(p[kRows * 128 + r] - top);
-        sum += f * p[kRows * 129 + r];
+    for (int c = 0; c < 8; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < rows)
+#pragma unroll 2
+        for (int k = warp; k < u.sharers; k += 8) {
+            const float* const p = part(k);
+            const float ref = p[kRows * 128 + r], l = p[kRows * 129 + r], next = fmaxf(top, ref), f0 = ex2(top - next), f1 = ex2(ref - next);
+            top = next;
+            sum = sum * f0 + l * f1;
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-            const float4 y = reinterpret_cast<const float4*>(p)[(warp + 8 * c) * kRows + r];
-            o[c].x += f * y.x, o[c].y += f * y.y, o[c].z += f * y.z, o[c].w += f * y.w;
+            for (int c = 0; c < 8; ++c) {
+                const float4 y = reinterpret_cast<const float4*>(p)[(d0 + c) * kRows + r];
+                o[c].x = o[c].x * f0 + y.x * f1, o[c].y = o[c].y * f0 + y.y * f1;
+                o[c].z = o[c].z * f0 + y.z * f1, o[c].w = o[c].w * f0 + y.w * f1;
+            }
         }
+    tops[warp][r] = top, sums[warp][r] = sum;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) os[warp][c][r] = o[c];
+    __syncthreads();
+    if (r >= rows) return;
+    // the warps' parts in order; warp w: dims d0 + w
+    float all = tops[0][r], total = 0.f;
+#pragma unroll
+    for (int w = 1; w < 8; ++w) all = fmaxf(all, tops[w][r]);
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+        if (w >= u.sharers) break;      // (its part is nothing, whatever its reference)
+        const float f = ex2(tops[w][r] - all);
+        const float4 z = os[w][warp][r];
+        total += f * sums[w][r];
+        y.x += f * z.x, y.y += f * z.y, y.z += f * z.z, y.w += f * z.w;
     }
-    if (r >= u.tokens * a.G) return;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const float inv = total == 0.f ? 0.f : 1.f / total;
     const int tok = r / a.G;
     const int64_t at = (int64_t)(u.row + tok) * a.Hq + g * a.G + r - tok * a.G;
-#pragma unroll
-    for (int c = 0; c < D / 32; ++c)
-        *reinterpret_cast<uint2*>(a.out + at * D + (warp + 8 * c) * 4) =
-            make_uint2(pack_bf16(o[c].x * inv, o[c].y * inv), pack_bf16(o[c].z * inv, o[c].w * inv));
-    if (a.lse && warp == 0) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    *reinterpret_cast<uint2*>(a.out + at * D + (d0 + warp) * 4) = make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
+    if (a.lse && d0 == 0 && warp == 0) a.lse[at] = total == 0.f ? -INFINITY : (all + log2f(total)) * kLn2;
 }
 
 template <int D, bool MAP>
@@ -608,7 +626,7 @@ cudaError_t launch(kvsel_ctx* ctx, const CUtensorMap& mq, const CUtensorMap& mk,
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || a.shares == 1) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(blocks, kHeads);
+    cfg.gridDim = dim3(blocks, kHeads * (D / 32));
     cfg.blockDim = dim3(256);
     cfg.stream = s;
     cudaLaunchAttribute attr;
