@@ -100,6 +100,15 @@ SHAPES = [
     ([2, 1, 1], [767, 4000, 769], 160, 160, 64, 16),  # more kv heads than SMs
     ([900, 1, 500], [4900, 6000, 500], 32, 8, 128, 16),
     ([600], [600], 40, 8, 128, 16),
+    # sessions of few tokens beside others, an odd number of kv heads, rows that just fill what the kernel for few takes
+    ([1] * 20 + [100, 3], [40 + 133 * i for i in range(20)] + [777, 3000], 8, 2, 128, 16),
+    ([1, 1, 1, 30], [2000, 300, 129, 500], 12, 3, 64, 16),
+    ([2, 8, 9], [3000, 40, 900], 4, 1, 128, 16),
+    ([8, 8, 7], [8, 300, 4000], 8, 2, 128, 16),
+    ([1, 1], [900, 70], 64, 2, 128, 16),
+    ([1, 2], [300, 200], 40, 1, 64, 16),
+    ([1, 1, 0, 1], [3000, 20000, 5, 1], 6, 6, 64, 16),
+    ([4] * 9, [500 * i + 4 for i in range(9)], 15, 5, 128, 32),
 ]
 
 
