@@ -610,8 +610,14 @@ int kvsel_prompt_attention(kvsel_ctx* ctx, const void* q, const void* k, const v
  *   q        bf16, token i at element i*q_stride, its Hq rows back to back
  *   k_pool, v_pool  bf16, P pages of `page` slots, k_stride and v_stride elements apart
  *   out      bf16 [T][Hq][D]; lse fp32 [T][Hq] or NULL
+ * The products take bf16 (softmax weights rounded to it), sums are fp32.  Results
+ * do not depend on anything but the arguments.
+ * Blocks exchange partial results through memory of a fixed size that the context
+ * holds from its creation on, so a captured call needs no earlier one; calls on one
+ * context must not overlap, replays of graphs with them included.
  * Requires D in {64,128}, Hq % Hkv == 0, Hq/Hkv <= 128, scale > 0, T <= 2^24,
- * S and Hq <= 65535, P*page < 2^31; q, out, pools and strides 16-byte aligned.
+ * S and Hq <= 65535, P*page < 2^31, k_stride and v_stride < 2^30; q, out, pools and
+ * strides 16-byte aligned.
  */
 int kvsel_pool_attention(kvsel_ctx* ctx, const void* q, int64_t q_stride, const int32_t* cu_new, int S, int T, int Hq,
                          int Hkv, int D, const void* k_pool, const void* v_pool, int64_t k_stride, int64_t v_stride,
@@ -624,12 +630,13 @@ int kvsel_pool_attention(kvsel_ctx* ctx, const void* q, int64_t q_stride, const 
  *   score_out[s,j] = score_in[s,j] + sum_{i,h} exp( scale * q[i,h] . K[j,g(h)] - lse[i,h] )
  * over the rows whose token sees j; tokens that no row sees keep score_in.
  * lse is what kvsel_pool_attention gave for the same arguments; a row whose
- * lse is -inf adds nothing.  Called after every step (and for every layer) on one
+ * lse is -inf (it sees nothing, or logits of -inf alone) adds nothing.  Called after every step (and for every layer) on one
  * score, it accumulates the attention weight that kvsel_evict_slots goes by.
  *   score_in, score_out  fp32 [S][score_ld], score_ld at least the positions that
  *   a row of the map or table reaches; those are written whole.  score_in NULL: zeros;
  *   it may be score_out.
- * Sums are fp32, in an order that the sizes alone decide.  Rules as kvsel_pool_attention.
+ * The products take bf16, sums are fp32, in an order that the arguments alone decide.
+ * Rules, limits and memory as kvsel_pool_attention.
  */
 int kvsel_attention_mass(kvsel_ctx* ctx, const void* q, int64_t q_stride, const float* lse, const int32_t* cu_new, int S,
                          int T, int Hq, int Hkv, int D, const void* k_pool, int64_t k_stride, int P, int page,
