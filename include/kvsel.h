@@ -610,8 +610,8 @@ int kvsel_prompt_attention(kvsel_ctx* ctx, const void* q, const void* k, const v
  *   q        bf16, token i at element i*q_stride, its Hq rows back to back
  *   k_pool, v_pool  bf16, P pages of `page` slots, k_stride and v_stride elements apart
  *   out      bf16 [T][Hq][D]; lse fp32 [T][Hq] or NULL
- * The products take bf16 (softmax weights rounded to it), sums are fp32.  Results
- * do not depend on anything but the arguments.
+ * The products take bf16 (softmax weights rounded to it), sums are fp32.  On one
+ * device equal arguments give equal results.
  * Blocks exchange partial results through memory of a fixed size that the context
  * holds from its creation on, so a captured call needs no earlier one; calls on one
  * context must not overlap, replays of graphs with them included.

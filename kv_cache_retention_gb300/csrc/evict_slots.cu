@@ -8,6 +8,8 @@
 // shared memory after one pass over scores and slots.  A session is worked on by a thread-block cluster that shares its
 // positions; histograms and counts are read from the other blocks' shared memory.  Warps own contiguous positions, so
 // the places of the evicted in the list follow from each warp's count of smaller and of equal keys.
+// Measured: a token each of 36 sessions of up to 8192 positions 14 us, a tenth kept of 92160 25 us (latency: the passes of
+// a cluster), a fifth of 64 sessions of up to 92160 evicted 50 us (28 M instructions, 58% of issue slots, DRAM 10%).
 #include <cooperative_groups.h>
 
 #include <limits.h>

