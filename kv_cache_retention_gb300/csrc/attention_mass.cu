@@ -336,6 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         typename C::Piece w;
         for (uint32_t u = 0; ok && next_piece(u, w, true); ++u) {
             const int nt = row_tiles(w);
+            const bool narrow = w.count <= a.small_tokens;
             Item it;
             do {
                 if (!next_item(t, l, it, stop, a.err, ok)) break;
@@ -357,7 +358,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             // columns that count: of tokens that see the key, and of the session's tokens
                             const int lo = min(max(behind - i * a.tile_tokens, 0), a.tile_tokens) * a.G;
                             const int hi = min(a.tile_tokens, w.count - i * a.tile_tokens) * a.G;
-                            const bool part = __any_sync(0xffffffffu, lo > 0) || hi < a.tile_tokens * a.G;
+                            // (of a narrow product, the columns behind its own hold what other kernels left there)
+                            const bool part = __any_sync(0xffffffffu, lo > 0) || hi < a.tile_tokens * a.G || narrow;
                             const float* const nl = t.lse[c % C::kL];
                             uint32_t s0[32], s1[32];
                             auto taken = [&]() {    // the buffer's columns are all in registers
