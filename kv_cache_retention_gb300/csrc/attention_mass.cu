@@ -23,6 +23,8 @@
 //
 // Every wait is bounded (1 s); on a timeout the block flags KVSEL_ERR_TIMEOUT in the device error word, drains its own copies
 // and MMAs, frees TMEM and returns.
+#include <type_traits>
+
 #include "pool_lists.cuh"
 
 namespace {
@@ -126,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    if (a.tile_tokens * a.G < kTile) {  // rows that no tile fills: zeros, whose weights come to nothing
+    if (a.tile_tokens * a.G < kTile) {  // rows that no tile fills: zeros (their columns are not looked at)
         for (int i = threadIdx.x; i < C::kQ * C::kBytes / 16; i += kThreads) reinterpret_cast<uint4*>(sq)[i] = make_uint4(0, 0, 0, 0);
         fence_async();
     }
@@ -332,11 +334,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int x = (warp - 8) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t ts = kTmem + ((uint32_t)(quarter * 32) << 16) + x * 256;
         const float2 sc2 = make_float2(a.scale2, a.scale2);
+        const int full = a.tile_tokens * a.G;       // rows of a full tile: more than 64, whatever G is
         uint32_t c = 0, cs = 0;                     // row tiles, and this list's buffers used so far
         typename C::Piece w;
         for (uint32_t u = 0; ok && next_piece(u, w, true); ++u) {
             const int nt = row_tiles(w);
-            const bool narrow = w.count <= a.small_tokens;
             Item it;
             do {
                 if (!next_item(t, l, it, stop, a.err, ok)) break;
@@ -358,8 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             // columns that count: of tokens that see the key, and of the session's tokens
                             const int lo = min(max(behind - i * a.tile_tokens, 0), a.tile_tokens) * a.G;
                             const int hi = min(a.tile_tokens, w.count - i * a.tile_tokens) * a.G;
-                            // (of a narrow product, the columns behind its own hold what other kernels left there)
-                            const bool part = __any_sync(0xffffffffu, lo > 0) || hi < a.tile_tokens * a.G || narrow;
+                            const bool part = __any_sync(0xffffffffu, lo > 0) || hi < full;
                             const float* const nl = t.lse[c % C::kL];
                             uint32_t s0[32], s1[32];
                             auto taken = [&]() {    // the buffer's columns are all in registers
@@ -369,9 +370,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                             };
                             tmem_ld32(ts + b * 128, s0);
                             tmem_wait_ld();
-                            if (!part) {
-                                // 32 columns at a time, the next ones on their way meanwhile
-                                auto add = [&](const uint32_t* s, int h) {
+                            // 32 columns at a time, the next ones on their way meanwhile.  Columns behind the tile's rows, from
+                            // place `first` on, are no logits (rows of zeros times an infinite key, or what a narrow product
+                            // has not written: NaN, which their bias of -inf would not hide), and are set to zero.  Groups of up
+                            // to 12 heads leave 8 columns at most, and those of a power of two none (2048 tokens over 34816: setting
+                            // 8 costs 1% with groups of 5 and 7, where all 64 cost 8 and 10%, and 9% with groups of 13).
+                            auto whole = [&](auto first) {
+                                auto add = [&](uint32_t* s, int h) {
+#pragma unroll
+                                    for (int k = 0; k < 32; ++k)
+                                        if (h + k >= decltype(first)::value) s[k] = h + k < full ? s[k] : 0u;
 #pragma unroll
                                     for (int k = 0; k < 8; ++k) {
                                         const float4 m = *reinterpret_cast<const float4*>(nl + h + 4 * k);
@@ -394,6 +402,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 tmem_wait_ld();
                                 taken();
                                 add(s1, 96);
+                            };
+                            if (!part && full == kTile) {
+                                whole(std::integral_constant<int, kTile>());
+                            } else if (!part && full >= kTile - 8) {
+                                whole(std::integral_constant<int, kTile - 8>());
+                            } else if (!part) {
+                                whole(std::integral_constant<int, kTile / 2>());
                             } else {
                                 const unsigned wide = (unsigned)max(hi - lo, 0);
 #pragma unroll 1

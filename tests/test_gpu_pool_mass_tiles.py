@@ -35,3 +35,28 @@ def test_one_token_of_a_large_group(ctx, G, D, n):
         ctx.attention_mass(w.q, lse, w.k, w.cu, w.lens, score, scale=w.scale, **w.args)
         ctx.check_device()
         ref.check_mass(score, ref.mass(w.q, lse, w.k, w.cu_host, w.lens_host, w.slots, w.live, w.scale, torch.zeros_like(score)))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G", [1, 3, 4, 5, 7, 10, 22, 40, 43, 65, 100])
+@pytest.mark.parametrize("new", [1, 150])
+def test_minus_infinite_logits(ctx, G, D, new):
+    """Keys with an infinite element whose logits are -inf for every row have no weight, whatever the group's size leaves of
+    a tile: their scores stay, and the others' are what they are without them."""
+    n = 900
+    w = World([new], [n], 2 * G, 2, D, 16, "table", seed=G)
+    w.q[..., 0] = 1
+    hidden = w.slots[0, 200:450]
+    w.k.flatten(0, 1)[hidden] = 0
+    w.k.flatten(0, 1)[hidden, :, 0] = -float("inf")
+    live = torch.ones_like(w.live)
+    live[0, 200:450] = False
+    clean = w.k.clone()
+    clean.flatten(0, 1)[hidden] = 0
+    lse = ref.attend(w.q, clean, w.v, w.cu_host, w.lens_host, w.slots, live, w.scale)[1].to(F32)
+    before = torch.rand((1, w.slots.shape[1]), device="cuda")
+    score = torch.empty_like(before)
+    ctx.attention_mass(w.q, lse, w.k, w.cu, w.lens, score, score_in=before, scale=w.scale, **w.args)
+    ctx.check_device()
+    assert torch.equal(score[0, 200:450], before[0, 200:450])
+    ref.check_mass(score, ref.mass(w.q, lse, clean, w.cu_host, w.lens_host, w.slots, live, w.scale, before))
