@@ -452,7 +452,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 __global__ void __launch_bounds__(256) mass_copy_kernel(const float* before, float* score, int64_t ld, int n) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int64_t row = (int64_t)blockIdx.y * ld;
-    for (int j = blockIdx.x * 256 + threadIdx.x; j < n; j += gridDim.x * 256) score[row + j] = before ? before[row + j] : 0.f;
+    // (64 bits: the last step may pass 2^31)
+    for (int64_t j = blockIdx.x * 256 + threadIdx.x; j < n; j += gridDim.x * 256) score[row + j] = before ? before[row + j] : 0.f;
 }
 
 // score_out = score_in + the parts of the blocks that shared the kv heads, in their order, where a token is live.
@@ -463,6 +464,7 @@ __global__ void __launch_bounds__(256) mass_add_kernel(const MassArgs a, const f
     unsigned err = 0;
     const Session x = session_at(a.cu, a.lens, a.T, a.map.reach, s);
     const int32_t* const row = a.map.map + (int64_t)s * a.map.ld;
+    // (the reach is far below 2^31 here: the parts fit the context's memory for them)
     for (int j = blockIdx.x * 256 + threadIdx.x; j < a.map.reach; j += gridDim.x * 256) {
         float sum = 0.f;
         if (x.count > 0 && j < x.len && live_slot<MAP>(a.map, raw_entry(a.map, row, j), j, err) >= 0)
