@@ -105,7 +105,7 @@ struct ListMeta {
     int causal;     // not all of them are seen by every row
     int last;       // of its piece
     int first;      // position of its first token
-    unsigned runs;  // of each four tokens, whether they go on a run of slots that starts with their kRun; a bit each
+    unsigned runs;  // of each four tokens, whether all are there and go on a run of slots that starts with their kRun; a bit each
 };
 
 // A ring of N lists.  token: slot and position, in ascending positions; behind the n-th the slot of the first.
@@ -157,7 +157,8 @@ __device__ __forceinline__ bool make_lists(Lists<N>& t, const TokenMap& m, const
         const int2* const list = &t.token[l % N * kTile];
         const int4 s01 = *reinterpret_cast<const int4*>(list + 4 * lane), s23 = *reinterpret_cast<const int4*>(list + 4 * lane + 2);
         const int first = list[(lane & ~(kRun / 4 - 1)) * 4].x, off = 4 * (lane % (kRun / 4));
-        const bool run = s01.x == first + off && s01.z == s01.x + 1 && s23.x == s01.x + 2 && s23.z == s01.x + 3;
+        // (places behind the n-th token are in no run: their rows are to be zeros)
+        const bool run = 4 * lane + 3 < n && s01.x == first + off && s01.z == s01.x + 1 && s23.x == s01.x + 2 && s23.z == s01.x + 3;
         const unsigned runs = __ballot_sync(0xffffffffu, run);
         if (lane == 0) {
             t.meta[l % N] = ListMeta{n, n > 0 && list[n - 1].y > pos0, last, list[0].y, runs};
