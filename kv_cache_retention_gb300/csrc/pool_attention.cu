@@ -644,7 +644,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&t.o_free[x][u & 1]);
-            const int odd = *(volatile int*)&t.odd[u & 1];
             const int64_t row_at = (int64_t)(w.row + tok0 + r_tok) * a.Hq + r_head;
             float* const part = w.part < 0 ? nullptr : a.parts + ((size_t)blockIdx.x * 2 + w.part) * kPart + x * kPartTile;
             if (active && part) {
@@ -682,28 +681,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (a.lse && r < rows) a.lse[row_at] = l_sum == 0.f ? -INFINITY : (ref + log2f(l_sum)) * kLn2;
             }
-            if (odd != INT_MAX && r < rows) {
-                // what the row sees of the values that were set to zero: a sum of infinities and NaN
-                unsigned err = 0;
-                const int32_t* const map = a.map.map + (int64_t)w.session * a.map.ld;
-                const int upto = min(row_pos, w.stop - 1);
-#pragma unroll 1
-                for (int d = 0; d < D; ++d) {
-                    float add = 0.f;
-#pragma unroll 1
-                    for (int j = odd; j <= upto; ++j) {
-                        const int slot = live_slot<MAP>(a.map, raw_entry(a.map, map, j), j, err);
-                        if (slot < 0) continue;
-                        const float e = __bfloat162float(a.v[(uint64_t)(uint32_t)slot * (a.v_bytes / 2) + (int64_t)g * D + d]);
-                        if (!(fabsf(e) < INFINITY)) add += e;
-                    }
-                    if (add == 0.f) continue;
+            const int odd = __shfl_sync(0xffffffffu, *(volatile int*)&t.odd[u & 1], 0);
+            if (odd != INT_MAX)
+                add_odd<D, MAP>(a, w.session, g, odd, r < rows ? min(row_pos, w.stop - 1) : -1, lane, [&](int d, float add) {
                     if (part)
                         part[((d >> 2) * kTile + r) * 4 + (d & 3)] += add;
                     else
                         a.out[row_at * D + d] = __float2bfloat16_rn(__bfloat162float(a.out[row_at * D + d]) + add);
-                }
-            }
+                });
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&t.piece_empty[u & 1]);

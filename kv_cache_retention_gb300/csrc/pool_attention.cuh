@@ -38,4 +38,41 @@ struct PoolArgs {
     int stuck;                          // tile 0's issuer waits for what never comes (test entry)
 };
 
+// What a row sees of V's values that were set to zero in lists that not every row sees whole: put(d, sum) for the dims whose
+// sum, of infinities and NaN, is one.  from: the first key of such a list; upto: the last key that the lane's row sees, -1
+// for none.  The whole warp calls, a row a lane: its lanes read the map 32 positions at a time and look at each live token's row
+// together, eight dims in a walk, since such a list may span a whole session of which little is live.
+template <int D, bool MAP, class Put>
+__device__ __forceinline__ void add_odd(const PoolArgs& a, int session, int head, int from, int upto, int lane, Put put) {
+    unsigned err = 0;                   // (what is wrong with the map has been said)
+    const int32_t* const map = a.map.map + (int64_t)session * a.map.ld;
+    const __nv_bfloat16* const v = a.v + (int64_t)head * D;
+    const int end = __reduce_max_sync(0xffffffffu, upto);
+#pragma unroll 1
+    for (int d = 0; d < D; d += 8) {
+        float add[8] = {};
+#pragma unroll 1
+        for (int p = from; p <= end; p += 32) {
+            const int j = p + lane;
+            const int slot = j <= end ? live_slot<MAP>(a.map, raw_entry(a.map, map, j), j, err) : -1;
+#pragma unroll 1
+            for (unsigned live = __ballot_sync(0xffffffffu, slot >= 0); live; live &= live - 1) {
+                const int k = __ffs(live) - 1;
+                const uint32_t s = __shfl_sync(0xffffffffu, slot, k);
+                const uint4 y = *reinterpret_cast<const uint4*>(v + (uint64_t)s * (a.v_bytes / 2) + d);
+                const uint32_t e[4] = {y.x, y.y, y.z, y.w};
+                if (p + k > upto) continue;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float f = __uint_as_float(i & 1 ? e[i / 2] & 0xFFFF0000u : e[i / 2] << 16);
+                    if (!(fabsf(f) < INFINITY)) add[i] += f;
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (add[i] != 0.f) put(d + i, add[i]);  // (a NaN is not 0)
+    }
+}
+
 }  // namespace

@@ -523,28 +523,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (a.lse && lane < rows) a.lse[row_at] = l_sum == 0.f ? -INFINITY : (ref + log2f(l_sum)) * kLn2;
                 }
-                if (odd != INT_MAX && lane < rows) {
-                    // what the row sees of the values that were set to zero: a sum of infinities and NaN
-                    unsigned err = 0;
-                    const int32_t* const map = a.map.map + (int64_t)w.session * a.map.ld;
-                    const int upto = min(row_pos, w.stop - 1);
-#pragma unroll 1
-                    for (int d = 0; d < D; ++d) {
-                        float add = 0.f;
-#pragma unroll 1
-                        for (int j = odd; j <= upto; ++j) {
-                            const int slot = live_slot<MAP>(a.map, raw_entry(a.map, map, j), j, err);
-                            if (slot < 0) continue;
-                            const float e = __bfloat162float(a.v[(uint64_t)(uint32_t)slot * (a.v_bytes / 2) + (int64_t)(head0 + x) * D + d]);
-                            if (!(fabsf(e) < INFINITY)) add += e;
-                        }
-                        if (add == 0.f) continue;
+                if (odd != INT_MAX)
+                    add_odd<D, MAP>(a, w.session, head0 + x, odd, lane < rows ? min(row_pos, w.stop - 1) : -1, lane, [&](int d, float add) {
                         if (part)
                             part[((d >> 2) * kRows + lane) * 4 + (d & 3)] += add;
                         else
                             a.out[row_at * D + d] = __float2bfloat16_rn(__bfloat162float(a.out[row_at * D + d]) + add);
-                    }
-                }
+                    });
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&t.piece_empty[u & 1]);
