@@ -240,7 +240,8 @@ extern "C" int kvsel_evict_slots(kvsel_ctx* ctx, const float* score, int64_t sco
         if (e != cudaSuccess) return kvsel_cuda_fail(ctx, e, "evict_slots set-up");
         ctx->ready |= KVSEL_READY_EVICT;
     }
-    // A cluster as large as keeps all sessions' blocks on the GPU at once (three an SM) and leaves a thread four positions.
+    // A cluster as large as keeps all sessions' blocks on the GPU at once, three an SM, and leaves a thread four positions.  (Three
+    // fit while a block holds 14000 keys or fewer; of longer rows one or two do, and many such sessions take several rounds.)
     int c = 1;
     while (c < 8 && 2 * (int64_t)S * c <= 3 * ctx->num_sms && ld > c * 4 * kThreads) c *= 2;
     const int64_t per = (((int64_t)ld + c * kWarps - 1) / (c * kWarps) + 31) & ~31;
