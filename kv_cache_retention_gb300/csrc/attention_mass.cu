@@ -18,7 +18,7 @@
 // into equal contiguous shares, a block each, found from the lengths on the device.  Where there are few chunks, several
 // blocks take a share's kv heads in turn and a second kernel adds their parts up in order.
 //
-// Measured, 32/8 heads of 128: 2048 tokens over 34816 0.52 ms (1.10 PFLOP/s; tensor pipe 50%, issue slots 45%, DRAM 2%: no unit
+// Measured, 32/8 heads of 128: 2048 tokens over 34816 0.51 ms (1.11 PFLOP/s; tensor pipe 50%, issue slots 45%, DRAM 2%: no unit
 // is full); a decode step of 36 sessions pruned to a quarter, 500 MB, 112 us (4.5 TB/s).
 //
 // Every wait is bounded (1 s); on a timeout the block flags KVSEL_ERR_TIMEOUT in the device error word, drains its own copies
@@ -31,7 +31,7 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kLists = 8;
-constexpr int kLoad = 2;                // row tiles that a chunk's own loads and its start count as
+constexpr int kLoad = 2;                // row tiles that a chunk's own loads and its start count as (1 costs 2048 tokens 1%; 4 and 8 nothing)
 constexpr uint32_t kTmem = 0;           // all of TMEM is allocated, so its base is column 0
 constexpr int kTmemCols = 512;
 

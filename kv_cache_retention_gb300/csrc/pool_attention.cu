@@ -33,8 +33,8 @@
 // softmax warps set such values to zero in shared memory before the product, and if there were any, each row adds those it
 // does see to its output at the end (what the sum would be: infinite or NaN).
 //
-// Measured: 2048 tokens behind 32768, 32/8 heads of 128, 0.87 ms (1.31 PFLOP/s, 74% of a sustained matrix product's rate).
-// No unit is full: tensor pipe 66%, issue slots 50%, DRAM 32%.  Steps on the way there: rows by TMA gathers of four slots
+// Measured: 2048 tokens behind 32768, 32/8 heads of 128, 0.84 to 0.86 ms (1.32 to 1.36 PFLOP/s, three quarters of a sustained
+// matrix product's rate).  No unit is full: tensor pipe 66%, issue slots 50%, DRAM 32%.  Steps on the way there: rows by TMA gathers of four slots
 // took 2.73 ms, an issuer's waits within its turn 1.09 and ahead of it 0.98, MMAs in a branch of one elected thread 0.97 -> 0.86;
 // without turns it took 1.05 where turns took 0.98.
 //
@@ -52,8 +52,9 @@ constexpr int kThreads = 512;
 constexpr int kRegsLaunch = 128, kRegsCtl = 72, kRegsSoft = 184;
 static_assert(2 * kRegsCtl + 2 * kRegsSoft <= 4 * kRegsLaunch && kRegsLaunch * kThreads <= 65536, "register split");
 constexpr int kLists = 8;
-constexpr int kStart = 4;               // lists that the start of a unit counts as when shares are cut
-constexpr int kLeast = 4;               // lists that a share has at least, so cut
+// Lists that the start of a unit counts as when shares are cut, and that a share has at least, so cut.  Measured: a start of 2
+// costs a batch of 16 sessions of 1 to 1013 new tokens 2 to 5%, one of 8 changes nothing; no difference between shares of 1 to 8.
+constexpr int kStart = 4, kLeast = 4;
 
 template <int D>
 struct Cfg {
@@ -786,7 +787,11 @@ int attention_call(kvsel_ctx* ctx, const void* q, int64_t q_stride, const int32_
     const int G = Hq / Hkv, tile_tokens = kTile / G;
     const int most = decode::kRows / G;  // tokens that the rows of few hold
     // Sessions of few tokens go to the kernel for them where they may be most of the batch's; its launch is not worth it for
-    // chunks, whose own kernel takes them too.  Where all tokens together are few, that one is not needed.
+    // chunks, whose own kernel takes them too.  Where all tokens together are few, that one is not needed.  The host knows T and S
+    // alone, so the rule goes by rows a session.  With and without the kernel, 36 sessions of 8192 tokens, 32/8 heads: new tokens
+    // of 1 or 8 each 190 or 193 and 250 or 257 us; 8 and 16 by turns 260 and 260; 12, 16 or 24 each, where none are few, 291, 293
+    // or 286 and 274, 276 or 271; 35 of one beside one of 256, 512 or 2048, 244, 265 or 404 and 305, 338 or 466.  The border at 64
+    // rows lies behind 16 each and the one beside 512: two kernels for nothing cost 16 us there, and 62 are lost beside 2048.
     const bool few = most > 0 && (int64_t)T * G <= 2 * (int64_t)decode::kRows * S, all_few = T <= most;
     CUtensorMap mq, ms, mk, mv;
     if (!make_query_map(&mq, q, T, Hq, D, q_stride, G, tile_tokens) ||
